@@ -31,6 +31,15 @@ Q8_MAX_ROWS = 32
 Q8_MAX_GEMM_ROWS = 8192
 Q8_MAX_PARTS = 4
 Q8_MAX_TWO_WORD_ROWS = 16
+Q8_MAX_SEQS = 8192
+Q8_KV_BF16 = 0
+Q8_KV_Q8_0 = 1
+Q8_ROPE_HALF = 0
+Q8_ROPE_INTERLEAVED = 1
+Q8_ROPE_SCALE_NONE = 0
+Q8_ROPE_SCALE_LINEAR = 1
+Q8_ROPE_SCALE_TURNS = 2
+Q8_ROPE_SCALE_INDEX = 3
 
 STATUS = {0: "Q8_OK", 1: "Q8_ERR_SHAPE", 2: "Q8_ERR_ACT_FMT", 3: "Q8_ERR_NULL",
           4: "Q8_ERR_ALIGN", 5: "Q8_ERR_WORKSPACE", 6: "Q8_ERR_HIP", 7: "Q8_ERR_PLAN"}
@@ -66,6 +75,37 @@ class q8_glu_epilogue(ctypes.Structure):
 class q8_part(ctypes.Structure):
     _fields_ = [("W_q8", ctypes.c_void_p), ("W_q8_scale", ctypes.c_void_p),
                 ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("N", ctypes.c_int64)]
+
+
+class q8_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("fmt", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32)]
+
+
+class q8_kv_step_args(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in
+                ("lens", "new_rows", "table", "free_pages", "free_count", "lens_out",
+                 "free_count_out", "row_start", "positions", "slots", "status")] + \
+               [("n", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("free_cap", ctypes.c_int64), ("m", ctypes.c_int64), ("page", ctypes.c_int32)]
+
+
+class q8_rope(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("original", ctypes.c_int64), ("rot", ctypes.c_int32),
+                ("scaling", ctypes.c_int32)]
+
+
+class q8_heads(ctypes.Structure):
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("freqs", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("attn_factor", ctypes.c_float), ("rot", ctypes.c_int32),
+                ("layout", ctypes.c_int32)]
+
+
+class q8_attn(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
 
 _i64 = ctypes.c_int64
@@ -128,6 +168,17 @@ _SIGS = {
     "q8_gemv_noalloc": (_int, [_p, _p, _p, _p, _i64, _i64, _i64, _int, _p]),
     "q8_noalloc_scratch_bytes": (_sz, []),
     "q8_layout_version": (_int, []),
+    "q8_kv_bytes": (_sz, [_int, _i64, _i64, _i64, _i64]),
+    "q8_kv_step": (_int, [ctypes.POINTER(q8_kv_step_args), _p]),
+    "q8_rope_freqs": (_int, [ctypes.POINTER(q8_rope), _p, _p]),
+    "q8_qkv_heads": (_int, [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, ctypes.POINTER(q8_heads),
+                            _p, _p, _p, ctypes.POINTER(q8_kv_cache), _p]),
+    "q8_kv_gather": (_int, [ctypes.POINTER(q8_kv_cache), _p, _i64, _p, _p, _p]),
+    "q8_attn_workspace_bytes": (_sz, [_i64, _i64, _i64, ctypes.POINTER(q8_kv_cache)]),
+    "q8_attn_decode": (_int, [_p, _i64, ctypes.POINTER(q8_kv_cache), _p, _i64, _p, _i64,
+                              ctypes.POINTER(q8_attn), _p, _p, _p, _p, _sz]),
+    "q8_attn_rows": (_int, [_p, _i64, _i64, ctypes.POINTER(q8_kv_cache), _p, _i64, _p, _p, _i64,
+                            ctypes.POINTER(q8_attn), _p, _p, _p, _p, _sz]),
 }
 
 _lib = None
@@ -390,6 +441,83 @@ def q8_gemm(x, W_q8, W_q8_scale, y, m, K, N, act_fmt, stream=None) -> None:
 def q8_gemm_block_dots(x_q8, W_q8, dots, m, K, N, stream=None) -> None:
     _check(lib().q8_gemm_block_dots(_addr(x_q8), _addr(W_q8), _addr(dots), m, K, N,
                                     _stream(stream)))
+
+
+# ---- between the projections ------------------------------------------------------
+
+def q8_kv_bytes(fmt: int, kv_heads: int, head_dim: int, page: int, n_pages: int) -> int:
+    return int(lib().q8_kv_bytes(fmt, kv_heads, head_dim, page, n_pages))
+
+
+def make_kv_cache(k, v, n_pages, fmt, kv_heads, head_dim, page) -> q8_kv_cache:
+    """A ``q8_kv_cache`` over two device tensors (or raw addresses)."""
+    return q8_kv_cache(_addr(k), _addr(v), n_pages, fmt, kv_heads, head_dim, page)
+
+
+def make_kv_step(lens, new_rows, n, table, max_pages, page, free_pages, free_cap, free_count,
+                 lens_out, free_count_out, row_start, positions, slots, m,
+                 status) -> q8_kv_step_args:
+    """A ``q8_kv_step_args`` over device tensors (or raw addresses)."""
+    return q8_kv_step_args(*(_addr(t) for t in (lens, new_rows, table, free_pages, free_count,
+                                                lens_out, free_count_out, row_start, positions,
+                                                slots, status)),
+                           n, max_pages, free_cap, m, page)
+
+
+def make_rope(base, rot, scaling=Q8_ROPE_SCALE_NONE, factor=1.0, low=1.0, high=4.0,
+              original=8192) -> q8_rope:
+    return q8_rope(base, factor, low, high, original, rot, scaling)
+
+
+def make_heads(q_norm, k_norm, eps, freqs, rot, layout, attn_factor=1.0) -> q8_heads:
+    """A ``q8_heads`` over device tensors (or raw addresses, or None)."""
+    return q8_heads(_addr(q_norm), _addr(k_norm), _addr(freqs), eps, attn_factor, rot, layout)
+
+
+def make_attn(scale, window=0, sinks=0) -> q8_attn:
+    return q8_attn(scale, window, sinks)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def q8_kv_step(step: q8_kv_step_args, stream=None) -> None:
+    _check(lib().q8_kv_step(_ref(step), _stream(stream)))
+
+
+def q8_rope_freqs(rope: q8_rope, freqs, stream=None) -> None:
+    _check(lib().q8_rope_freqs(_ref(rope), _addr(freqs), _stream(stream)))
+
+
+def q8_qkv_heads(q, ldq, k, ldk, v, ldv, m, q_heads, heads: q8_heads, positions, slots, q_out,
+                 cache: q8_kv_cache, stream=None) -> None:
+    _check(lib().q8_qkv_heads(_addr(q), ldq, _addr(k), ldk, _addr(v), ldv, m, q_heads,
+                              _ref(heads), _addr(positions), _addr(slots), _addr(q_out),
+                              _ref(cache), _stream(stream)))
+
+
+def q8_kv_gather(cache: q8_kv_cache, slots, rows, k_out, v_out, stream=None) -> None:
+    _check(lib().q8_kv_gather(_ref(cache), _addr(slots), rows, _addr(k_out), _addr(v_out),
+                              _stream(stream)))
+
+
+def q8_attn_workspace_bytes(m, n, q_heads, cache: q8_kv_cache) -> int:
+    return int(lib().q8_attn_workspace_bytes(m, n, q_heads, _ref(cache)))
+
+
+def q8_attn_decode(q, q_heads, cache: q8_kv_cache, table, max_pages, lens, n, attn: q8_attn, o,
+                   o_q8=None, stream=None, workspace=None, ws_bytes=0) -> None:
+    _check(lib().q8_attn_decode(_addr(q), q_heads, _ref(cache), _addr(table), max_pages,
+                                _addr(lens), n, _ref(attn), _addr(o), _addr(o_q8),
+                                _stream(stream), _addr(workspace), ws_bytes))
+
+
+def q8_attn_rows(q, m, q_heads, cache: q8_kv_cache, table, max_pages, lens, row_start, n,
+                 attn: q8_attn, o, o_q8=None, stream=None, workspace=None, ws_bytes=0) -> None:
+    _check(lib().q8_attn_rows(_addr(q), m, q_heads, _ref(cache), _addr(table), max_pages,
+                              _addr(lens), _addr(row_start), n, _ref(attn), _addr(o),
+                              _addr(o_q8), _stream(stream), _addr(workspace), ws_bytes))
 
 
 def q8_status_string(status: int) -> str:

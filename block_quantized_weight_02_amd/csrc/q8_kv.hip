@@ -1,0 +1,427 @@
+// q8_kv.hip -- the cache's bookkeeping and what writes it: a step's page
+// tables, positions and slots (q8_kv_step), the rotary frequencies
+// (q8_rope_freqs), head norms with the position rotation and the cache rows
+// (q8_qkv_heads), and rows read back (q8_kv_gather).  The formulas, layouts
+// and refusals are in include/q8gemv.h.
+#include <hip/hip_runtime.h>
+
+#include "q8_device.h"
+#include "q8_kv.h"
+
+namespace q8 {
+namespace {
+
+using namespace dev;
+
+// ---- a step's tables -----------------------------------------------------------
+
+// Inclusive sum over the workgroup's threads in thread order; *total gets the
+// sum of all.  sums: one int per wave.
+__device__ __forceinline__ int scan_workgroup(int v, int *sums, int *total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();                      // sums may still be read from the last scan
+  if (lane == 63) sums[wave] = v;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < waves; ++w) {
+    const int s = sums[w];
+    before += w < wave ? s : 0;
+    all += s;
+  }
+  *total = all;
+  return v + before;
+}
+
+// One workgroup: thread t takes sequences t*E .. t*E+E-1 (E = 1 up to 1024
+// sequences, 8 at most), so that two running sums in thread order -- rows and
+// returned pages, then needed pages -- give every sequence its place.  Rows
+// then look their sequence up in the row starts, held in LDS.  All lengths
+// are read before any is written (lens_out may be lens); the table's and the
+// list's new entries are read back after a barrier by the workgroup that
+// wrote them.  Bound by latency: launch, three dependent loads, six barriers.
+constexpr unsigned kRefused = 1u << 31;
+
+template <int E>
+__global__ void __launch_bounds__(1024)
+kv_step_kernel(q8_kv_step_args a, int page_log2) {
+  extern __shared__ unsigned starts[];   // n + 1 row starts, kRefused in the top bit
+  __shared__ int sums[16];
+  const int n = (int)a.n, m = (int)a.m, most = (int)a.max_pages, cap = (int)a.free_cap;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int P1 = (1 << page_log2) - 1;
+  const long long longest = (long long)most << page_log2;
+  int len[E], rows[E], held[E];
+  bool ended[E];
+  int sum_rows = 0, sum_back = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = tid * E + e;
+    const int l = i < n ? a.lens[i] : 0;
+    const int w = i < n ? a.new_rows[i] : 0;
+    len[e] = (int)min((long long)max(l, 0), longest);
+    ended[e] = w < 0;
+    rows[e] = min(max(w, 0), m + 1);      // more than m is refused whatever the number
+    held[e] = (len[e] >> page_log2) + ((len[e] & P1) != 0);
+    sum_rows += rows[e];
+    sum_back += ended[e] ? held[e] : 0;
+  }
+  const int count0 = min(max(a.free_count[0], 0), cap);
+  int total_rows, total_back, total_need;
+  int row = scan_workgroup(sum_rows, sums, &total_rows) - sum_rows;
+  int back = scan_workgroup(sum_back, sums, &total_back) - sum_back;
+  const int have = (int)min((long long)count0 + total_back, (long long)cap);
+
+  // needed pages, and who is refused whatever the list holds
+  int need[E], row0[E];
+  bool barred[E];
+  int sum_need = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    row0[e] = row;
+    row += rows[e];
+    const long long after = (long long)len[e] + rows[e];
+    const int pages = (int)((after + P1) >> page_log2);
+    barred[e] = !ended[e] && (pages > most || row > m || after > 0x7fffffff);
+    need[e] = (ended[e] || barred[e]) ? 0 : pages - held[e];
+    sum_need += need[e];
+  }
+  int upto = scan_workgroup(sum_need, sums, &total_need) - sum_need;
+  int taken = 0, refusals = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = tid * E + e;
+    const int first = upto;
+    upto += need[e];
+    const bool refused = barred[e] || (need[e] > 0 && upto > have);
+    if (refused) ++refusals, need[e] = 0;
+    taken += need[e];
+    if (i < n) {
+      starts[i] = (unsigned)min(row0[e], m) | (refused ? kRefused : 0u);
+      a.row_start[i] = min(row0[e], m);
+      a.lens_out[i] = ended[e] ? 0 : (refused ? len[e] : len[e] + rows[e]);
+    }
+    // Ended sequences' pages go to the list's end: a wave copies one sequence's
+    // pages at a time, its lanes side by side.
+    unsigned long long some = __ballot(i < n && ended[e] && held[e] > 0);
+    const int at = (int)min((long long)count0 + back, (long long)cap);
+    back += ended[e] ? held[e] : 0;
+    while (some) {
+      const int src = __ffsll(some) - 1;
+      some &= some - 1;
+      const int si = __shfl(i, src), sh = __shfl(held[e], src), sat = __shfl(at, src);
+      for (int j = lane; j < sh; j += 64)
+        if (sat + j < cap) a.free_pages[sat + j] = a.table[(long long)si * most + j];
+    }
+    row0[e] = first;                       // from here: the sequence's first grant
+  }
+  if (tid == 0) {
+    starts[n] = (unsigned)min(total_rows, m);
+    a.row_start[n] = min(total_rows, m);
+  }
+  int all_taken, all_refused;
+  (void)scan_workgroup(taken, sums, &all_taken);   // its barriers order the list's new entries
+  (void)scan_workgroup(refusals, sums, &all_refused);
+  if (tid == 0) {
+    a.free_count_out[0] = have - all_taken;
+    a.status[0] = all_refused;
+    a.status[1] = max(total_need - have, 0);
+  }
+  // grants, from the list's end
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = tid * E + e;
+    unsigned long long some = __ballot(i < n && need[e] > 0);
+    while (some) {
+      const int src = __ffsll(some) - 1;
+      some &= some - 1;
+      const int si = __shfl(i, src), sn = __shfl(need[e], src), sh = __shfl(held[e], src),
+                sf = __shfl(row0[e], src);
+      for (int j = lane; j < sn; j += 64)
+        a.table[(long long)si * most + sh + j] = a.free_pages[have - 1 - sf - j];
+    }
+  }
+  __syncthreads();
+  // the rows
+  for (int r = tid; r < m; r += blockDim.x) {
+    int pos = 0, slot = -1;
+    if (r < (int)starts[n]) {
+      int lo = 0, hi = n - 1;              // the last sequence that starts at or before r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int)(starts[mid] & ~kRefused) <= r) lo = mid; else hi = mid - 1;
+      }
+      const unsigned s = starts[lo];
+      if (!(s & kRefused)) {
+        const int cnt = (int)(starts[lo + 1] & ~kRefused) - (int)s;
+        pos = a.lens_out[lo] - cnt + (r - (int)s);
+        slot = (a.table[(long long)lo * most + (pos >> page_log2)] << page_log2) + (pos & P1);
+      }
+    }
+    a.positions[r] = pos;
+    a.slots[r] = slot;
+  }
+}
+
+// ---- rotary frequencies ----------------------------------------------------------
+
+__global__ void __launch_bounds__(128) rope_freqs_kernel(q8_rope r, double *__restrict__ freqs) {
+  const int p = threadIdx.x, half = r.rot / 2;
+  if (p >= half) return;
+  const double kTwoPi = 6.283185307179586476925287;
+  const double f = pow(r.base, -2.0 * p / r.rot);
+  double keep = 1.0;
+  if (r.scaling == Q8_ROPE_SCALE_LINEAR) {
+    keep = 0.0;
+  } else if (r.scaling == Q8_ROPE_SCALE_TURNS) {
+    const double t = (double)r.original * f / kTwoPi;
+    keep = fmin(fmax((t - r.low) / (r.high - r.low), 0.0), 1.0);
+  } else if (r.scaling == Q8_ROPE_SCALE_INDEX) {
+    const double d = r.rot / (2.0 * log(r.base));
+    const double a = fmax(floor(d * log((double)r.original / (kTwoPi * r.high))), 0.0);
+    double b = fmin(ceil(d * log((double)r.original / (kTwoPi * r.low))), (double)r.rot - 1.0);
+    b = fmax(b, a + 0.001);
+    keep = 1.0 - fmin(fmax((p - a) / (b - a), 0.0), 1.0);
+  }
+  freqs[p] = f * keep + (keep == 1.0 ? 0.0 : f / r.factor * (1.0 - keep));
+}
+
+// ---- head norms, rotation, cache rows ----------------------------------------------
+
+__device__ __forceinline__ uint16_t bf16_bits(float f) {   // nearest even; NaN stays NaN
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+__device__ __forceinline__ uint2 bf16x4_bits(const float *x) {
+  return make_uint2((uint32_t)bf16_bits(x[0]) | (uint32_t)bf16_bits(x[1]) << 16,
+                    (uint32_t)bf16_bits(x[2]) | (uint32_t)bf16_bits(x[3]) << 16);
+}
+
+// A wave handles one row: 64 / (D/4) heads side by side in a pass, a lane four
+// dims of one head (one 16-byte load), `passes` passes.  The four angles' cos
+// and sin are the same for all of a row's heads, so they are computed once a
+// wave: the angle in turns in fp64 (a position of 2^31 keeps 2^-22 turns),
+// reduced to half a turn, then fp32.  The norm's sum and the quantizer's amax
+// are lane reductions within the head; the half layout's partner dims sit
+// rot/8 lanes away.
+template <int D, int FMT>
+__global__ void __launch_bounds__(512)
+qkv_heads_kernel(HeadsArgs a, int passes) {
+  constexpr int LPH = D / 4, HPW = 64 / LPH;
+  const int lane = threadIdx.x & 63;
+  const int r = blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+  if (r >= a.m) return;
+  const int slot = a.slots[r];
+  const KvCache c = a.cache;
+  if (slot < 0 || (slot >> c.page_log2) >= c.n_pages) return;
+  const int hl = lane / LPH, il = lane % LPH, d0 = il * 4;
+  const int P = 1 << c.page_log2, tok = slot & (P - 1);
+  const size_t page_at = (size_t)(slot >> c.page_log2) * c.page_bytes();
+  const int Ht = a.q_heads + 2 * c.heads;
+  const int half = a.rot >> 1;
+
+  float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  int partner = lane;
+  if (a.rot > 0 && d0 < a.rot) {
+    const double pos = (double)max(a.positions[r], 0);
+    const bool halves = a.layout == Q8_ROPE_HALF;
+    const int p0 = halves ? (d0 < half ? d0 : d0 - half) : d0 >> 1;
+    float ct[4], st[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e < 2 || halves) {
+        const double turns = pos * (a.freqs[p0 + e] * 0.15915494309189533577);
+        const float f = (float)(turns - rint(turns));
+        sincospif(2.0f * f, &st[e], &ct[e]);
+        ct[e] *= a.attn_factor;
+        st[e] *= a.attn_factor;
+      }
+    }
+    // y = x cos + (partner) sin with the sign of the partner's term in sin
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = halves ? e : e >> 1;
+      cs[e] = ct[t];
+      sn[e] = (halves ? d0 < half : (e & 1) == 0) ? -st[t] : st[t];
+    }
+    if (halves) partner = lane + (d0 < half ? half / 4 : -(half / 4));
+  }
+  float wq[4] = {1.0f, 1.0f, 1.0f, 1.0f}, wk[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (a.q_norm) wq[e] = a.q_norm[d0 + e];
+    if (a.k_norm) wk[e] = a.k_norm[d0 + e];
+  }
+
+  const int first = blockIdx.y * passes;
+  for (int ps = first; ps < first + passes; ++ps) {
+    const int h = ps * HPW + hl;
+    if (ps * HPW >= Ht) break;
+    const bool live = h < Ht;
+    const int kind = h < a.q_heads ? 0 : (h < a.q_heads + c.heads ? 1 : 2);
+    const int hh = kind == 0 ? h : h - a.q_heads - (kind == 2 ? c.heads : 0);
+    const float *src = kind == 0 ? a.q + r * a.ldq : (kind == 1 ? a.k + r * a.ldk : a.v + r * a.ldv);
+    float4 x4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (live) x4 = *reinterpret_cast<const float4 *>(src + (size_t)hh * D + d0);
+    float x[4] = {x4.x, x4.y, x4.z, x4.w};
+    float ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o);
+    const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+    const bool normed = (kind == 0 && a.q_norm) || (kind == 1 && a.k_norm);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (normed) x[e] = x[e] * inv * (kind == 0 ? wq[e] : wk[e]);
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float other = __shfl(x[e], partner);
+      const float mate = a.layout == Q8_ROPE_HALF ? other : x[e ^ 1];
+      y[e] = x[e] * cs[e] + mate * sn[e];
+    }
+    if (kind == 2 || d0 >= a.rot) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = x[e];
+    }
+    float dq = 0.0f;
+    if constexpr (FMT == Q8_KV_Q8_0) {
+      float am = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor(am, o));
+      dq = q8_scale_of(am);
+    }
+    if (!live) continue;
+    if (kind == 0) {
+      *reinterpret_cast<uint2 *>(a.q_out + ((size_t)r * a.q_heads + h) * D + d0) = bf16x4_bits(y);
+      continue;
+    }
+    char *rec = (kind == 1 ? c.k : c.v) + page_at + (size_t)hh * c.record();
+    if constexpr (FMT == Q8_KV_BF16) {
+      uint16_t *vals = reinterpret_cast<uint16_t *>(rec);
+      if (kind == 1) {
+        *reinterpret_cast<uint2 *>(vals + ((size_t)(d0 >> 3) * P + tok) * 8 + (d0 & 7)) =
+            bf16x4_bits(y);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          vals[((size_t)(tok >> 3) * D + d0 + e) * 8 + (tok & 7)] = bf16_bits(y[e]);
+      }
+    } else {
+      int8_t *vals = reinterpret_cast<int8_t *>(rec);
+      int8_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = q8_code_of(y[e], dq);
+      if (kind == 1) {
+        const uint32_t w = (uint32_t)(uint8_t)q[0] | (uint32_t)(uint8_t)q[1] << 8 |
+                           (uint32_t)(uint8_t)q[2] << 16 | (uint32_t)(uint8_t)q[3] << 24;
+        *reinterpret_cast<uint32_t *>(vals + ((size_t)(d0 >> 3) * P + tok) * 8 + (d0 & 7)) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          vals[((size_t)(tok >> 3) * D + d0 + e) * 8 + (tok & 7)] = q[e];
+      }
+      if ((d0 & 31) == 0)
+        reinterpret_cast<float *>(vals + (size_t)D * P)[(size_t)(d0 >> 5) * P + tok] = dq;
+    }
+  }
+}
+
+// ---- rows read back -----------------------------------------------------------------
+
+// A thread reads eight dims of one (row, head): one 16-byte piece of the keys,
+// eight places of the values.
+template <int FMT>
+__global__ void __launch_bounds__(256)
+kv_gather_kernel(KvCache c, const int32_t *__restrict__ slots, int rows,
+                 uint16_t *__restrict__ k_out, uint16_t *__restrict__ v_out) {
+  const int D = c.dim, per_row = c.heads * (D / 8);
+  const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int r = (int)(idx / per_row);
+  if (r >= rows) return;
+  const int slot = slots[r];
+  const int P = 1 << c.page_log2;
+  if (slot < 0 || (slot >> c.page_log2) >= c.n_pages) return;
+  const int h = (int)(idx % per_row) / (D / 8), ch = (int)(idx % per_row) % (D / 8);
+  const int tok = slot & (P - 1);
+  const size_t at = (size_t)(slot >> c.page_log2) * c.page_bytes() + (size_t)h * c.record();
+  const size_t out = ((size_t)r * c.heads + h) * D + ch * 8;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    uint16_t *dst = which ? v_out : k_out;
+    if (!dst) continue;
+    const char *rec = (which ? c.v : c.k) + at;
+    uint16_t y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const size_t i = which ? ((size_t)(tok >> 3) * D + ch * 8 + e) * 8 + (tok & 7)
+                             : ((size_t)ch * P + tok) * 8 + e;
+      if constexpr (FMT == Q8_KV_BF16) {
+        y[e] = reinterpret_cast<const uint16_t *>(rec)[i];
+      } else {
+        const float d = reinterpret_cast<const float *>(rec + (size_t)D * P)[(ch >> 2) * P + tok];
+        y[e] = bf16_bits((float)reinterpret_cast<const int8_t *>(rec)[i] * d);
+      }
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = (uint32_t)y[2 * e] | (uint32_t)y[2 * e + 1] << 16;
+    *reinterpret_cast<uint4 *>(dst + out) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+int log2_of(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+}  // namespace
+
+hipError_t launch_kv_step(const q8_kv_step_args &a, hipStream_t stream) {
+  const int need = (int)(a.n > a.m ? a.n : a.m);
+  const int threads = need >= 1024 ? 1024 : (need + 63) / 64 * 64;
+  const size_t lds = (size_t)(a.n + 1) * 4;
+  const int pl = log2_of(a.page);
+  if (a.n <= threads)
+    kv_step_kernel<1><<<1, threads, lds, stream>>>(a, pl);
+  else
+    kv_step_kernel<8><<<1, 1024, lds, stream>>>(a, pl);
+  return hipGetLastError();
+}
+
+hipError_t launch_rope_freqs(const q8_rope &r, double *freqs, hipStream_t stream) {
+  rope_freqs_kernel<<<1, 128, 0, stream>>>(r, freqs);
+  return hipGetLastError();
+}
+
+hipError_t launch_qkv_heads(const HeadsArgs &a, hipStream_t stream) {
+  const int D = a.cache.dim, hpw = 256 / D, heads = a.q_heads + 2 * a.cache.heads;
+  const int all = (heads + hpw - 1) / hpw;
+  const int waves = a.m >= 8 ? 8 : 1;
+  const int groups = (a.m + waves - 1) / waves;
+  int split = 4096 / (groups * waves);
+  if (split < 1) split = 1;
+  if (split > all) split = all;
+  const int passes = (all + split - 1) / split;
+  const dim3 grid(groups, (all + passes - 1) / passes);
+  const bool q = a.cache.fmt == Q8_KV_Q8_0;
+  auto k = D == 64 ? (q ? qkv_heads_kernel<64, 1> : qkv_heads_kernel<64, 0>)
+                   : D == 128 ? (q ? qkv_heads_kernel<128, 1> : qkv_heads_kernel<128, 0>)
+                              : (q ? qkv_heads_kernel<256, 1> : qkv_heads_kernel<256, 0>);
+  k<<<grid, 64 * waves, 0, stream>>>(a, passes);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_gather(const KvCache &c, const int32_t *slots, int rows, uint16_t *k_out,
+                            uint16_t *v_out, hipStream_t stream) {
+  const long long total = (long long)rows * c.heads * (c.dim / 8);
+  const unsigned blocks = (unsigned)((total + 255) / 256);
+  auto k = c.fmt == Q8_KV_BF16 ? kv_gather_kernel<0> : kv_gather_kernel<1>;
+  k<<<blocks, 256, 0, stream>>>(c, slots, rows, k_out, v_out);
+  return hipGetLastError();
+}
+
+}  // namespace q8

@@ -72,7 +72,7 @@ typedef enum {
 typedef enum {
   Q8_OK = 0,
   Q8_ERR_SHAPE = 1,     /* m, K or N out of range; K not whole 32-blocks      */
-  Q8_ERR_ACT_FMT = 2,   /* unknown act_fmt                                    */
+  Q8_ERR_ACT_FMT = 2,   /* unknown act_fmt, cache format or rotation kind     */
   Q8_ERR_NULL = 3,      /* a required pointer is NULL                         */
   Q8_ERR_ALIGN = 4,     /* a device pointer is not 16-byte aligned            */
   Q8_ERR_WORKSPACE = 5, /* workspace missing or smaller than required         */
@@ -467,6 +467,259 @@ int q8_gemm_block_dots(const void *x_q8, const int8_t *W_q8, int32_t *dots,
  */
 int q8_gemm_parts(const void *x, const q8_part *parts, int n_parts, int64_t m,
                   int64_t K, int act_fmt, hipStream_t stream);
+
+/* ---- between the projections: head norms, rotation, cache, attention -------- */
+
+/*
+ * What a decoder layer runs between its q/k/v product (q8_gemv_parts,
+ * q8_gemm_parts) and its output product (q8_gemv_fused): the launches Rope,
+ * SetRow and Attention of codegen_cuda/lane/plan.rs, enum Launch, over a
+ * cache in pages.
+ *
+ *   q8_kv_step      page tables, positions and cache slots of a step's rows
+ *                   from the request lengths, on the GPU
+ *   q8_qkv_heads    the q/k/v product's fp32 rows -> normed and rotated query
+ *                   heads (bf16) and the cache's key and value rows
+ *   q8_attn_decode  attention of one row a sequence over the cache
+ *   q8_attn_rows    attention of a chunk of rows a sequence (causal)
+ *   q8_kv_gather    cache rows back as bf16 rows, by slot
+ *
+ * The attention's output is the next product's activation: bf16 rows, or the
+ * q8_quantize_act form.
+ *
+ * The cache is two buffers, keys and values, of q8_kv_bytes(...) bytes each:
+ * n_pages pages of `page` tokens.  A token's slot is page_index * page + its
+ * place in the page.  A page holds one record per head; a record holds the
+ * page's tokens of that head, D = head_dim:
+ *   keys:    token t, dim d at value ((d/8) * page + t) * 8 + d % 8
+ *   values:  token t, dim d at value ((t/8) * D + d) * 8 + t % 8
+ * as bf16 (Q8_KV_BF16), or as int8 codes followed by fp32 scales, one per
+ * token and 32 dims, at scale (d/32) * page + t (Q8_KV_Q8_0: the q8_quantize_act
+ * arithmetic on the fp32 row; 1.125 bytes a value).  So a matrix-core lane
+ * reads its eight keys' or dims' values as one load.  Pages are independent:
+ * a page is copied, shared or moved as page_bytes = q8_kv_bytes(.., 1)
+ * consecutive bytes of each buffer.  A cache needs no initialisation: bytes of
+ * tokens never written are never part of a result.
+ */
+typedef enum {
+  Q8_KV_BF16 = 0, /* bf16 values                                             */
+  Q8_KV_Q8_0 = 1  /* int8 codes and one fp32 scale per token and 32 dims     */
+} q8_kv_fmt;
+
+typedef struct q8_kv_cache {
+  void *k;          /* q8_kv_bytes(fmt, kv_heads, head_dim, page, n_pages)     */
+  void *v;          /* the same size                                           */
+  int64_t n_pages;  /* >= 1; n_pages * page <= 2^31 - 1                        */
+  int32_t fmt;      /* q8_kv_fmt                                               */
+  int32_t kv_heads; /* 1 .. 128                                                */
+  int32_t head_dim; /* 64, 128 or 256                                          */
+  int32_t page;     /* tokens a page: 16, 32, 64, 128 or 256                   */
+} q8_kv_cache;
+
+/* Bytes of each of a cache's two buffers; 0 on a bad shape or format. */
+size_t q8_kv_bytes(int fmt, int64_t kv_heads, int64_t head_dim, int64_t page,
+                   int64_t n_pages);
+
+/* Most sequences of a step, and of an attention call. */
+#define Q8_MAX_SEQS 8192
+
+/*
+ * q8_kv_step: one step's bookkeeping for n sequences, in one launch without a
+ * host round trip.  Per sequence i (all integers, P = page):
+ *     rows_i = max(new_rows[i], 0)            held_i = ceil(lens[i] / P)
+ *   - new_rows[i] < 0: the sequence ends.  Its held_i pages table[i][0..] are
+ *     appended to free_pages (in sequence order), lens_out[i] = 0.
+ *   - otherwise it needs ceil((lens[i] + rows_i) / P) - held_i new pages.  They
+ *     are taken from the end of free_pages, in sequence order and page order
+ *     (the pages of ended sequences included), and written to table[i][held_i
+ *     ..]; lens_out[i] = lens[i] + rows_i.
+ *   - It is refused when it would need more than max_pages pages in all, when
+ *     its rows end past m, or when it needs pages and the list does not hold
+ *     all that it and the sequences before it need.  A refused sequence keeps
+ *     its length and pages, takes no page, and its rows get slot -1.
+ * Row r of the step belongs to the sequence with row_start[i] <= r <
+ * row_start[i+1], row_start the running sum of rows_i, cut at m.  positions[r]
+ * = lens[i] + r - row_start[i], slots[r] = table[i][positions[r] / P] * P +
+ * positions[r] % P; rows of refused sequences and rows past the last
+ * sequence's get position 0 and slot -1 (q8_qkv_heads skips them), so a
+ * captured step may have more rows than are used.
+ * status[0] = refused sequences, status[1] = pages lacking (what the sequences
+ * refused for want of pages, and all others, need in all, less what the list
+ * holds).  lens_out may be lens, and free_count_out free_count (a captured
+ * step advances in place); otherwise outputs must not overlap inputs.  table
+ * and free_pages are updated in place: entries not named above stay as they
+ * were.  Requires 1 <= n <= Q8_MAX_SEQS, 1 <= m <= Q8_MAX_GEMM_ROWS, page as in
+ * q8_kv_cache, max_pages >= 1, n * max_pages and free_cap <= 2^31 - 1.  A
+ * length below 0 counts as 0 and one above max_pages * P as that, a
+ * free_count outside 0 .. free_cap as the nearer of the two; pages past
+ * free_cap are dropped.
+ */
+typedef struct q8_kv_step_args {
+  const int32_t *lens;       /* n: tokens each sequence has in the cache       */
+  const int32_t *new_rows;   /* n: its rows in this step; < 0: it ends         */
+  int32_t *table;            /* n x max_pages page indexes, updated            */
+  int32_t *free_pages;       /* free_cap page indexes, the first free_count    */
+  const int32_t *free_count; /* 1                                              */
+  int32_t *lens_out;         /* n; may be lens                                 */
+  int32_t *free_count_out;   /* 1; may be free_count                           */
+  int32_t *row_start;        /* n + 1                                          */
+  int32_t *positions;        /* m                                              */
+  int32_t *slots;            /* m                                              */
+  int32_t *status;           /* 2                                              */
+  int64_t n;
+  int64_t max_pages;
+  int64_t free_cap;
+  int64_t m;
+  int32_t page;
+} q8_kv_step_args;
+
+int q8_kv_step(const q8_kv_step_args *step /* host pointer */, hipStream_t stream);
+
+/*
+ * q8_rope_freqs: the rotary frequencies freqs[p], p < rot/2, in radians a
+ * position, fp64 (device memory, 16-byte aligned), from
+ *     f_p = base^(-2p / rot)
+ * scaled for contexts longer than the original one by
+ *   Q8_ROPE_SCALE_NONE    f_p
+ *   Q8_ROPE_SCALE_LINEAR  f_p / factor
+ *   Q8_ROPE_SCALE_TURNS   f_p g + (f_p / factor) (1 - g), g = clamp((t - low) /
+ *                         (high - low), 0, 1), t = original * f_p / 2 pi the
+ *                         turns the pair makes over the original context
+ *   Q8_ROPE_SCALE_INDEX   the same with g = 1 - clamp((p - a) / (b - a), 0, 1),
+ *                         a = max(floor(c(high)), 0), b = min(ceil(c(low)), rot - 1),
+ *                         c(t) = rot ln(original / (2 pi t)) / (2 ln base) the
+ *                         pair index that makes t turns (b - a at least 0.001)
+ * Any other frequencies may be written to freqs instead.  Requires rot % 8 ==
+ * 0, 8 <= rot <= 256, base > 1 (TURNS, INDEX: high > low > 0, original >= 1;
+ * all but NONE: factor >= 1).
+ */
+typedef enum {
+  Q8_ROPE_SCALE_NONE = 0,
+  Q8_ROPE_SCALE_LINEAR = 1,
+  Q8_ROPE_SCALE_TURNS = 2,
+  Q8_ROPE_SCALE_INDEX = 3
+} q8_rope_scale;
+
+typedef struct q8_rope {
+  double base;
+  double factor;
+  double low;       /* turns below which a pair is slowed whole               */
+  double high;      /* turns above which a pair is kept                       */
+  int64_t original; /* positions of the original context                      */
+  int32_t rot;      /* rotated dims of a head                                  */
+  int32_t scaling;  /* q8_rope_scale                                           */
+} q8_rope;
+
+int q8_rope_freqs(const q8_rope *rope /* host pointer */, double *freqs,
+                  hipStream_t stream);
+
+/*
+ * q8_qkv_heads: head norms, position rotation and cache write in one launch.
+ * q, k, v are the fp32 outputs of the q/k/v product (m rows of q_heads,
+ * kv_heads and kv_heads heads of head_dim, strides ldq, ldk, ldv in floats,
+ * multiples of 4; parts of one buffer are fine).  Per row r with slot s =
+ * slots[r] and position p = positions[r], per query and key head x:
+ *     x = x / sqrt(mean(x^2) + eps) * norm       (where its norm is given)
+ *     (a, b) = (a cos - b sin, b cos + a sin)    for each pair of the first rot
+ *         dims: dims i and i + rot/2 (Q8_ROPE_HALF) or 2i and 2i + 1
+ *         (Q8_ROPE_INTERLEAVED), cos and sin of the angle p * freqs[i], taken
+ *         in fp64, times attn_factor; rot = 0: none
+ * in fp32, rounded once: query heads to bf16 rows q_out (m x q_heads x
+ * head_dim), key heads and (as they are) value heads to the cache's slot s in
+ * the cache's format.  Rows whose slot lies outside 0 .. n_pages * page - 1
+ * are skipped: their q_out rows stay as they were.  Two rows of one call must
+ * not have the same slot (which of them the cache then holds, or parts of
+ * which, is not defined); a position below 0 counts as 0.  Requires 1 <= m <=
+ * Q8_MAX_GEMM_ROWS, q_heads a multiple of kv_heads, at most 1024; rot % 8 == 0,
+ * 0 <= rot <= head_dim, freqs when rot > 0; eps >= 0.
+ */
+typedef enum { Q8_ROPE_HALF = 0, Q8_ROPE_INTERLEAVED = 1 } q8_rope_layout;
+
+typedef struct q8_heads {
+  const float *q_norm;  /* head_dim fp32, or NULL: no norm of the query heads   */
+  const float *k_norm;  /* head_dim fp32, or NULL: no norm of the key heads     */
+  const double *freqs;  /* rot / 2 fp64 radians a position, or NULL with rot 0  */
+  float eps;
+  float attn_factor;    /* multiplies cos and sin (1: plain)                    */
+  int32_t rot;
+  int32_t layout;       /* q8_rope_layout                                       */
+} q8_heads;
+
+int q8_qkv_heads(const float *q, int64_t ldq, const float *k, int64_t ldk,
+                 const float *v, int64_t ldv, int64_t m, int64_t q_heads,
+                 const q8_heads *heads /* host pointer */, const int32_t *positions,
+                 const int32_t *slots, uint16_t *q_out,
+                 const q8_kv_cache *cache /* host pointer */, hipStream_t stream);
+
+/*
+ * q8_kv_gather: the cache rows at slots[0..rows) as bf16 rows (rows x kv_heads
+ * x head_dim, row-major; a Q8_0 row's code * scale rounded once).  Rows whose
+ * slot lies outside the cache stay as they were.  k_out or v_out may be NULL
+ * (not both).  Requires 1 <= rows <= 2^24.
+ */
+int q8_kv_gather(const q8_kv_cache *cache /* host pointer */, const int32_t *slots,
+                 int64_t rows, uint16_t *k_out, uint16_t *v_out, hipStream_t stream);
+
+/*
+ * Attention over the cache.  Sequence i has lens[i] tokens in the cache, this
+ * call's rows the last of them, token t in page table[i][t / page].  A row at
+ * position p sees the tokens
+ *     t <= p,  and with window > 0 only those with t > p - window or t < sinks
+ * (the last `window` tokens, its own among them, and the first `sinks`).  Query
+ * head h reads key/value head h / (q_heads / kv_heads):
+ *     o[h] = sum_t softmax_t(scale * q[h] . k_t) v_t
+ * the scores, softmax statistics and sums in fp32; the probabilities enter the
+ * value product rounded to bf16 (times the value scale in a Q8_0 cache).  A
+ * row that sees no token gets zeros.  Tokens not seen are not part of the
+ * result whatever their cache bytes hold.  A length below 0 counts as 0, one
+ * above max_pages * page as that; tokens on a page index outside 0 .. n_pages
+ * - 1 are not seen.
+ *
+ * q is m x q_heads x head_dim bf16.  The output is written as o (m x q_heads *
+ * head_dim bf16, may be NULL) and/or o_q8 (its quantized form from the fp32
+ * values, by q8_quantize_act's arithmetic and layout for m rows of K = q_heads *
+ * head_dim: the next product's activation; may be NULL).
+ *
+ * The workspace is the caller's: q8_attn_workspace_bytes(...) bytes, 16-byte
+ * aligned, NULL when that is 0.  As in q8_gemv_ws its first 4 MiB are arrival
+ * counters, zero at the first use and left at zero by every call (so a
+ * workspace zeroed once serves calls of any shape, the products' too); calls
+ * that share a workspace must be ordered, graphs captured over it included.
+ * Results do not depend on timing: pieces of a sequence are joined in order.
+ */
+typedef struct q8_attn {
+  float scale;     /* finite                                                  */
+  int32_t window;  /* tokens a row sees back, its own included; 0: all        */
+  int32_t sinks;   /* first tokens always seen (with window > 0), >= 0        */
+} q8_attn;
+
+/* Workspace bytes of q8_attn_rows for m rows of n sequences, or with m = 0 of
+ * q8_attn_decode for n sequences (0 on invalid arguments). */
+size_t q8_attn_workspace_bytes(int64_t m, int64_t n, int64_t q_heads,
+                               const q8_kv_cache *cache /* host pointer */);
+
+/*
+ * q8_attn_decode: row i is the last token of sequence i, 1 <= n <= Q8_MAX_SEQS
+ * (a sequence of length 0 gets zeros).  Each workgroup takes an equal share of
+ * all sequences' tokens, so long and short sequences mix freely.
+ */
+int q8_attn_decode(const uint16_t *q, int64_t q_heads,
+                   const q8_kv_cache *cache /* host pointer */, const int32_t *table,
+                   int64_t max_pages, const int32_t *lens, int64_t n,
+                   const q8_attn *attn /* host pointer */, uint16_t *o, void *o_q8,
+                   hipStream_t stream, void *workspace, size_t ws_bytes);
+
+/*
+ * q8_attn_rows: rows row_start[i] .. row_start[i+1]-1 are the last tokens of
+ * sequence i (row_start as q8_kv_step writes it: n + 1 values that do not
+ * fall, from 0, at most m).  Rows past row_start[n] are left as they were in o
+ * and o_q8.  1 <= m <= Q8_MAX_GEMM_ROWS, 1 <= n <= Q8_MAX_SEQS.
+ */
+int q8_attn_rows(const uint16_t *q, int64_t m, int64_t q_heads,
+                 const q8_kv_cache *cache /* host pointer */, const int32_t *table,
+                 int64_t max_pages, const int32_t *lens, const int32_t *row_start,
+                 int64_t n, const q8_attn *attn /* host pointer */, uint16_t *o,
+                 void *o_q8, hipStream_t stream, void *workspace, size_t ws_bytes);
 
 /* ---- errors and resources ------------------------------------------------ */
 
