@@ -23,7 +23,8 @@ SOURCES = ["q8_kernels.hip", "q8_mfma32.hip", "q8_tile16.hip", "q8_gemm.hip", "q
 # Per-source device flags.  The GEMM writes its MFMA results to VGPRs (by
 # default the compiler routes them through one AGPR quad and serialises the
 # matrix core behind its reads).
-SOURCE_FLAGS = {"q8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+SOURCE_FLAGS = {s: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+                for s in ("q8_gemm.hip", "q8_attn.hip", "q8_attn_rows.hip")}
 ARCH = os.environ.get("Q8_OFFLOAD_ARCH", "gfx950")
 
 

@@ -14,20 +14,21 @@ using namespace dev;
 
 constexpr float kLowest = -3.0e38f;   // below every score's running maximum, and finite
 
-// The tiles of kKvTile tokens that rows at positions p0 .. p1 of a sequence
+// The tiles of KT tokens that rows at positions p0 .. p1 of a sequence
 // see: tiles 0 .. a-1 (the first tokens kept under a window), then t0 .. up to
 // p1's.  Tile u of the nt is tile u (u < a) or u - a + t0.
 struct Span {
   int a, t0, nt;
   __device__ __forceinline__ int tile(int u) const { return u < a ? u : u - a + t0; }
 };
+template <int KT>
 __device__ __forceinline__ Span span_of(int p0, int p1, int window, int sinks) {
   Span s;
   const int lo = (window > 0 && p0 >= window) ? p0 - window + 1 : 0;
-  s.t0 = lo / kKvTile;
-  s.a = (min(sinks, lo) + kKvTile - 1) / kKvTile;
+  s.t0 = lo / KT;
+  s.a = (int)(((long long)min(sinks, lo) + KT - 1) / KT);
   if (s.a >= s.t0) s.a = s.t0 = 0;
-  s.nt = p1 < 0 ? 0 : s.a + p1 / kKvTile + 1 - s.t0;
+  s.nt = p1 < 0 ? 0 : s.a + p1 / KT + 1 - s.t0;
   return s;
 }
 

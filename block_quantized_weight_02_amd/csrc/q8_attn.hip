@@ -7,12 +7,15 @@
 namespace q8 {
 namespace {
 
-constexpr int kWaves = 4;              // waves of a workgroup, each its own tiles
 constexpr int kHeadTile = 16;          // query heads of one matrix-core tile
-constexpr int kTargetWorkgroups = 512; // two of the 256 CUs' each
-constexpr int kMinTiles = kWaves;      // fewest tiles of a workgroup's share
+constexpr int kTargetWorkgroups = 256;
+constexpr int kMinTiles = 4;           // fewest tiles of a workgroup's share
+constexpr int kListTiles = 256;        // tiles of a share listed in LDS at a time
+constexpr int kListSeqs = 64;          // and sequences
 
-// One key/value tile of a wave in registers.
+__device__ __forceinline__ bf16x8_t as_bf16x8(uint4 v) { return __builtin_bit_cast(bf16x8_t, v); }
+
+// One key/value tile of a wave in registers: lane (i = l%16, c = l/16).
 template <int D, int FMT> struct Tile;
 template <int D> struct Tile<D, Q8_KV_BF16> {
   uint4 k[D / 32][2];   // block b: keys 2i and 2i+1, dims 32b + 8c ..+7
@@ -21,81 +24,99 @@ template <int D> struct Tile<D, Q8_KV_BF16> {
 template <int D> struct Tile<D, Q8_KV_Q8_0> {
   uint4 k[D / 32];      // block b: dims 32b + 8c ..+7 of keys 2i, then 2i+1
   uint4 v[D / 32];      // keys 8c ..+7 of dims 32T + 2i, then 32T + 2i + 1
-  float4 ks[D / 32][2]; // key scales of keys 8c ..+7
-  float4 vs[D / 32][2];
+  float ks[D / 64];     // the scale of (block, key) = (j / 32, j % 32), j = l + 64r;
+  float vs[D / 64];     // they go through LDS to the lanes that need them
 };
 
-__device__ __forceinline__ bf16x8_t as_bf16x8(uint4 v) { return __builtin_bit_cast(bf16x8_t, v); }
+// A listed tile: its pages (of its two 16-token halves, -1: none), its first
+// token, and its sequence's place in the list.
+struct Listed {
+  int page[2];
+  int key0;
+  int seq;
+};
+
+// A value all lanes hold alike, in a scalar register.
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ Listed listed(const Listed &t) {   // into scalar registers
+  return Listed{{uni(t.page[0]), uni(t.page[1])}, uni(t.key0), 0};
+}
 
 // The online softmax of one wave: scores transposed.  A 16x16x32 product of
-// (16 keys x 32 dims) with (32 dims x 16 query heads) leaves lane (i = l%16,
-// c = l/16) with keys 4c .. 4c+3 of head i.  The key fragments' rows are
-// interleaved -- row r of the first product is key 2r of the 32-key tile, of
-// the second key 2r+1 -- so the lane's eight scores are keys 8c .. 8c+7, which
-// is exactly the operand the value product wants (k = 8c+j, column i): the
-// probabilities never leave their lane, and the sums O^T (dims x heads) are
-// rescaled by one factor a lane.
+// (16 keys x 32 dims) with (32 dims x 16 query heads) leaves lane (i, c) with
+// keys 4c .. 4c+3 of head i.  The key fragments' rows are interleaved -- row r
+// of the first product is key 2r of the 32-key tile, of the second key 2r+1 --
+// so the lane's eight scores are keys 8c .. 8c+7, which is exactly the operand
+// the value product wants (k = 8c+j, column i): the probabilities never leave
+// their lane, and the sums O^T (dims x heads) are rescaled by one factor a lane.
 template <int D, int FMT>
 struct Wave {
   static constexpr int NB = D / 32, NT = D / 16;
   bf16x8_t q[NB];
   f32x4_t o[NT];
   float m, l;
+  Tile<D, FMT> t;
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) o[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int T = 0; T < NT; ++T) o[T] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     m = kLowest;
     l = 0.0f;
   }
 
-  // kpage, vpage: this lane's pages of the tile (its keys 2i, 2i+1 and 8c ..)
-  __device__ __forceinline__ static void load(Tile<D, FMT> &t, const KvCache &c, size_t head_off,
-                                              int key0, int kpage, int vpage) {
+  __device__ __forceinline__ void load_k(const KvCache &c, size_t head_off, const Listed &ti) {
     const int lane = threadIdx.x & 63, i = lane & 15, cc = lane >> 4;
     const int P = 1 << c.page_log2;
-    const int kt = (key0 + 2 * i) & (P - 1), vt = (key0 + 8 * cc) & (P - 1);
-    const char *kr = c.k + (size_t)kpage * c.page_bytes() + head_off;
-    const char *vr = c.v + (size_t)vpage * c.page_bytes() + head_off;
+    const int kt = (ti.key0 + 2 * i) & (P - 1);
+    const int page = max(i < 8 ? ti.page[0] : ti.page[1], 0);
+    const char *kr = c.k + (size_t)page * c.page_bytes() + head_off;
     if constexpr (FMT == Q8_KV_BF16) {
+      const char *p = kr + (cc * P + kt) * 16;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const char *p = kr + ((size_t)((4 * b + cc) * P + kt)) * 16;
-        t.k[b][0] = ld_stream16(p);
-        t.k[b][1] = ld_stream16(p + 16);
+        t.k[b][0] = ld_stream16(p + (size_t)b * P * 64);
+        t.k[b][1] = ld_stream16(p + (size_t)b * P * 64 + 16);
       }
-#pragma unroll
-      for (int T = 0; T < NT; ++T) t.v[T] = ld_stream16(vr + ((size_t)(vt >> 3) * D + 16 * T + i) * 16);
     } else {
-      const float *ks = reinterpret_cast<const float *>(kr + (size_t)D * P);
-      const float *vs = reinterpret_cast<const float *>(vr + (size_t)D * P);
-      // the key scales are those of the lane's scores: keys 8c .., the value
-      // page's tokens
-      const float *ksc = reinterpret_cast<const float *>(c.k + (size_t)vpage * c.page_bytes() +
-                                                         head_off + (size_t)D * P);
-      (void)ks;
+      const char *p = kr + (cc * P + kt) * 8;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        t.k[b] = ld_stream16(kr + ((size_t)((4 * b + cc) * P + kt)) * 8);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        t.ks[b][0] = ld_scale16f(reinterpret_cast<const float4 *>(ksc + b * P + vt));
-        t.ks[b][1] = ld_scale16f(reinterpret_cast<const float4 *>(ksc + b * P + vt + 4));
-      }
-#pragma unroll
-      for (int T = 0; T < NB; ++T)
-        t.v[T] = ld_stream16(vr + ((size_t)(vt >> 3) * D + 32 * T + 2 * i) * 8);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        t.vs[b][0] = ld_scale16f(reinterpret_cast<const float4 *>(vs + b * P + vt));
-        t.vs[b][1] = ld_scale16f(reinterpret_cast<const float4 *>(vs + b * P + vt + 4));
-      }
+      for (int b = 0; b < NB; ++b) t.k[b] = ld_stream16(p + (size_t)b * P * 32);
+      load_scales(t.ks, c.k, c, head_off, ti);
     }
   }
 
-  // seen: bit j set if key key0 + 8c + j is seen; all: every lane's are all set
-  __device__ __forceinline__ void step(Tile<D, FMT> &t, float scale_log2, unsigned seen, bool all) {
-    float s[8];
+  __device__ __forceinline__ void load_v(const KvCache &c, size_t head_off, const Listed &ti) {
+    const int lane = threadIdx.x & 63, i = lane & 15, cc = lane >> 4;
+    const int P = 1 << c.page_log2;
+    const int vt = (ti.key0 + 8 * cc) & (P - 1);
+    const int page = max(cc < 2 ? ti.page[0] : ti.page[1], 0);
+    const char *vr = c.v + (size_t)page * c.page_bytes() + head_off;
+    if constexpr (FMT == Q8_KV_BF16) {
+      const char *p = vr + ((vt >> 3) * D + i) * 16;
+#pragma unroll
+      for (int T = 0; T < NT; ++T) t.v[T] = ld_stream16(p + T * 256);
+    } else {
+      const char *p = vr + ((vt >> 3) * D + 2 * i) * 8;
+#pragma unroll
+      for (int T = 0; T < NB; ++T) t.v[T] = ld_stream16(p + T * 256);
+      load_scales(t.vs, c.v, c, head_off, ti);
+    }
+  }
+
+  __device__ __forceinline__ static void load_scales(float *s, const char *base, const KvCache &c,
+                                                     size_t head_off, const Listed &ti) {
+    const int lane = threadIdx.x & 63, P = 1 << c.page_log2, key = lane & 31;
+    const int page = max(key < 16 ? ti.page[0] : ti.page[1], 0);
+    const float *p = reinterpret_cast<const float *>(base + (size_t)page * c.page_bytes() +
+                                                     head_off + (size_t)D * P) +
+                     (lane >> 5) * P + ((ti.key0 + key) & (P - 1));
+#pragma unroll
+    for (int r = 0; r < D / 64; ++r) s[r] = ld_scale4f(p + (size_t)r * 2 * P);
+  }
+
+  // Scores of the tile in t.k, as exponents of two.
+  __device__ __forceinline__ void scores(float *s, float scale_log2, float *wlds) {
     if constexpr (FMT == Q8_KV_BF16) {
       f32x4_t s0{0.0f, 0.0f, 0.0f, 0.0f}, s1{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -109,6 +130,9 @@ struct Wave {
         s[2 * r + 1] = s1[r];
       }
     } else {
+      const int lane = threadIdx.x & 63, cc = lane >> 4;
+#pragma unroll
+      for (int r = 0; r < D / 64; ++r) wlds[r * 64 + lane] = t.ks[r];
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] = 0.0f;
 #pragma unroll
@@ -118,8 +142,9 @@ struct Wave {
             i8x8_to_bf16(make_uint2(t.k[b].x, t.k[b].y)), q[b], z, 0, 0, 0);
         const f32x4_t s1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
             i8x8_to_bf16(make_uint2(t.k[b].z, t.k[b].w)), q[b], z, 0, 0, 0);
-        const float ks[8] = {t.ks[b][0].x, t.ks[b][0].y, t.ks[b][0].z, t.ks[b][0].w,
-                             t.ks[b][1].x, t.ks[b][1].y, t.ks[b][1].z, t.ks[b][1].w};
+        const float4 a0 = *reinterpret_cast<const float4 *>(wlds + b * 32 + 8 * cc);
+        const float4 a1 = *reinterpret_cast<const float4 *>(wlds + b * 32 + 8 * cc + 4);
+        const float ks[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           s[2 * r] = fmaf(ks[2 * r], s0[r], s[2 * r]);
@@ -129,12 +154,35 @@ struct Wave {
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] *= scale_log2;
-    if (!all) {
-      // unseen keys: no score, and no value (their bytes may hold anything)
+  }
+
+  // Softmax step over the scores (s becomes probabilities); unseen keys hold
+  // -infinity.
+  __device__ __forceinline__ void soften(float *s) {
+    float mx = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])),
+                     fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
+    mx = max_across(mx);
+    const float mn = fmaxf(m, mx);
+    const float alpha = exp2_fast(m - mn);
+    m = mn;
+    float ps = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (!(seen >> j & 1)) s[j] = -__builtin_inff();
-      if constexpr (FMT == Q8_KV_BF16) {
+    for (int j = 0; j < 8; ++j) {
+      s[j] = exp2_fast(s[j] - mn);
+      ps += s[j];
+    }
+    l = l * alpha + ps;
+    if (__any(alpha != 1.0f)) {
+#pragma unroll
+      for (int T = 0; T < NT; ++T) o[T] *= alpha;
+    }
+  }
+
+  // Adds the tile's values.  seen: bit j set if key 8c + j is; all: in every lane.
+  __device__ __forceinline__ void values(const float *p, unsigned seen, bool all, float *wlds) {
+    if constexpr (FMT == Q8_KV_BF16) {
+      const bf16x8_t pb = to_bf16x8(p);
+      if (!all) {                        // an unseen key's values may be anything
         const uint32_t keep[4] = {(seen & 1 ? 0xffffu : 0u) | (seen & 2 ? 0xffff0000u : 0u),
                                   (seen & 4 ? 0xffffu : 0u) | (seen & 8 ? 0xffff0000u : 0u),
                                   (seen & 16 ? 0xffffu : 0u) | (seen & 32 ? 0xffff0000u : 0u),
@@ -147,39 +195,21 @@ struct Wave {
           t.v[T].w &= keep[3];
         }
       }
-    }
-    float mx = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])),
-                     fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float mn = fmaxf(m, mx);
-    const float alpha = exp2_fast(m - mn);
-    m = mn;
-    float p[8], ps = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      p[j] = exp2_fast(s[j] - mn);
-      ps += p[j];
-    }
-    l = l * alpha + ps;
-    if (__any(alpha != 1.0f)) {
-#pragma unroll
-      for (int t2 = 0; t2 < NT; ++t2) o[t2] *= alpha;
-    }
-    if constexpr (FMT == Q8_KV_BF16) {
-      const bf16x8_t pb = to_bf16x8(p);
 #pragma unroll
       for (int T = 0; T < NT; ++T)
         o[T] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(t.v[T]), pb, o[T], 0, 0, 0);
     } else {
+      const int lane = threadIdx.x & 63, cc = lane >> 4;
+      wlds += D;
+#pragma unroll
+      for (int r = 0; r < D / 64; ++r) wlds[r * 64 + lane] = t.vs[r];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float vs[8] = {t.vs[b][0].x, t.vs[b][0].y, t.vs[b][0].z, t.vs[b][0].w,
-                             t.vs[b][1].x, t.vs[b][1].y, t.vs[b][1].z, t.vs[b][1].w};
-        float w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = p[j] * vs[j];
-        if (!all) {
+        const float4 a0 = *reinterpret_cast<const float4 *>(wlds + b * 32 + 8 * cc);
+        const float4 a1 = *reinterpret_cast<const float4 *>(wlds + b * 32 + 8 * cc + 4);
+        float w[8] = {p[0] * a0.x, p[1] * a0.y, p[2] * a0.z, p[3] * a0.w,
+                      p[4] * a1.x, p[5] * a1.y, p[6] * a1.z, p[7] * a1.w};
+        if (!all) {                      // nor may its scale count
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if (!(seen >> j & 1)) w[j] = 0.0f;
@@ -192,73 +222,57 @@ struct Wave {
       }
     }
   }
-};
 
-// A sequence's place in the launch: its tiles are before .. before + nt of all.
-struct Place {
-  int i;
-  int before;
-};
-
-__device__ __forceinline__ int tiles_of(const AttnArgs &a, int i) {
-  const int len = clamp_len(a.lens[i], a.max_pages, a.cache.page_log2);
-  return span_of(len - 1, len - 1, a.window, a.sinks).nt;
-}
-
-// The number of all sequences' tiles, and by all threads alike the sequence
-// that holds tile number x * C (n if there is none), C = what fits(total)
-// gives.  A wave takes 64 sequences at a time; with more than 64 the blocks'
-// sums go through LDS.
-__device__ __forceinline__ Place find_place(const AttnArgs &a, int *sums, int x, int chunks,
-                                            int *C_out, int *total_out) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int blocks = (a.n + 63) / 64;
-  int total = 0, block = 0, base = 0, C, x0;
-  if (blocks == 1) {
-    const int t = lane < a.n ? tiles_of(a, lane) : 0;
-    int incl = t;
+  // The sums of head i to dst[dim].
+  __device__ __forceinline__ void store(float *dst) const {
+    const int cc = (threadIdx.x & 63) >> 4;
+    if constexpr (FMT == Q8_KV_BF16) {   // o[T]: dims 16T + 4c ..+3
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(incl, o);
-      if (lane >= o) incl += u;
+      for (int T = 0; T < NT; ++T)
+        *reinterpret_cast<float4 *>(dst + 16 * T + 4 * cc) =
+            make_float4(o[T][0], o[T][1], o[T][2], o[T][3]);
+    } else {                             // o[2b], o[2b+1]: even and odd dims of 32b + 8c ..+7
+#pragma unroll
+      for (int T = 0; T < NT; T += 2) {
+        float4 *p = reinterpret_cast<float4 *>(dst + 16 * T + 8 * cc);
+        p[0] = make_float4(o[T][0], o[T + 1][0], o[T][1], o[T + 1][1]);
+        p[1] = make_float4(o[T][2], o[T + 1][2], o[T][3], o[T + 1][3]);
+      }
     }
-    total = __shfl(incl, 63);
-    C = max((total + chunks - 1) / chunks, kMinTiles);
-    x0 = x * C;
-    const int before = __popcll(__ballot(incl <= x0 && lane < a.n));
-    *C_out = C;
-    *total_out = total;
-    Place p;
-    p.i = before;
-    p.before = before > 0 ? __shfl(incl, before - 1) : 0;
-    return p;
   }
-  for (int b = wave; b < blocks; b += kWaves) {
-    const int i = b * 64 + lane;
-    int t = i < a.n ? tiles_of(a, i) : 0;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) t += __shfl_xor(t, o);
-    if (lane == 0) sums[b] = t;
+
+  __device__ __forceinline__ static float max_across(float x) {   // over the lanes of one head
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
   }
-  __syncthreads();
-  for (int b = 0; b < blocks; ++b) total += sums[b];
-  C = max((total + chunks - 1) / chunks, kMinTiles);
-  x0 = x * C;
-  for (block = 0; block < blocks - 1 && base + sums[block] <= x0; ++block) base += sums[block];
-  const int i = block * 64 + lane;
-  int incl = i < a.n ? tiles_of(a, i) : 0;
+};
+
+__device__ __forceinline__ int tiles_of(const AttnArgs &a, int len) {
+  return span_of<kKvTile>(len - 1, len - 1, a.window, a.sinks).nt;
+}
+__device__ __forceinline__ int len_of(const AttnArgs &a, int i) {
+  return i < a.n ? clamp_len(a.lens[i], a.max_pages, a.cache.page_log2) : 0;
+}
+__device__ __forceinline__ int scan_wave(int v) {   // inclusive sum over the lanes
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(incl, o);
-    if (lane >= o) incl += u;
+    const int u = __shfl_up(v, o);
+    if (lane >= o) v += u;
   }
-  const int before = __popcll(__ballot(base + incl <= x0 && i < a.n));
-  *C_out = C;
-  *total_out = total;
-  Place p;
-  p.i = block * 64 + before;
-  p.before = base + (before > 0 ? __shfl(incl, before - 1) : 0);
-  return p;
+  return v;
+}
+
+// The thread's index, opaque: what is computed from it stays where it is used
+// (once a sequence or list) rather than being kept in registers across the
+// token stream.
+__device__ __forceinline__ int thread_here() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
 }
 
 // Floats of one partial result: up to 16 heads' sums, then their maxima and
@@ -267,25 +281,38 @@ __host__ __device__ constexpr int record_floats(int heads, int dim) {
   return heads * dim + 2 * kHeadTile;
 }
 
+// Dynamic LDS: the waves' sums (and a join's, in their place), and for Q8_0
+// each wave's scales.
+template <int D> constexpr int kRowFloats = D + 4;   // 16-byte shifts between heads' rows
+template <int D, int FMT, int kWaves>
+size_t decode_lds_bytes(int heads) {
+  return ((size_t)kWaves * heads * kRowFloats<D> + (FMT == Q8_KV_Q8_0 ? kWaves * 2 * D : 0)) * 4;
+}
+
 // Grid: (chunks, units); a unit is one key/value head and up to 16 of its query
 // heads.  All sequences' tiles stand in one row and workgroup x takes tiles x*C
 // .. (x+1)*C - 1 of it, C the same for all, so that the token streams are
 // equally long whatever the lengths; a share may end one sequence and begin
-// the next.  The share's waves take every fourth tile, two tiles in flight
-// each (K and V of the next are loaded while this one is computed), and meet
-// in LDS.  A sequence that lies in one share is finished there; otherwise its
-// pieces go to the workspace and the last workgroup to arrive joins them in
-// order.
-template <int D, int FMT>
+// the next.  The share's tiles are listed in LDS with their pages (no table
+// lookup in the stream), wave w takes every kWaves-th: while a tile's scores
+// turn into probabilities the next one's keys are in flight, and after its
+// values are added the next one's values.  At a sequence's end the waves meet
+// in LDS, with the next sequence's first tiles already loading.  A sequence
+// that lies in one share is finished there; otherwise its pieces go to the
+// workspace and the last workgroup to arrive joins them in order.
+template <int D, int FMT, int kWaves>
 __global__ void __launch_bounds__(64 * kWaves)
 attn_decode_kernel(AttnArgs a) {
-  constexpr int NB = D / 32, NT = D / 16;
-  constexpr int kStride = D + 4;                       // LDS row: 16-byte shifts between heads
-  __shared__ float red[(kWaves - 1) * kHeadTile * kStride];
+  constexpr int kThreads = 64 * kWaves;
+  constexpr int NB = D / 32, kRow = kRowFloats<D>, per_head = D / 4;
+  extern __shared__ __align__(16) float red[];
   __shared__ float red_m[kWaves][kHeadTile], red_l[kWaves][kHeadTile];
+  __shared__ Listed list[kListTiles];
+  __shared__ int pre[kListSeqs + 1], slen[kListSeqs];
   __shared__ int sums[Q8_MAX_SEQS / 64];
   __shared__ int is_last;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, c4 = lane >> 4;
+  const int lane = threadIdx.x & 63, i16 = lane & 15, c4 = lane >> 4;
+  const int wave = uni(threadIdx.x >> 6);
   const int units = gridDim.y, unit = blockIdx.y, x = blockIdx.x, chunks = gridDim.x;
   const int tiles_a_head = (a.group + kHeadTile - 1) / kHeadTile;
   const int hk = unit / tiles_a_head, h0 = hk * a.group + (unit % tiles_a_head) * kHeadTile;
@@ -294,227 +321,297 @@ attn_decode_kernel(AttnArgs a) {
   const KvCache c = a.cache;
   const size_t head_off = (size_t)hk * c.record();
   const int pl = c.page_log2;
+  float *wlds = red + (size_t)kWaves * min(a.group, kHeadTile) * kRow + wave * 2 * D;
 
-  int C, total;
-  Place pc = find_place(a, sums, x, chunks, &C, &total);
-  const int x1 = min((x + 1) * C, total);
-  int t = x * C;
-
-  while (t < x1) {
-    const int len = clamp_len(a.lens[pc.i], a.max_pages, pl);
-    const Span sp = span_of(len - 1, len - 1, a.window, a.sinks);
-    if (sp.nt == 0) {
-      ++pc.i;
-      continue;
+  // The number of all tiles, the share's size, and the 64 sequences it starts
+  // in (w0; before: the tiles of those before them).  list_seqs writes 64
+  // sequences' lengths and first tiles.
+  auto list_seqs = [&](int w0, int before) {
+    const int l = thread_here();
+    const int len = len_of(a, w0 + l);
+    const int incl = scan_wave(tiles_of(a, len));
+    if (wave == 0) {
+      if (l == 0) pre[0] = before;
+      pre[l + 1] = before + incl;
+      slen[l] = len;
     }
-    const int s0 = t - pc.before, s1 = min(x1 - pc.before, sp.nt);
-    const int32_t *row = a.table + (long long)pc.i * a.max_pages;
-    const int last_page = (len - 1) >> pl;
+    return uni(__shfl(incl, 63));
+  };
+  const int blocks = (a.n + 63) / 64;
+  int total = 0, w0 = 0, before = 0;
+  if (blocks == 1) {
+    if (wave == 0) total = list_seqs(0, 0);
+    __syncthreads();
+    total = uni(pre[kListSeqs]);
+  } else {
+    for (int b = wave; b < blocks; b += kWaves) {
+      const int s = scan_wave(tiles_of(a, len_of(a, b * 64 + lane)));
+      if (lane == 63) sums[b] = s;
+    }
+    __syncthreads();
+    for (int b = 0; b < blocks; ++b) total += uni(sums[b]);
+  }
+  const int C = max((total + chunks - 1) / chunks, kMinTiles);
+  const int x0 = x * C, x1 = min(x0 + C, total);
+  if (blocks > 1)
+    for (; w0 / 64 < blocks - 1 && before + uni(sums[w0 / 64]) <= x0; w0 += 64)
+      before += uni(sums[w0 / 64]);
+  bool seqs_listed = blocks == 1;
 
-    Wave<D, FMT> w;
-    w.reset();
+  Wave<D, FMT> w;
+  w.reset();
+  auto load_q = [&](int i) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (i16 < heads)
-        v = *reinterpret_cast<const uint4 *>(a.q + ((size_t)pc.i * a.q_heads + h0 + i16) * D +
+        v = *reinterpret_cast<const uint4 *>(a.q + ((size_t)i * a.q_heads + h0 + i16) * D +
                                              32 * b + 8 * c4);
       w.q[b] = as_bf16x8(v);
     }
-
-    Tile<D, FMT> ta, tb;
-    bool oka, okb;    // the lane's value page is a page of the cache
-    // tile u of the sequence into registers; tiles past the share reload its last
-    auto fetch = [&](Tile<D, FMT> &tile, bool &ok, int u) {
-      const int key0 = sp.tile(min(u, s1 - 1)) * kKvTile;
-      int kp = row[min((key0 + 2 * i16) >> pl, last_page)];
-      int vp = row[min((key0 + 8 * c4) >> pl, last_page)];
-      ok = (unsigned)vp < (unsigned)c.n_pages;
-      if ((unsigned)kp >= (unsigned)c.n_pages) kp = 0;
-      if (!ok) vp = 0;
-      w.load(tile, c, head_off, key0, kp, vp);
-    };
-    auto compute = [&](Tile<D, FMT> &tile, bool ok, int u) {
-      const int key = sp.tile(u) * kKvTile + 8 * c4;
-      unsigned seen = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = key + j;
-        const bool in = k < len && (a.window <= 0 || k >= len - a.window || k < a.sinks);
-        seen |= (in && ok) ? 1u << j : 0u;
-      }
-      w.step(tile, a.scale_log2, seen, __all(seen == 0xffu));
-    };
-    int u = s0 + wave;
-    if (u < s1) {
-      fetch(ta, oka, u);
-      for (; u < s1; u += 2 * kWaves) {
-        fetch(tb, okb, u + kWaves);
-        compute(ta, oka, u);
-        if (u + kWaves >= s1) break;
-        fetch(ta, oka, u + 2 * kWaves);
-        compute(tb, okb, u + kWaves);
-      }
+  };
+  int open = -1;                          // the sequence whose heads (and sums) the waves hold
+  bool fresh = true;                      // no sums yet
+  for (int tb = x0; tb < x1;) {
+    // list 64 sequences from w0, and the share's next tiles among theirs
+    if (!seqs_listed) {
+      __syncthreads();                    // the last list is read
+      if (wave == 0) (void)list_seqs(w0, before);
+      __syncthreads();
     }
-
-    // the waves meet: each scales its sums to the common maximum
-    w.l += __shfl_xor(w.l, 16);
-    w.l += __shfl_xor(w.l, 32);
-    __syncthreads();                       // the last segment's LDS is read
-    if (c4 == 0) {
-      red_m[wave][i16] = w.m;
-      red_l[wave][i16] = w.l;
+    seqs_listed = false;
+    const int te = min(min(x1, tb + kListTiles), uni(pre[kListSeqs]));
+    for (int k0 = wave * 64; k0 < te - tb; k0 += kThreads) {
+      // a tile's sequence is the last that starts at or before it: the wave finds
+      // that of its first tile, its other tiles are in that one or soon after
+      const int l = thread_here() & 63, k = k0 + l;
+      int lo = __popcll(__ballot(pre[l + 1] <= tb + k0));
+      if (k >= te - tb) continue;
+      while (pre[lo + 1] <= tb + k) ++lo;
+      const int len = slen[lo];
+      Listed ti;
+      ti.key0 = span_of<kKvTile>(len - 1, len - 1, a.window, a.sinks).tile(tb + k - pre[lo]) * kKvTile;
+      ti.seq = lo;
+      const int32_t *row = a.table + (long long)(w0 + lo) * a.max_pages;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int p = row[min(ti.key0 + 16 * h, len - 1) >> pl];
+        ti.page[h] = (unsigned)p < (unsigned)c.n_pages ? p : -1;
+      }
+      list[k] = ti;
     }
     __syncthreads();
-    float M = red_m[0][i16];
-#pragma unroll
-    for (int v = 1; v < kWaves; ++v) M = fmaxf(M, red_m[v][i16]);
-    const float f = exp2_fast(w.m - M);
-#pragma unroll
-    for (int T = 0; T < NT; ++T) w.o[T] *= f;
-    // (wave, head, dim) in LDS; wave 0's slot is written last, summed in wave order
-    auto place = [&](float *dst, int T, bool add) {
-      // bf16: T's rows are dims 16T + 4c ..+3.  Q8_0: T = 2b and 2b+1 hold the
-      // even and odd dims of 32b + 8c ..+7.
-      if constexpr (FMT == Q8_KV_BF16) {
-        float4 *p = reinterpret_cast<float4 *>(dst + 16 * T + 4 * c4);
-        *p = make_float4(w.o[T][0], w.o[T][1], w.o[T][2], w.o[T][3]);
-      } else {
-        if (T & 1) return;
-        float4 *p = reinterpret_cast<float4 *>(dst + 16 * T + 8 * c4);
-        p[0] = make_float4(w.o[T][0], w.o[T + 1][0], w.o[T][1], w.o[T + 1][1]);
-        p[1] = make_float4(w.o[T][2], w.o[T + 1][2], w.o[T][3], w.o[T + 1][3]);
-      }
-      (void)add;
-    };
-    if (wave > 0 && i16 < heads) {
-#pragma unroll
-      for (int T = 0; T < NT; ++T) place(red + ((wave - 1) * kHeadTile + i16) * kStride, T, false);
+    const int nk = te - tb;
+    int k = wave;
+    if (k < nk) {
+      w.load_k(c, head_off, listed(list[k]));
+      w.load_v(c, head_off, listed(list[k]));
     }
-    __syncthreads();
-    if (wave == 0 && i16 < heads) {
-      // wave 0 adds the others' sums to its own registers and leaves the result
-      // in the first slot
+
+    int j = nk > 0 ? uni(list[0].seq) : kListSeqs;
+    for (; j < kListSeqs; ++j) {
+      const int s0 = uni(pre[j]), s1 = uni(pre[j + 1]);   // the sequence's tiles of all
+      if (s0 >= te) break;
+      if (s0 == s1) continue;
+      const int i = w0 + j, len = uni(slen[j]), ke = min(s1, te) - tb;
+      const int from = a.window > 0 ? len - a.window : 0;   // the window's first token
+      if (open != i || fresh) {
+        if (open != i) load_q(i);         // else it came while the last one was finished
+        open = i;
+        fresh = false;
+        w.reset();
+        // waited for here, so that the stream below waits for its own loads only
 #pragma unroll
-      for (int T = 0; T < NT; ++T) {
-        if constexpr (FMT == Q8_KV_BF16) {
-          const int at = i16 * kStride + 16 * T + 4 * c4;
+        for (int b = 0; b < NB; ++b) asm volatile("" : "+v"(w.q[b]));
+      }
+      for (; k < ke; k += kWaves) {
+        const Listed ti = listed(list[k]), tn = listed(list[min(k + kWaves, nk - 1)]);
+        float s[8];
+        w.scores(s, a.scale_log2, wlds);
+        w.load_k(c, head_off, tn);
+        const bool all = ((ti.key0 + kKvTile <= len) & ((ti.page[0] | ti.page[1]) >= 0) &
+                          ((ti.key0 >= from) | (ti.key0 + kKvTile <= a.sinks)));
+        unsigned seen = 0xffu;
+        if (!all) {
+          seen = 0;
+          const int stop = (c4 < 2 ? ti.page[0] : ti.page[1]) >= 0 ? len : 0;
 #pragma unroll
-          for (int v = 0; v < kWaves - 1; ++v) {
-            const float4 y = *reinterpret_cast<const float4 *>(red + v * kHeadTile * kStride + at);
-            w.o[T] += f32x4_t{y.x, y.y, y.z, y.w};
-          }
-        } else if (!(T & 1)) {
-          const int at = i16 * kStride + 16 * T + 8 * c4;
-#pragma unroll
-          for (int v = 0; v < kWaves - 1; ++v) {
-            const float4 y0 = *reinterpret_cast<const float4 *>(red + v * kHeadTile * kStride + at);
-            const float4 y1 =
-                *reinterpret_cast<const float4 *>(red + v * kHeadTile * kStride + at + 4);
-            w.o[T] += f32x4_t{y0.x, y0.z, y1.x, y1.z};
-            w.o[T + 1] += f32x4_t{y0.y, y0.w, y1.y, y1.w};
+          for (int e = 0; e < 8; ++e) {
+            const int key = ti.key0 + 8 * c4 + e;
+            const bool in = (key < stop) & ((key >= from) | (key < a.sinks));
+            seen |= in ? 1u << e : 0u;
+            s[e] = in ? s[e] : -__builtin_inff();
           }
         }
-        if (FMT == Q8_KV_BF16 || (T & 1)) place(red + i16 * kStride, FMT == Q8_KV_BF16 ? T : T - 1, true);
+        w.soften(s);
+        w.values(s, seen, all, wlds);
+        w.load_v(c, head_off, tn);
       }
-    }
-    __syncthreads();
+      if (s1 > te && te < x1) break;      // the share's next list goes on with this sequence
 
-    const int first = pc.before / C, segs = (pc.before + sp.nt - 1) / C - first + 1;
-    const int per_head = D / 4;
-    if (segs == 1) {
-      for (int idx = threadIdx.x; idx < heads * per_head; idx += 64 * kWaves) {
-        const int h = idx / per_head, d = (idx % per_head) * 4;
-        float Mh = red_m[0][h], L = 0.0f;
-#pragma unroll
-        for (int v = 1; v < kWaves; ++v) Mh = fmaxf(Mh, red_m[v][h]);
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) L += red_l[v][h] * exp2_fast(red_m[v][h] - Mh);
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const float4 y = *reinterpret_cast<const float4 *>(red + h * kStride + d);
-        store_out(a, pc.i, (h0 + h) * D + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+      // the waves meet, the next sequence's heads already on their way
+      const bool more = ke < nk;
+      open = more ? w0 + uni(list[min(ke, nk - 1)].seq) : -1;
+      fresh = true;
+      if (more) load_q(open);
+      float lsum = w.l + __shfl_xor(w.l, 16);
+      lsum += __shfl_xor(lsum, 32);
+      __syncthreads();                    // the last sequence's sums are read
+      if (i16 < heads) {
+        w.store(red + (wave * heads + i16) * kRow);
+        if (c4 == 0) {
+          red_m[wave][i16] = w.m;
+          red_l[wave][i16] = lsum;
+        }
       }
-    } else {
-      // this piece to the workspace, at slot x + i (unique: each step along
-      // the tiles moves on x or i)
+      __syncthreads();
+      const int first = s0 / C, segs = (s1 - 1) / C - first + 1;
       const size_t stride = (size_t)units * rec;
-      float *mine = a.partial + ((size_t)(x + pc.i) * units + unit) * rec;
-      const buf_t out = make_buf(mine, rec * 4);
-      for (int idx = threadIdx.x; idx < heads * per_head; idx += 64 * kWaves) {
+      // this piece's slot x + i is its own: each step along the tiles moves on
+      // x or i
+      const buf_t out = make_buf(a.partial + ((size_t)(x + i) * units + unit) * rec, rec * 4);
+      for (int idx = thread_here(); idx < heads * per_head; idx += kThreads) {
         const int h = idx / per_head, d = (idx % per_head) * 4;
-        buf_st16_sys(out, (h * D + d) * 4, *reinterpret_cast<const float4 *>(red + h * kStride + d));
+        float M = red_m[0][h], L = 0.0f;
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v) M = fmaxf(M, red_m[v][h]);
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+          const float f = exp2_fast(red_m[v][h] - M);
+          const float4 z = *reinterpret_cast<const float4 *>(red + (v * heads + h) * kRow + d);
+          L += red_l[v][h] * f;
+          y.x += z.x * f;
+          y.y += z.y * f;
+          y.z += z.z * f;
+          y.w += z.w * f;
+        }
+        if (segs == 1) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          store_out(a, i, (h0 + h) * D + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+        } else {
+          buf_st16_sys(out, (h * D + d) * 4, y);
+          if (d == 0) {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(M), out, (rec - 2 * kHeadTile + h) * 4, 0, kBufSys);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(L), out, (rec - kHeadTile + h) * 4, 0, kBufSys);
+          }
+        }
       }
-      if (threadIdx.x < heads) {
-        const int h = threadIdx.x;
-        float Mh = red_m[0][h], L = 0.0f;
-        for (int v = 1; v < kWaves; ++v) Mh = fmaxf(Mh, red_m[v][h]);
-        for (int v = 0; v < kWaves; ++v) L += red_l[v][h] * exp2_fast(red_m[v][h] - Mh);
-        float *ml = mine + (rec - 2 * kHeadTile);
-        __hip_atomic_store(ml + h, Mh, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-        __hip_atomic_store(ml + kHeadTile + h, L, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-      }
+      if (segs == 1) continue;
       stores_done();
       __syncthreads();
+      unsigned *cnt = &a.counters[(size_t)i * units + unit];
       if (threadIdx.x == 0)
-        is_last = __hip_atomic_fetch_add(&a.counters[pc.i * units + unit], 1u, __ATOMIC_RELAXED,
-                                         __HIP_MEMORY_SCOPE_SYSTEM) == (unsigned)(segs - 1);
+        is_last = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM) ==
+                  (unsigned)(segs - 1);
       __syncthreads();
-      if (is_last) {
-        const float *base = a.partial + ((size_t)(first + pc.i) * units + unit) * rec;
-        const buf_t in = make_buf(base, (unsigned)(((size_t)(segs - 1) * stride + rec) * 4));
-        const unsigned step = (unsigned)(stride * 4);
-        for (int idx = threadIdx.x; idx < heads * per_head; idx += 64 * kWaves) {
-          const int h = idx / per_head, d = (idx % per_head) * 4;
-          const unsigned at = (h * D + d) * 4, mat = (rec - 2 * kHeadTile + h) * 4;
-          float Mh = kLowest, L = 0.0f;
-          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          constexpr int kBatch = 8;
-          for (int g0 = 0; g0 < segs; g0 += kBatch) {
-            float gm[kBatch], gl[kBatch];
-            float4 gy[kBatch];
+      if (!is_last) continue;
+      // Join: groups of threads take runs of the pieces, then meet in LDS.
+      const buf_t in = make_buf(a.partial + ((size_t)(first + i) * units + unit) * rec,
+                                (unsigned)(((size_t)(segs - 1) * stride + rec) * 4));
+      const unsigned step = (unsigned)(stride * 4);
+      const int items = heads * per_head;
+      const int groups = max(1, min(kThreads / items, kWaves));
+      for (int idx = thread_here(); idx < items * groups; idx += kThreads) {
+        const int g = idx / items, h = idx % items / per_head, d = (idx % per_head) * 4;
+        const unsigned at = (h * D + d) * 4, mat = (rec - 2 * kHeadTile + h) * 4;
+        const int g0 = segs * g / groups, g1 = segs * (g + 1) / groups;
+        float M = kLowest, L = 0.0f;
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        constexpr int kBatch = 8;
+        for (int p0 = g0; p0 < g1; p0 += kBatch) {
+          float gm[kBatch], gl[kBatch];
+          float4 gy[kBatch];
 #pragma unroll
-            for (int g = 0; g < kBatch; ++g) {
-              const unsigned off = (unsigned)min(g0 + g, segs - 1) * step;
-              gm[g] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(in, off + mat, 0, kBufSys));
-              gl[g] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(in, off + mat + kHeadTile * 4, 0, kBufSys));
-              gy[g] = buf_ld16_sys(in, off + at);
-            }
+          for (int p = 0; p < kBatch; ++p) {
+            const unsigned off = (unsigned)min(p0 + p, g1 - 1) * step;
+            gm[p] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(in, off + mat, 0, kBufSys));
+            gl[p] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(in, off + mat + kHeadTile * 4, 0, kBufSys));
+            gy[p] = buf_ld16_sys(in, off + at);
+          }
 #pragma unroll
-            for (int g = 0; g < kBatch; ++g) {
-              if (g0 + g < segs) {
-                const float Mn = fmaxf(Mh, gm[g]);
-                const float fo = exp2_fast(Mh - Mn), fn = exp2_fast(gm[g] - Mn);
-                L = L * fo + gl[g] * fn;
-                y.x = y.x * fo + gy[g].x * fn;
-                y.y = y.y * fo + gy[g].y * fn;
-                y.z = y.z * fo + gy[g].z * fn;
-                y.w = y.w * fo + gy[g].w * fn;
-                Mh = Mn;
-              }
+          for (int p = 0; p < kBatch; ++p) {
+            if (p0 + p < g1) {
+              const float Mn = fmaxf(M, gm[p]);
+              const float fo = exp2_fast(M - Mn), fn = exp2_fast(gm[p] - Mn);
+              L = L * fo + gl[p] * fn;
+              y.x = y.x * fo + gy[p].x * fn;
+              y.y = y.y * fo + gy[p].y * fn;
+              y.z = y.z * fo + gy[p].z * fn;
+              y.w = y.w * fo + gy[p].w * fn;
+              M = Mn;
             }
           }
-          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-          store_out(a, pc.i, (h0 + h) * D + d,
-                    make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
         }
-        if (threadIdx.x == 0)
-          __hip_atomic_store(&a.counters[pc.i * units + unit], 0u, __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_SYSTEM);
+        if (groups == 1) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          store_out(a, i, (h0 + h) * D + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+        } else {
+          *reinterpret_cast<float4 *>(red + (g * heads + h) * kRow + d) = y;
+          if (d == 0) {
+            red_m[g][h] = M;
+            red_l[g][h] = L;
+          }
+        }
       }
+      if (groups > 1) {
+        __syncthreads();
+        for (int idx = thread_here(); idx < items; idx += kThreads) {
+          const int h = idx / per_head, d = (idx % per_head) * 4;
+          float M = kLowest, L = 0.0f;
+          for (int g = 0; g < groups; ++g) M = fmaxf(M, red_m[g][h]);
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int g = 0; g < groups; ++g) {
+            const float f = exp2_fast(red_m[g][h] - M);
+            const float4 z = *reinterpret_cast<const float4 *>(red + (g * heads + h) * kRow + d);
+            L += red_l[g][h] * f;
+            y.x += z.x * f;
+            y.y += z.y * f;
+            y.z += z.z * f;
+            y.w += z.w * f;
+          }
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          store_out(a, i, (h0 + h) * D + d, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+        }
+      }
+      if (threadIdx.x == 0)
+        __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
     }
-    t = pc.before + s1;
-    if (s1 == sp.nt) {
-      pc.before += sp.nt;
-      ++pc.i;
+    tb = te;
+    // the next list starts at the sequence that holds tile te
+    if (tb < x1) {
+      const int jn = min(j, kListSeqs);
+      before = pre[jn];
+      w0 += jn;
     }
   }
 
   // sequences without a token: zeros
   for (int i = x; i < a.n; i += chunks) {
-    if (tiles_of(a, i) != 0) continue;
-    for (int idx = threadIdx.x; idx < heads * (D / 4); idx += 64 * kWaves)
-      store_out(a, i, (h0 + idx / (D / 4)) * D + idx % (D / 4) * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    if (tiles_of(a, len_of(a, i)) != 0) continue;
+    for (int idx = threadIdx.x; idx < heads * per_head; idx += kThreads)
+      store_out(a, i, (h0 + idx / per_head) * D + idx % per_head * 4,
+                make_float4(0.0f, 0.0f, 0.0f, 0.0f));
   }
+}
+
+// Waves of a workgroup: eight where a tile is short (64 dims) or its codes have
+// to be widened, four else, and at 256 dims, where eight waves' registers spill.
+// Measured on MI355X (us, eight against four): 64 sequences of 64 dims behind a
+// window of 1024 32.4 against 33.5; Q8_0, 16 sequences up to 32768 tokens 96
+// against 112; bf16, 128 dims, 1 x 131072 88 against 85.
+template <int D, int FMT>
+hipError_t launch(const AttnArgs &a, int units, hipStream_t stream) {
+  constexpr int kWaves = D == 64 || (FMT == Q8_KV_Q8_0 && D == 128) ? 8 : 4;
+  const size_t lds = decode_lds_bytes<D, FMT, kWaves>(a.group < kHeadTile ? a.group : kHeadTile);
+  if (lds > 48 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void *>(attn_decode_kernel<D, FMT, kWaves>),
+        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  attn_decode_kernel<D, FMT, kWaves><<<dim3(a.chunks, units), 64 * kWaves, lds, stream>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -535,14 +632,12 @@ size_t attn_decode_partial_bytes(int64_t n, int64_t q_heads, int64_t kv_heads, i
 
 hipError_t launch_attn_decode(const AttnArgs &a, hipStream_t stream) {
   const int units = a.cache.heads * ((a.group + kHeadTile - 1) / kHeadTile);
-  const dim3 grid(a.chunks, units);
   const bool q = a.cache.fmt == Q8_KV_Q8_0;
-  auto k = a.cache.dim == 64
-               ? (q ? attn_decode_kernel<64, 1> : attn_decode_kernel<64, 0>)
-               : a.cache.dim == 128 ? (q ? attn_decode_kernel<128, 1> : attn_decode_kernel<128, 0>)
-                                    : (q ? attn_decode_kernel<256, 1> : attn_decode_kernel<256, 0>);
-  k<<<grid, 64 * kWaves, 0, stream>>>(a);
-  return hipGetLastError();
+  switch (a.cache.dim) {
+    case 64: return q ? launch<64, 1>(a, units, stream) : launch<64, 0>(a, units, stream);
+    case 128: return q ? launch<128, 1>(a, units, stream) : launch<128, 0>(a, units, stream);
+    default: return q ? launch<256, 1>(a, units, stream) : launch<256, 0>(a, units, stream);
+  }
 }
 
 }  // namespace q8

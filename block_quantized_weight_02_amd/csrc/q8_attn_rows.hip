@@ -15,10 +15,15 @@ constexpr int kMinSplitTiles = 8;       // fewest tiles of a split that computes
 
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 
-// LDS bytes of one stage: a tile of keys and values, and their scales.
+// Keys of a stage: what the workgroup loads, and waits for, at a time.
+template <int D> constexpr int kStageKeys = D == 256 ? 32 : 64;
+constexpr int kListGroups = 512;        // 16-token groups whose pages are held in LDS at a time
+
+// LDS bytes of one stage: keys and values as bf16 (Q8_0: the codes, exact),
+// and their scales.
 template <int D, int FMT>
 constexpr int stage_bytes() {
-  return FMT == Q8_KV_BF16 ? 2 * kKvTile * D * 2 : 2 * kKvTile * D + 2 * kKvTile * (D / 32) * 4;
+  return kStageKeys<D> * (2 * D * 2 + (FMT == Q8_KV_Q8_0 ? 2 * (D / 32) * 4 : 0));
 }
 
 struct Block {
@@ -60,30 +65,85 @@ __device__ __forceinline__ Block find_block(const AttnArgs &a, int x) {
   return r;
 }
 
+__device__ __forceinline__ float swap_halves(float x) {   // lane l's value in lane l ^ 32
+  return __shfl_xor(x, 32);
+}
+
+// Adds one 16-key step of a tile that some columns see in part.  Probabilities
+// of unseen keys are zero, but their values may be infinite or NaN: those are
+// left out of the product, and set the sums of the columns that do see them.
+// seen: bit e for key 8 hf + e of the step.
+__device__ __forceinline__ void add_values_masked(f32x16_t &o, uint4 f, bf16x8_t p, unsigned seen) {
+  uint32_t w[4] = {f.x, f.y, f.z, f.w}, plus[4], minus[4], any = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    // 0xffff in the halves that are not finite (exponent all ones)
+    const uint32_t odd = (((w[e] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u) >> 15;
+    const uint32_t mask = odd * 0xffffu;
+    const uint32_t nan = (((w[e] & 0x007f007fu) + 0x007f007fu) & 0x00800080u) >> 7;   // mantissa set
+    const uint32_t neg = (w[e] >> 15) & 0x00010001u;
+    plus[e] = (odd & (nan | (neg ^ 0x00010001u))) * 0x3f80u;    // 1.0 where +inf or NaN
+    minus[e] = (odd & (nan | neg)) * 0x3f80u;                   // 1.0 where -inf or NaN
+    w[e] &= ~mask;
+    any |= odd;
+  }
+  o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+      __builtin_bit_cast(bf16x8_t, make_uint4(w[0], w[1], w[2], w[3])), p, o, 0, 0, 0);
+  if (__any(any != 0)) {
+    uint32_t s[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      s[e] = (seen >> (2 * e) & 1 ? 0x3f80u : 0u) | (seen >> (2 * e + 1) & 1 ? 0x3f800000u : 0u);
+    const bf16x8_t sb = __builtin_bit_cast(bf16x8_t, make_uint4(s[0], s[1], s[2], s[3]));
+    f32x16_t z;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+    const f32x16_t zp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        __builtin_bit_cast(bf16x8_t, make_uint4(plus[0], plus[1], plus[2], plus[3])), sb, z, 0, 0, 0);
+    const f32x16_t zm = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        __builtin_bit_cast(bf16x8_t, make_uint4(minus[0], minus[1], minus[2], minus[3])), sb, z, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if (zp[e] > 0.0f) o[e] += __builtin_inff();
+      if (zm[e] > 0.0f) o[e] -= __builtin_inff();
+    }
+  }
+}
+
 __host__ __device__ constexpr int record_floats(int dim) { return kCols * dim + 2 * kCols; }
 
 // Grid: (blocks of columns x key/value heads, the heads fastest -- eight of
 // them put a head's keys in one XCD's L2 --, key splits).  A column is one
 // (row, query head of the group) pair, so the group's heads share the keys;
-// a wave holds 32 columns, the workgroup's waves share the tiles in LDS.
-// Scores are transposed (32 keys x 32 columns, v_mfma 32x32x16): a lane's
-// sixteen scores belong to one column, and with the key fragments' rows
-// permuted (row 8a + 4h + e is key 16 (a/2) + 8h + 4 (a%2) + e) they are, eight
-// by eight, the value product's operand, so probabilities stay in their lane.
+// a wave holds 32 columns, the workgroup's waves share the staged keys and
+// values in LDS (two stages; the next one's loads are in flight, in registers,
+// while this one is computed).  Scores are transposed (32 keys x 32 columns,
+// v_mfma 32x32x16): a lane's sixteen scores belong to one column, and with the
+// key fragments' rows permuted (row 8a + 4h + e is key 16 (a/2) + 8h + 4 (a%2) +
+// e) they are, eight by eight, the value product's operand, so probabilities
+// stay in their lane, and the running maximum is a lane's own scalar.  That
+// maximum is only raised when a score passes it by 2^8 (kSlack): sums stay far
+// inside fp32, and the sums O^T are rescaled once or twice a block instead of
+// at nearly every stage.
+constexpr float kSlack = 8.0f;
+
 template <int D, int FMT>
-__global__ void __launch_bounds__(64 * kWaves)
+__global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
 attn_rows_kernel(AttnArgs a) {
-  constexpr int NB = D / 32, NK = D / 16;
+  constexpr int NB = D / 32, NK = D / 16, KT = kStageKeys<D>, NS = KT / 32;
+  constexpr int kThreads = 64 * kWaves;
   constexpr int kStage = stage_bytes<D, FMT>();
-  constexpr int kValBytes = FMT == Q8_KV_BF16 ? kKvTile * D * 2 : kKvTile * D;
-  constexpr int kElem = FMT == Q8_KV_BF16 ? 16 : 8;       // bytes of eight values
-  constexpr int kPieces = kValBytes / 16;                  // 16-byte pieces of K (and of V)
-  constexpr int kPer = kPieces / (64 * kWaves);            // a thread's
-  static_assert(kPieces % (64 * kWaves) == 0 || kPieces < 64 * kWaves, "pieces");
-  constexpr int kIt = kPer > 0 ? kPer : 1;
+  constexpr int kVal = KT * D * 2;                         // bytes of the staged keys
+  constexpr int kElem = FMT == Q8_KV_BF16 ? 16 : 8;        // bytes of eight cached values
+  constexpr int kPer = 16 / kElem;                         // eights in a 16-byte piece
+  constexpr int kIt = KT * D / 8 / kPer / kThreads;        // a thread's pieces of the keys
+  static_assert(kIt * kThreads * kPer * 8 == KT * D, "pieces");
+  constexpr int kScales = KT * NB;                         // scales of the keys
+  constexpr int kSIt = (kScales + kThreads - 1) / kThreads;
   extern __shared__ __align__(16) char lds[];
+  __shared__ int pids[kListGroups];
   __shared__ int is_last;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, hf = lane >> 5;
   const KvCache c = a.cache;
   const int hk = blockIdx.x % c.heads, bx = blockIdx.x / c.heads;
@@ -100,7 +160,7 @@ attn_rows_kernel(AttnArgs a) {
   const int blk = blocks - 1 - bl.block;
   const int c0 = blk * kCols, c1 = min(c0 + kCols, ncol) - 1;
   const int p0 = len - R + c0 / a.group, p1 = len - R + c1 / a.group;
-  const Span sp = span_of(max(p0, 0), p1, a.window, a.sinks);
+  const Span sp = span_of<KT>(max(p0, 0), p1, a.window, a.sinks);
   const int S = min((int)gridDim.y, max(sp.nt / kMinSplitTiles, 1));
   const int s = blockIdx.y;
   if (s >= S) return;
@@ -111,12 +171,19 @@ attn_rows_kernel(AttnArgs a) {
   const int j = min(mycol, ncol - 1) / a.group, head = hk * a.group + min(mycol, ncol - 1) % a.group;
   const int pos = len - R + j, row = start + j;
 
+  // a negative scale goes into the queries' signs
+  const float scale = fabsf(a.scale_log2);
+  const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
   bf16x8_t q[NK];
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (live)
       v = *reinterpret_cast<const uint4 *>(a.q + ((size_t)row * a.q_heads + head) * D + 16 * k + 8 * hf);
+    v.x ^= flip;
+    v.y ^= flip;
+    v.z ^= flip;
+    v.w ^= flip;
     q[k] = __builtin_bit_cast(bf16x8_t, v);
   }
 
@@ -128,224 +195,233 @@ attn_rows_kernel(AttnArgs a) {
   float m = kLowest, l = 0.0f;
 
   const int32_t *trow = a.table + (long long)bl.i * a.max_pages;
-  const int last_page = max(len - 1, 0) >> pl;
+  const int last = max(len - 1, 0);
   const size_t head_off = (size_t)hk * c.record();
+  const size_t page_bytes = c.page_bytes();
 
-  // the thread's pieces of a tile, global -> registers -> LDS
+  // The thread's 16-byte pieces of a stage, cache -> registers.  Keys lie as
+  // [D/8][KT][8], values as [KT/8][D][8], in the cache's pages and in LDS; a
+  // piece is one eight of bf16 values or two of int8 codes.
   uint4 rk[kIt], rv[kIt];
-  float rs[2][(NB * kKvTile + 64 * kWaves - 1) / (64 * kWaves)];
-  auto page_of = [&](int key, bool &ok) {
-    const int p = trow[min(key >> pl, last_page)];
-    ok = (unsigned)p < (unsigned)c.n_pages;
-    return ok ? p : 0;
-  };
-  auto fetch = [&](int u) {
-    const int key0 = sp.tile(u) * kKvTile;
+  float rks[kSIt], rvs[kSIt];
+  auto fetch = [&](int u, int base) {
+    const int *ids = pids + (u - base) * (KT / 16);
+    const int key0 = sp.tile(u) * KT;
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
-      const int p = threadIdx.x + it * 64 * kWaves;
-      if (kPieces >= 64 * kWaves || p < kPieces) {
-        // keys: [D/8][32 keys][kElem]
-        const int kk = p * 16 / kElem;                       // (chunk, key) of the piece
-        const int key = key0 + kk % kKvTile, ch = kk / kKvTile;
-        bool ok;
-        const char *rec = c.k + (size_t)page_of(key, ok) * c.page_bytes() + head_off;
-        rk[it] = *reinterpret_cast<const uint4 *>(rec + ((size_t)ch * P + (key & (P - 1))) * kElem);
-        // values: [4 key chunks][D][kElem]
-        const int kv = p * 16 / kElem;
-        const int vkey = key0 + kv / D * 8, d = kv % D;
-        rec = c.v + (size_t)page_of(vkey, ok) * c.page_bytes() + head_off;
-        rv[it] = *reinterpret_cast<const uint4 *>(rec + ((size_t)((vkey & (P - 1)) >> 3) * D + d) * kElem);
-      }
+      const int e = ((int)threadIdx.x + it * kThreads) * kPer;
+      const int key = e % KT, ch = e / KT;
+      const char *rec = c.k + (size_t)max(ids[key / 16], 0) * page_bytes + head_off;
+      rk[it] = *reinterpret_cast<const uint4 *>(rec + (ch * P + ((key0 + key) & (P - 1))) * kElem);
+      const int vc = e / D, d = e % D;
+      rec = c.v + (size_t)max(ids[vc / 2], 0) * page_bytes + head_off;
+      rv[it] = *reinterpret_cast<const uint4 *>(
+          rec + ((((key0 + 8 * vc) & (P - 1)) >> 3) * D + d) * kElem);
     }
     if constexpr (FMT == Q8_KV_Q8_0) {
 #pragma unroll
-      for (int it = 0; it < (NB * kKvTile + 64 * kWaves - 1) / (64 * kWaves); ++it) {
-        const int p = threadIdx.x + it * 64 * kWaves;
-        if (p < NB * kKvTile) {
-          const int key = key0 + p % kKvTile, b = p / kKvTile;
-          bool ok;
-          const size_t at = (size_t)page_of(key, ok) * c.page_bytes() + head_off + (size_t)D * P;
-          rs[0][it] = reinterpret_cast<const float *>(c.k + at)[b * P + (key & (P - 1))];
-          rs[1][it] = reinterpret_cast<const float *>(c.v + at)[b * P + (key & (P - 1))];
-        }
+      for (int it = 0; it < kSIt; ++it) {
+        const int p = min((int)threadIdx.x + it * kThreads, kScales - 1);
+        const int key = p % KT, b = p / KT;
+        const size_t at = (size_t)max(ids[key / 16], 0) * page_bytes + head_off + (size_t)D * P +
+                          (b * P + ((key0 + key) & (P - 1))) * 4;
+        rks[it] = *reinterpret_cast<const float *>(c.k + at);
+        rvs[it] = *reinterpret_cast<const float *>(c.v + at);
       }
     }
   };
   auto stage = [&](char *st) {
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
-      const int p = threadIdx.x + it * 64 * kWaves;
-      if (kPieces >= 64 * kWaves || p < kPieces) {
-        *reinterpret_cast<uint4 *>(st + p * 16) = rk[it];
-        *reinterpret_cast<uint4 *>(st + kValBytes + p * 16) = rv[it];
+      char *d = st + ((int)threadIdx.x + it * kThreads) * kPer * 16;
+      if constexpr (FMT == Q8_KV_BF16) {
+        *reinterpret_cast<uint4 *>(d) = rk[it];
+        *reinterpret_cast<uint4 *>(d + kVal) = rv[it];
+      } else {
+        *reinterpret_cast<bf16x8_t *>(d) = i8x8_to_bf16(make_uint2(rk[it].x, rk[it].y));
+        *reinterpret_cast<bf16x8_t *>(d + 16) = i8x8_to_bf16(make_uint2(rk[it].z, rk[it].w));
+        *reinterpret_cast<bf16x8_t *>(d + kVal) = i8x8_to_bf16(make_uint2(rv[it].x, rv[it].y));
+        *reinterpret_cast<bf16x8_t *>(d + kVal + 16) = i8x8_to_bf16(make_uint2(rv[it].z, rv[it].w));
       }
     }
     if constexpr (FMT == Q8_KV_Q8_0) {
-      float *sc = reinterpret_cast<float *>(st + 2 * kValBytes);
+      float *sc = reinterpret_cast<float *>(st + 2 * kVal);
 #pragma unroll
-      for (int it = 0; it < (NB * kKvTile + 64 * kWaves - 1) / (64 * kWaves); ++it) {
-        const int p = threadIdx.x + it * 64 * kWaves;
-        if (p < NB * kKvTile) {
-          sc[p] = rs[0][it];
-          sc[NB * kKvTile + p] = rs[1][it];
+      for (int it = 0; it < kSIt; ++it) {
+        const int p = (int)threadIdx.x + it * kThreads;
+        if (kScales % kThreads == 0 || p < kScales) {
+          sc[p] = rks[it];
+          sc[kScales + p] = rvs[it];
         }
       }
     }
   };
-  // row `col` of the key fragment is this key of the tile
+  // row `col` of a key fragment is this key of its 32
   const int fkey = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
 
-  auto compute = [&](const char *st, int u) {
-    const int key0 = sp.tile(u) * kKvTile;
-    const char *kb = st, *vb = st + kValBytes;
-    const float *ksc = reinterpret_cast<const float *>(st + 2 * kValBytes), *vsc = ksc + NB * kKvTile;
-    f32x16_t x;
+  auto compute = [&](const char *st, int u, int base) {
+    const int key0 = sp.tile(u) * KT;
+    const char *kb = st, *vb = st + kVal;
+    const float *ksc = reinterpret_cast<const float *>(st + 2 * kVal), *vsc = ksc + kScales;
+    f32x16_t x[NS];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-    if constexpr (FMT == Q8_KV_BF16) {
+    for (int n = 0; n < NS; ++n) {
 #pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        const uint4 f = *reinterpret_cast<const uint4 *>(kb + ((2 * k + hf) * kKvTile + fkey) * 16);
-        x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f), q[k], x, 0, 0, 0);
-      }
-    } else {
+      for (int e = 0; e < 16; ++e) x[n][e] = 0.0f;
+      if constexpr (FMT == Q8_KV_BF16) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        f32x16_t z;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) z[e] = 0.0f;
-#pragma unroll
-        for (int k = 2 * b; k < 2 * b + 2; ++k) {
-          const uint2 f = *reinterpret_cast<const uint2 *>(kb + ((2 * k + hf) * kKvTile + fkey) * 8);
-          z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(i8x8_to_bf16(f), q[k], z, 0, 0, 0);
+        for (int k = 0; k < NK; ++k) {
+          const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(kb + ((2 * k + hf) * KT + 32 * n + fkey) * 16);
+          x[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k], x[n], 0, 0, 0);
         }
+      } else {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 w = *reinterpret_cast<const float4 *>(ksc + b * kKvTile + 16 * (g >> 1) + 8 * hf + 4 * (g & 1));
-          x[4 * g] = fmaf(w.x, z[4 * g], x[4 * g]);
-          x[4 * g + 1] = fmaf(w.y, z[4 * g + 1], x[4 * g + 1]);
-          x[4 * g + 2] = fmaf(w.z, z[4 * g + 2], x[4 * g + 2]);
-          x[4 * g + 3] = fmaf(w.w, z[4 * g + 3], x[4 * g + 3]);
+        for (int b = 0; b < NB; ++b) {
+          f32x16_t z;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+#pragma unroll
+          for (int k = 2 * b; k < 2 * b + 2; ++k) {
+            const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(kb + ((2 * k + hf) * KT + 32 * n + fkey) * 16);
+            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k], z, 0, 0, 0);
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float4 w = *reinterpret_cast<const float4 *>(ksc + b * KT + 32 * n + 16 * (g >> 1) + 8 * hf + 4 * (g & 1));
+            x[n][4 * g] = fmaf(w.x, z[4 * g], x[n][4 * g]);
+            x[n][4 * g + 1] = fmaf(w.y, z[4 * g + 1], x[n][4 * g + 1]);
+            x[n][4 * g + 2] = fmaf(w.z, z[4 * g + 2], x[n][4 * g + 2]);
+            x[n][4 * g + 3] = fmaf(w.w, z[4 * g + 3], x[n][4 * g + 3]);
+          }
         }
       }
     }
+    // seen[n] bit e: key 32n + 16 (e/8) + 8 hf + e%8 is
+    const int *ids = pids + (u - base) * (KT / 16);
+    int pages = ids[0];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] *= a.scale_log2;
-    // bit e: key e of the lane's sixteen (16 (e/8) + 8 hf + e%8) is seen
-    const bool inner = key0 + kKvTile - 1 <= p0 &&
-                       (a.window <= 0 || key0 > p1 - a.window || key0 + kKvTile <= a.sinks);
-    bool ok0, ok1;
-    (void)page_of(key0 + 8 * hf, ok0);
-    (void)page_of(key0 + 16 + 8 * hf, ok1);
-    unsigned seen = 0xffffu;
-    unsigned vmask = 0xffffu;     // keys whose values may count for some column
-    if (!inner || !__all(ok0 && ok1)) {
-      seen = vmask = 0;
+    for (int g = 1; g < KT / 16; ++g) pages |= ids[g];
+    const bool all = ((key0 + KT - 1 <= p0) & (__builtin_amdgcn_readfirstlane(pages) >= 0) &
+                      ((a.window <= 0) | (key0 > p1 - a.window) | (key0 + KT <= a.sinks)));
+    unsigned seen[NS];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int key = key0 + 16 * (e >> 3) + 8 * hf + (e & 7);
-        const bool ok = (e < 8 ? ok0 : ok1) && key < len;
-        const bool in = ok && key <= pos && (a.window <= 0 || key > pos - a.window || key < a.sinks);
-        seen |= in ? 1u << e : 0u;
+    for (int n = 0; n < NS; ++n) seen[n] = 0xffffu;
+    if (!all) {
+      const int from = a.window > 0 ? pos - a.window + 1 : 0;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        seen[n] = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int key = key0 + 32 * n + 16 * (e >> 3) + 8 * hf + (e & 7);
+          const int stop = ids[2 * n + (e >> 3)] >= 0 ? min(pos, len - 1) : -1;
+          const bool in = (key <= stop) & ((key >= from) | (key < a.sinks));
+          seen[n] |= in ? 1u << e : 0u;
+          x[n][e] = in ? x[n][e] : -__builtin_inff();
+        }
       }
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (!(seen >> e & 1)) x[e] = -__builtin_inff();
     }
-    (void)vmask;
-    float mx = x[0];
+    float mx = x[0][0];
 #pragma unroll
-    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float mn = fmaxf(m, mx);
-    const float alpha = exp2_fast(m - mn);
-    m = mn;
-    float ps = 0.0f;
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      x[e] = exp2_fast(x[e] - mn);
-      ps += x[e];
-    }
-    l = l * alpha + ps;
-    if (__any(alpha != 1.0f)) {
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[n][e]);
+    mx = fmaxf(mx, swap_halves(mx)) * scale;
+    if (__any(mx > m + kSlack)) {
+      const float mn = fmaxf(m, mx);
+      const float alpha = exp2_fast(m - mn);
+      m = mn;
+      l *= alpha;
 #pragma unroll
       for (int T = 0; T < NB; ++T) o[T] *= alpha;
     }
-    if constexpr (FMT == Q8_KV_BF16) {
-      float p[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) p[e] = x[e];
-      const bf16x8_t pb[2] = {to_bf16x8(p), to_bf16x8(p + 8)};
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
-      for (int T = 0; T < NB; ++T)
+      for (int e = 0; e < 16; ++e) x[n][e] = exp2_fast(fmaf(x[n][e], scale, -m));
+    if (!all) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint4 f = *reinterpret_cast<const uint4 *>(vb + ((2 * t + hf) * D + 32 * T + col) * 16);
-          o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, f), pb[t], o[T], 0, 0, 0);
-        }
-    } else {
+      for (int n = 0; n < NS; ++n)
 #pragma unroll
-      for (int T = 0; T < NB; ++T) {
+        for (int e = 0; e < 16; ++e) x[n][e] = seen[n] >> e & 1 ? x[n][e] : 0.0f;
+    }
+    float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ps[e & 3] += x[n][e];
+    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      if constexpr (FMT == Q8_KV_BF16) {
         float p[16];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 w = *reinterpret_cast<const float4 *>(vsc + T * kKvTile + 16 * (g >> 1) + 8 * hf + 4 * (g & 1));
-          p[4 * g] = x[4 * g] * w.x;
-          p[4 * g + 1] = x[4 * g + 1] * w.y;
-          p[4 * g + 2] = x[4 * g + 2] * w.z;
-          p[4 * g + 3] = x[4 * g + 3] * w.w;
-        }
-        if (seen != 0xffffu) {
+        for (int e = 0; e < 16; ++e) p[e] = x[n][e];
+        const bf16x8_t pb[2] = {to_bf16x8(p), to_bf16x8(p + 8)};
+        if (all) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (!(seen >> e & 1)) p[e] = 0.0f;
-        }
+          for (int T = 0; T < NB; ++T)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint2 f = *reinterpret_cast<const uint2 *>(vb + ((2 * t + hf) * D + 32 * T + col) * 8);
-          o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(i8x8_to_bf16(f), to_bf16x8(p + 8 * t), o[T], 0, 0, 0);
+            for (int t = 0; t < 2; ++t) {
+              const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t + hf) * D + 32 * T + col) * 16);
+              o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[t], o[T], 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+          for (int T = 0; T < NB; ++T)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              uint4 f = *reinterpret_cast<const uint4 *>(vb + ((4 * n + 2 * t + hf) * D + 32 * T + col) * 16);
+              add_values_masked(o[T], f, pb[t], seen[n] >> (8 * t));
+            }
+        }
+      } else {
+#pragma unroll
+        for (int T = 0; T < NB; ++T) {
+          float p[16];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float4 w = *reinterpret_cast<const float4 *>(vsc + T * KT + 32 * n + 16 * (g >> 1) + 8 * hf + 4 * (g & 1));
+            p[4 * g] = x[n][4 * g] * w.x;
+            p[4 * g + 1] = x[n][4 * g + 1] * w.y;
+            p[4 * g + 2] = x[n][4 * g + 2] * w.z;
+            p[4 * g + 3] = x[n][4 * g + 3] * w.w;
+          }
+          if (!all) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p[e] = seen[n] >> e & 1 ? p[e] : 0.0f;
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t + hf) * D + 32 * T + col) * 16);
+            o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, to_bf16x8(p + 8 * t), o[T], 0, 0, 0);
+          }
         }
       }
     }
   };
 
-  // Values of tokens past the sequence, or on no page, may hold anything:
-  // those of a tile that reaches past the length (or names no page) are
-  // zeroed in LDS before they meet a probability of zero.
-  auto scrub = [&](char *st, int u) {
-    const int key0 = sp.tile(u) * kKvTile;
-    if constexpr (FMT == Q8_KV_BF16) {
-      bool ok0, ok1;
-      (void)page_of(key0, ok0);
-      (void)page_of(key0 + 16, ok1);
-      if (key0 + kKvTile <= len && ok0 && ok1) return;
-      uint16_t *v = reinterpret_cast<uint16_t *>(st + kValBytes);
-      for (int e = threadIdx.x; e < kKvTile * D; e += 64 * kWaves) {
-        const int k = e / (8 * D) * 8 + e % 8;
-        if (key0 + k >= len || !(k < 16 ? ok0 : ok1)) v[e] = 0;
-      }
+  constexpr int kListStages = kListGroups / (KT / 16);
+  for (int base = u0; base < u1; base += kListStages) {
+    const int end = min(base + kListStages, u1);
+    __syncthreads();                       // the last list is read
+    for (int g = threadIdx.x; g < (end - base) * (KT / 16); g += kThreads) {
+      const int key = sp.tile(base + g / (KT / 16)) * KT + g % (KT / 16) * 16;
+      const int p = trow[min(key, last) >> pl];
+      pids[g] = (unsigned)p < (unsigned)c.n_pages ? p : -1;
     }
-  };
-
-  if (u0 < u1) {
-    fetch(u0);
+    __syncthreads();
+    fetch(base, base);
     stage(lds);
     __syncthreads();
-    scrub(lds, u0);
-    __syncthreads();
     int cur = 0;
-    for (int u = u0; u < u1; ++u) {
-      if (u + 1 < u1) fetch(u + 1);
-      compute(lds + cur * kStage, u);
-      if (u + 1 < u1) {
-        char *nx = lds + (cur ^ 1) * kStage;
-        stage(nx);
-        __syncthreads();
-        scrub(nx, u + 1);
-        __syncthreads();
-      }
+    for (int u = base; u < end; ++u) {
+      fetch(min(u + 1, end - 1), base);
+      compute(lds + cur * kStage, u, base);
       cur ^= 1;
+      stage(lds + cur * kStage);
+      __syncthreads();
     }
   }
   l += __shfl_xor(l, 32);
