@@ -36,9 +36,6 @@ struct Listed {
   int seq;
 };
 
-// A value all lanes hold alike, in a scalar register.
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 __device__ __forceinline__ Listed listed(const Listed &t) {   // into scalar registers
   return Listed{{uni(t.page[0]), uni(t.page[1])}, uni(t.key0), 0};
 }

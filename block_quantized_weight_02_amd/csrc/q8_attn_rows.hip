@@ -69,45 +69,12 @@ __device__ __forceinline__ float swap_halves(float x) {   // lane l's value in l
   return __shfl_xor(x, 32);
 }
 
-// Adds one 16-key step of a tile that some columns see in part.  Probabilities
-// of unseen keys are zero, but their values may be infinite or NaN: those are
-// left out of the product, and set the sums of the columns that do see them.
-// seen: bit e for key 8 hf + e of the step.
-__device__ __forceinline__ void add_values_masked(f32x16_t &o, uint4 f, bf16x8_t p, unsigned seen) {
-  uint32_t w[4] = {f.x, f.y, f.z, f.w}, plus[4], minus[4], any = 0;
+// Whether any of eight bf16 values is infinite or NaN (exponent all ones).
+__device__ __forceinline__ bool not_finite(u32x4_t v) {
+  uint32_t odd = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    // 0xffff in the halves that are not finite (exponent all ones)
-    const uint32_t odd = (((w[e] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u) >> 15;
-    const uint32_t mask = odd * 0xffffu;
-    const uint32_t nan = (((w[e] & 0x007f007fu) + 0x007f007fu) & 0x00800080u) >> 7;   // mantissa set
-    const uint32_t neg = (w[e] >> 15) & 0x00010001u;
-    plus[e] = (odd & (nan | (neg ^ 0x00010001u))) * 0x3f80u;    // 1.0 where +inf or NaN
-    minus[e] = (odd & (nan | neg)) * 0x3f80u;                   // 1.0 where -inf or NaN
-    w[e] &= ~mask;
-    any |= odd;
-  }
-  o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-      __builtin_bit_cast(bf16x8_t, make_uint4(w[0], w[1], w[2], w[3])), p, o, 0, 0, 0);
-  if (__any(any != 0)) {
-    uint32_t s[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      s[e] = (seen >> (2 * e) & 1 ? 0x3f80u : 0u) | (seen >> (2 * e + 1) & 1 ? 0x3f800000u : 0u);
-    const bf16x8_t sb = __builtin_bit_cast(bf16x8_t, make_uint4(s[0], s[1], s[2], s[3]));
-    f32x16_t z;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) z[e] = 0.0f;
-    const f32x16_t zp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-        __builtin_bit_cast(bf16x8_t, make_uint4(plus[0], plus[1], plus[2], plus[3])), sb, z, 0, 0, 0);
-    const f32x16_t zm = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-        __builtin_bit_cast(bf16x8_t, make_uint4(minus[0], minus[1], minus[2], minus[3])), sb, z, 0, 0, 0);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (zp[e] > 0.0f) o[e] += __builtin_inff();
-      if (zm[e] > 0.0f) o[e] -= __builtin_inff();
-    }
-  }
+  for (int e = 0; e < 4; ++e) odd |= (v[e] & 0x7fff7fffu) + 0x00800080u;
+  return (odd & 0x80008000u) != 0;
 }
 
 __host__ __device__ constexpr int record_floats(int dim) { return kCols * dim + 2 * kCols; }
@@ -143,17 +110,20 @@ attn_rows_kernel(AttnArgs a) {
   extern __shared__ __align__(16) char lds[];
   __shared__ int pids[kListGroups];
   __shared__ int is_last;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
   const int col = lane & 31, hf = lane >> 5;
   const KvCache c = a.cache;
   const int hk = blockIdx.x % c.heads, bx = blockIdx.x / c.heads;
   const int pl = c.page_log2, P = 1 << pl;
 
-  const Block bl = find_block(a, bx);
+  Block bl = find_block(a, bx);
+  bl.i = uni(bl.i);
+  bl.block = uni(bl.block);
   if (bl.i >= a.n) return;
   int start;
-  const int R = rows_of(a, bl.i, &start);
-  const int len = clamp_len(a.lens[bl.i], a.max_pages, pl);
+  const int R = uni(rows_of(a, bl.i, &start));
+  start = uni(start);
+  const int len = uni(clamp_len(a.lens[bl.i], a.max_pages, pl));
   const int ncol = R * a.group;
   // heaviest first: the sequence's last rows see the most tokens
   const int blocks = (ncol + kCols - 1) / kCols;
@@ -202,7 +172,7 @@ attn_rows_kernel(AttnArgs a) {
   // The thread's 16-byte pieces of a stage, cache -> registers.  Keys lie as
   // [D/8][KT][8], values as [KT/8][D][8], in the cache's pages and in LDS; a
   // piece is one eight of bf16 values or two of int8 codes.
-  uint4 rk[kIt], rv[kIt];
+  u32x4_t rk[kIt], rv[kIt];
   float rks[kSIt], rvs[kSIt];
   auto fetch = [&](int u, int base) {
     const int *ids = pids + (u - base) * (KT / 16);
@@ -212,10 +182,10 @@ attn_rows_kernel(AttnArgs a) {
       const int e = ((int)threadIdx.x + it * kThreads) * kPer;
       const int key = e % KT, ch = e / KT;
       const char *rec = c.k + (size_t)max(ids[key / 16], 0) * page_bytes + head_off;
-      rk[it] = *reinterpret_cast<const uint4 *>(rec + (ch * P + ((key0 + key) & (P - 1))) * kElem);
+      rk[it] = *reinterpret_cast<const u32x4_t *>(rec + (ch * P + ((key0 + key) & (P - 1))) * kElem);
       const int vc = e / D, d = e % D;
       rec = c.v + (size_t)max(ids[vc / 2], 0) * page_bytes + head_off;
-      rv[it] = *reinterpret_cast<const uint4 *>(
+      rv[it] = *reinterpret_cast<const u32x4_t *>(
           rec + ((((key0 + 8 * vc) & (P - 1)) >> 3) * D + d) * kElem);
     }
     if constexpr (FMT == Q8_KV_Q8_0) {
@@ -230,13 +200,38 @@ attn_rows_kernel(AttnArgs a) {
       }
     }
   };
-  auto stage = [&](char *st) {
+  // Whether every column sees all of stage u.
+  auto whole = [&](int u, int base) {
+    const int key0 = sp.tile(u) * KT;
+    const int *ids = pids + (u - base) * (KT / 16);
+    int pages = ids[0];
+#pragma unroll
+    for (int g = 1; g < KT / 16; ++g) pages |= ids[g];
+    return (key0 + KT - 1 <= p0) & (uni(pages) >= 0) &
+           ((a.window <= 0) | (key0 > p1 - a.window) | (key0 + KT <= a.sinks));
+  };
+  // Registers -> LDS.  In a stage that is not whole (bf16), values of tokens
+  // past the sequence or on no page, whose bytes may be anything, become zero,
+  // and the return says whether a value of the others is infinite or NaN.
+  auto stage = [&](char *st, int u, int base, bool all) {
+    bool odd = false;
+    if (FMT == Q8_KV_BF16 && !all) {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const int vc = ((int)threadIdx.x + it * kThreads) / D;
+        const int left = pids[(u - base) * (KT / 16) + vc / 2] < 0 ? 0 : len - sp.tile(u) * KT - 8 * vc;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          rv[it][e] &= (left > 2 * e ? 0xffffu : 0u) | (left > 2 * e + 1 ? 0xffff0000u : 0u);
+        odd |= not_finite(rv[it]);
+      }
+    }
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
       char *d = st + ((int)threadIdx.x + it * kThreads) * kPer * 16;
       if constexpr (FMT == Q8_KV_BF16) {
-        *reinterpret_cast<uint4 *>(d) = rk[it];
-        *reinterpret_cast<uint4 *>(d + kVal) = rv[it];
+        *reinterpret_cast<u32x4_t *>(d) = rk[it];
+        *reinterpret_cast<u32x4_t *>(d + kVal) = rv[it];
       } else {
         *reinterpret_cast<bf16x8_t *>(d) = i8x8_to_bf16(make_uint2(rk[it].x, rk[it].y));
         *reinterpret_cast<bf16x8_t *>(d + 16) = i8x8_to_bf16(make_uint2(rk[it].z, rk[it].w));
@@ -255,11 +250,12 @@ attn_rows_kernel(AttnArgs a) {
         }
       }
     }
+    return odd;
   };
   // row `col` of a key fragment is this key of its 32
   const int fkey = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
 
-  auto compute = [&](const char *st, int u, int base) {
+  auto compute = [&](const char *st, int u, int base, bool all, bool odd, char *scratch) {
     const int key0 = sp.tile(u) * KT;
     const char *kb = st, *vb = st + kVal;
     const float *ksc = reinterpret_cast<const float *>(st + 2 * kVal), *vsc = ksc + kScales;
@@ -298,11 +294,6 @@ attn_rows_kernel(AttnArgs a) {
     }
     // seen[n] bit e: key 32n + 16 (e/8) + 8 hf + e%8 is
     const int *ids = pids + (u - base) * (KT / 16);
-    int pages = ids[0];
-#pragma unroll
-    for (int g = 1; g < KT / 16; ++g) pages |= ids[g];
-    const bool all = ((key0 + KT - 1 <= p0) & (__builtin_amdgcn_readfirstlane(pages) >= 0) &
-                      ((a.window <= 0) | (key0 > p1 - a.window) | (key0 + KT <= a.sinks)));
     unsigned seen[NS];
 #pragma unroll
     for (int n = 0; n < NS; ++n) seen[n] = 0xffffu;
@@ -339,7 +330,7 @@ attn_rows_kernel(AttnArgs a) {
     for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[n][e] = exp2_fast(fmaf(x[n][e], scale, -m));
-    if (!all) {
+    if (!all) {                          // also where the scale is zero
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -352,6 +343,35 @@ attn_rows_kernel(AttnArgs a) {
       for (int e = 0; e < 16; ++e) ps[e & 3] += x[n][e];
     l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
 
+    if (FMT == Q8_KV_BF16 && odd) {
+      // Some value is infinite or NaN and not every column sees every token: the
+      // matrix product would carry it, times zero, into columns that do not.
+      // Token by token instead, each column adding those it sees.
+      uint16_t *mine = reinterpret_cast<uint16_t *>(scratch) + wave * KT * 32;
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          mine[(32 * n + 16 * (e >> 3) + 8 * hf + (e & 7)) * 32 + col] =
+              seen[n] >> e & 1 ? __builtin_bit_cast(uint16_t, (__bf16)x[n][e]) : 0xffffu;
+      __syncthreads();
+      const uint16_t *vals = reinterpret_cast<const uint16_t *>(vb);
+#pragma unroll 1
+      for (int k = 0; k < KT; ++k) {
+        const uint16_t bits = mine[k * 32 + col];
+        const float p = __uint_as_float((uint32_t)bits << 16);
+#pragma unroll
+        for (int T = 0; T < NB; ++T)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int d = 32 * T + 8 * (e >> 2) + 4 * hf + (e & 3);
+            const float v = __uint_as_float((uint32_t)vals[((k >> 3) * D + d) * 8 + (k & 7)] << 16);
+            o[T][e] = bits != 0xffffu ? fmaf(p, v, o[T][e]) : o[T][e];
+          }
+      }
+      __syncthreads();
+      return;
+    }
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       if constexpr (FMT == Q8_KV_BF16) {
@@ -359,23 +379,13 @@ attn_rows_kernel(AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) p[e] = x[n][e];
         const bf16x8_t pb[2] = {to_bf16x8(p), to_bf16x8(p + 8)};
-        if (all) {
 #pragma unroll
-          for (int T = 0; T < NB; ++T)
+        for (int T = 0; T < NB; ++T)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t + hf) * D + 32 * T + col) * 16);
-              o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[t], o[T], 0, 0, 0);
-            }
-        } else {
-#pragma unroll
-          for (int T = 0; T < NB; ++T)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              uint4 f = *reinterpret_cast<const uint4 *>(vb + ((4 * n + 2 * t + hf) * D + 32 * T + col) * 16);
-              add_values_masked(o[T], f, pb[t], seen[n] >> (8 * t));
-            }
-        }
+          for (int t = 0; t < 2; ++t) {
+            const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t + hf) * D + 32 * T + col) * 16);
+            o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[t], o[T], 0, 0, 0);
+          }
       } else {
 #pragma unroll
         for (int T = 0; T < NB; ++T) {
@@ -413,15 +423,18 @@ attn_rows_kernel(AttnArgs a) {
     }
     __syncthreads();
     fetch(base, base);
-    stage(lds);
-    __syncthreads();
+    bool all = whole(base, base);
+    bool odd = stage(lds, base, base, all);
+    odd = __syncthreads_or(odd);
     int cur = 0;
     for (int u = base; u < end; ++u) {
-      fetch(min(u + 1, end - 1), base);
-      compute(lds + cur * kStage, u, base);
+      const int next = min(u + 1, end - 1);
+      fetch(next, base);
+      compute(lds + cur * kStage, u, base, all, odd, lds + (cur ^ 1) * kStage);
       cur ^= 1;
-      stage(lds + cur * kStage);
-      __syncthreads();
+      all = whole(next, base);
+      odd = stage(lds + cur * kStage, next, base, all);
+      if (FMT == Q8_KV_BF16 && !all) odd = __syncthreads_or(odd); else __syncthreads();
     }
   }
   l += __shfl_xor(l, 32);
