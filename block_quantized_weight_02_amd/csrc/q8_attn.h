@@ -17,6 +17,13 @@ constexpr float kLowest = -3.0e38f;   // below every score's running maximum, an
 // A value all lanes hold alike, in a scalar register.
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// A value made opaque where it is used: what is computed from it stays there
+// rather than being kept in registers across the token stream.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // The tiles of KT tokens that rows at positions p0 .. p1 of a sequence
 // see: tiles 0 .. a-1 (the first tokens kept under a window), then t0 .. up to
 // p1's.  Tile u of the nt is tile u (u < a) or u - a + t0.

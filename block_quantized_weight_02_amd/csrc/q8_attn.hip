@@ -263,15 +263,6 @@ __device__ __forceinline__ int scan_wave(int v) {   // inclusive sum over the la
   return v;
 }
 
-// The thread's index, opaque: what is computed from it stays where it is used
-// (once a sequence or list) rather than being kept in registers across the
-// token stream.
-__device__ __forceinline__ int thread_here() {
-  int t = threadIdx.x;
-  asm volatile("" : "+v"(t));
-  return t;
-}
-
 // Floats of one partial result: up to 16 heads' sums, then their maxima and
 // denominators.
 __host__ __device__ constexpr int record_floats(int heads, int dim) {
@@ -324,7 +315,7 @@ attn_decode_kernel(AttnArgs a) {
   // in (w0; before: the tiles of those before them).  list_seqs writes 64
   // sequences' lengths and first tiles.
   auto list_seqs = [&](int w0, int before) {
-    const int l = thread_here();
+    const int l = here(threadIdx.x);
     const int len = len_of(a, w0 + l);
     const int incl = scan_wave(tiles_of(a, len));
     if (wave == 0) {
@@ -381,7 +372,7 @@ attn_decode_kernel(AttnArgs a) {
     for (int k0 = wave * 64; k0 < te - tb; k0 += kThreads) {
       // a tile's sequence is the last that starts at or before it: the wave finds
       // that of its first tile, its other tiles are in that one or soon after
-      const int l = thread_here() & 63, k = k0 + l;
+      const int l = here(threadIdx.x) & 63, k = k0 + l;
       int lo = __popcll(__ballot(pre[l + 1] <= tb + k0));
       if (k >= te - tb) continue;
       while (pre[lo + 1] <= tb + k) ++lo;
@@ -467,7 +458,7 @@ attn_decode_kernel(AttnArgs a) {
       // this piece's slot x + i is its own: each step along the tiles moves on
       // x or i
       const buf_t out = make_buf(a.partial + ((size_t)(x + i) * units + unit) * rec, rec * 4);
-      for (int idx = thread_here(); idx < heads * per_head; idx += kThreads) {
+      for (int idx = here(threadIdx.x); idx < heads * per_head; idx += kThreads) {
         const int h = idx / per_head, d = (idx % per_head) * 4;
         float M = red_m[0][h], L = 0.0f;
 #pragma unroll
@@ -509,7 +500,7 @@ attn_decode_kernel(AttnArgs a) {
       const unsigned step = (unsigned)(stride * 4);
       const int items = heads * per_head;
       const int groups = max(1, min(kThreads / items, kWaves));
-      for (int idx = thread_here(); idx < items * groups; idx += kThreads) {
+      for (int idx = here(threadIdx.x); idx < items * groups; idx += kThreads) {
         const int g = idx / items, h = idx % items / per_head, d = (idx % per_head) * 4;
         const unsigned at = (h * D + d) * 4, mat = (rec - 2 * kHeadTile + h) * 4;
         const int g0 = segs * g / groups, g1 = segs * (g + 1) / groups;
@@ -553,7 +544,7 @@ attn_decode_kernel(AttnArgs a) {
       }
       if (groups > 1) {
         __syncthreads();
-        for (int idx = thread_here(); idx < items; idx += kThreads) {
+        for (int idx = here(threadIdx.x); idx < items; idx += kThreads) {
           const int h = idx / per_head, d = (idx % per_head) * 4;
           float M = kLowest, L = 0.0f;
           for (int g = 0; g < groups; ++g) M = fmaxf(M, red_m[g][h]);

@@ -2,6 +2,8 @@
 // (q8_attn_rows; the formula and layouts are in include/q8gemv.h).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "q8_attn.h"
 
 namespace q8 {
@@ -16,14 +18,28 @@ constexpr int kMinSplitTiles = 8;       // fewest tiles of a split that computes
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 
 // Keys of a stage: what the workgroup loads, and waits for, at a time.
-template <int D> constexpr int kStageKeys = D == 256 ? 32 : 64;
+#ifndef SPV
+#define SPV 0
+#endif
+#if SPV == 0
+#define SCHED_PV ;
+#elif SPV == 1
+#define SCHED_PV read_ahead<NS * NB * 2, 4>();
+#else
+#define SCHED_PV interleave<NS, NB>();
+#endif
+#ifndef KTB
+#define KTB 64
+#define OCC 2
+#endif
+template <int D, int FMT> constexpr int kStageKeys = D == 256 ? 32 : (FMT == Q8_KV_BF16 ? KTB : 64);
 constexpr int kListGroups = 512;        // 16-token groups whose pages are held in LDS at a time
 
 // LDS bytes of one stage: keys and values as bf16 (Q8_0: the codes, exact),
 // and their scales.
 template <int D, int FMT>
 constexpr int stage_bytes() {
-  return kStageKeys<D> * (2 * D * 2 + (FMT == Q8_KV_Q8_0 ? 2 * (D / 32) * 4 : 0));
+  return kStageKeys<D, FMT> * (2 * D * 2 + (FMT == Q8_KV_Q8_0 ? 2 * (D / 32) * 4 : 0));
 }
 
 struct Block {
@@ -65,6 +81,31 @@ __device__ __forceinline__ Block find_block(const AttnArgs &a, int x) {
   return r;
 }
 
+// Schedules a block of N fragment reads and N matrix products: `ahead` reads
+// first, then one more with each product.
+template <int N, int AHEAD>
+__device__ __forceinline__ void read_ahead() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < N - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
+}
+
+template <int NS, int NB>
+__device__ __forceinline__ void interleave() {
+  __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+  __builtin_amdgcn_sched_group_barrier(0x2, 56, 0);
+#pragma unroll
+  for (int i = 0; i < NS * NB * 2; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    if (i < NS * NB * 2 - 4) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (i < (NS - 1) * NB * 2) __builtin_amdgcn_sched_group_barrier(0x2, 56 / (NB * 2), 0);
+  }
+}
+
 __device__ __forceinline__ float swap_halves(float x) {   // lane l's value in lane l ^ 32
   return __shfl_xor(x, 32);
 }
@@ -76,6 +117,16 @@ __device__ __forceinline__ bool not_finite(u32x4_t v) {
   for (int e = 0; e < 4; ++e) odd |= (v[e] & 0x7fff7fffu) + 0x00800080u;
   return (odd & 0x80008000u) != 0;
 }
+
+// 16 bytes a lane from memory into LDS at `at` (a scalar) plus 16 times the
+// lane, without registers in between; loads_done waits for them.  They are
+// written out because the compiler would make every read of LDS wait for every
+// such load, the next stage's too.
+__device__ __forceinline__ void load_to_lds(const void *p, unsigned at) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(p), "s"(at) : "memory");
+}
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __host__ __device__ constexpr int record_floats(int dim) { return kCols * dim + 2 * kCols; }
 
@@ -95,9 +146,9 @@ __host__ __device__ constexpr int record_floats(int dim) { return kCols * dim + 
 constexpr float kSlack = 8.0f;
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(64 * kWaves, D == 256 ? 1 : FMT == Q8_KV_BF16 ? OCC : 2)
 attn_rows_kernel(AttnArgs a) {
-  constexpr int NB = D / 32, NK = D / 16, KT = kStageKeys<D>, NS = KT / 32;
+  constexpr int NB = D / 32, NK = D / 16, KT = kStageKeys<D, FMT>, NS = KT / 32;
   constexpr int kThreads = 64 * kWaves;
   constexpr int kStage = stage_bytes<D, FMT>();
   constexpr int kVal = KT * D * 2;                         // bytes of the staged keys
@@ -107,6 +158,7 @@ attn_rows_kernel(AttnArgs a) {
   static_assert(kIt * kThreads * kPer * 8 == KT * D, "pieces");
   constexpr int kScales = KT * NB;                         // scales of the keys
   constexpr int kSIt = (kScales + kThreads - 1) / kThreads;
+  static_assert(kScales % kThreads == 0 || kSIt == 1, "scales");
   extern __shared__ __align__(16) char lds[];
   __shared__ int pids[kListGroups];
   __shared__ int is_last;
@@ -141,19 +193,22 @@ attn_rows_kernel(AttnArgs a) {
   const int j = min(mycol, ncol - 1) / a.group, head = hk * a.group + min(mycol, ncol - 1) % a.group;
   const int pos = len - R + j, row = start + j;
 
-  // a negative scale goes into the queries' signs
-  const float scale = fabsf(a.scale_log2);
+  // The scale is used as a positive one (so that the largest score stays the
+  // largest, and an unseen key's -infinity is one): its sign goes into the
+  // queries, and a scale of zero makes them zero.
+  const float scale = a.scale_log2 == 0.0f ? 1.0f : fabsf(a.scale_log2);
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+  const uint32_t keep = a.scale_log2 == 0.0f ? 0u : 0xffffffffu;
   bf16x8_t q[NK];
 #pragma unroll
   for (int k = 0; k < NK; ++k) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (live)
       v = *reinterpret_cast<const uint4 *>(a.q + ((size_t)row * a.q_heads + head) * D + 16 * k + 8 * hf);
-    v.x ^= flip;
-    v.y ^= flip;
-    v.z ^= flip;
-    v.w ^= flip;
+    v.x = (v.x ^ flip) & keep;
+    v.y = (v.y ^ flip) & keep;
+    v.z = (v.z ^ flip) & keep;
+    v.w = (v.w ^ flip) & keep;
     q[k] = __builtin_bit_cast(bf16x8_t, v);
   }
 
@@ -169,34 +224,77 @@ attn_rows_kernel(AttnArgs a) {
   const size_t head_off = (size_t)hk * c.record();
   const size_t page_bytes = c.page_bytes();
 
-  // The thread's 16-byte pieces of a stage, cache -> registers.  Keys lie as
-  // [D/8][KT][8], values as [KT/8][D][8], in the cache's pages and in LDS; a
-  // piece is one eight of bf16 values or two of int8 codes.
-  u32x4_t rk[kIt], rv[kIt];
-  float rks[kSIt], rvs[kSIt];
-  auto fetch = [&](int u, int base) {
+  // A stage's 16-byte pieces, thread by thread.  Keys lie as [D/8][KT][8],
+  // values as [KT/8][D][8], in the cache's pages and in LDS; a piece is one
+  // eight of bf16 values or two of int8 codes.  All of a thread's key pieces are
+  // of one key (or pair); a wave's 64 value pieces follow each other within 16
+  // tokens, so their page is a scalar.
+  static_assert(kThreads * kPer % KT == 0 && (64 * kPer <= D || 64 * kPer % D == 0), "pieces");
+  const int tkey = (int)threadIdx.x * kPer % KT, tch = (int)threadIdx.x * kPer / KT;
+  auto key_piece = [&](int u, int base) {
     const int *ids = pids + (u - base) * (KT / 16);
-    const int key0 = sp.tile(u) * KT;
+    return c.k + (size_t)max(ids[tkey / 16], 0) * page_bytes + head_off +
+           (tch * P + ((sp.tile(u) * KT + tkey) & (P - 1))) * kElem;
+  };
+  const int key_step = kThreads * kPer / KT * P * kElem;
+  auto value_piece = [&](int u, int base, int it) {
+    const int *ids = pids + (u - base) * (KT / 16);
+    const int e = (wave * 64 + it * kThreads) * kPer, vc = e / D;
+    return c.v + (size_t)max(uni(ids[vc / 2]), 0) * page_bytes + head_off +
+           ((((sp.tile(u) * KT + 8 * vc) & (P - 1)) >> 3) * D + e % D) * kElem + lane * 16;
+  };
+  // bf16: straight into LDS.
+  const unsigned lds0 = (unsigned)(size_t)(__attribute__((address_space(3))) char *)lds + wave * 1024;
+  auto issue = [&](int u, int base, int buf) {
+    const char *kp = key_piece(u, base);
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
-      const int e = ((int)threadIdx.x + it * kThreads) * kPer;
-      const int key = e % KT, ch = e / KT;
-      const char *rec = c.k + (size_t)max(ids[key / 16], 0) * page_bytes + head_off;
-      rk[it] = *reinterpret_cast<const u32x4_t *>(rec + (ch * P + ((key0 + key) & (P - 1))) * kElem);
-      const int vc = e / D, d = e % D;
-      rec = c.v + (size_t)max(ids[vc / 2], 0) * page_bytes + head_off;
-      rv[it] = *reinterpret_cast<const u32x4_t *>(
-          rec + ((((key0 + 8 * vc) & (P - 1)) >> 3) * D + d) * kElem);
+      load_to_lds(kp, lds0 + buf * kStage + it * kThreads * 16);
+      kp += key_step;
     }
-    if constexpr (FMT == Q8_KV_Q8_0) {
 #pragma unroll
-      for (int it = 0; it < kSIt; ++it) {
-        const int p = min((int)threadIdx.x + it * kThreads, kScales - 1);
-        const int key = p % KT, b = p / KT;
-        const size_t at = (size_t)max(ids[key / 16], 0) * page_bytes + head_off + (size_t)D * P +
-                          (b * P + ((key0 + key) & (P - 1))) * 4;
-        rks[it] = *reinterpret_cast<const float *>(c.k + at);
-        rvs[it] = *reinterpret_cast<const float *>(c.v + at);
+    for (int it = 0; it < kIt; ++it)
+      load_to_lds(value_piece(u, base, it), lds0 + buf * kStage + kVal + it * kThreads * 16);
+  };
+  // Q8_0: through registers, where the codes are widened.
+  u32x4_t rk[kIt], rv[kIt];
+  float rks[kSIt], rvs[kSIt];
+  const int skey = (int)threadIdx.x % KT, sblk = (int)threadIdx.x / KT;
+  auto fetch = [&](int u, int base) {
+    const char *kp = key_piece(u, base);
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      rk[it] = *reinterpret_cast<const u32x4_t *>(kp);
+      kp += key_step;
+    }
+#pragma unroll
+    for (int it = 0; it < kIt; ++it)
+      rv[it] = *reinterpret_cast<const u32x4_t *>(value_piece(u, base, it));
+    const int *ids = pids + (u - base) * (KT / 16);
+    const size_t at = (size_t)max(ids[skey / 16], 0) * page_bytes + head_off + (size_t)D * P +
+                      (min(sblk, NB - 1) * P + ((sp.tile(u) * KT + skey) & (P - 1))) * 4;
+#pragma unroll
+    for (int it = 0; it < kSIt; ++it) {
+      rks[it] = *reinterpret_cast<const float *>(c.k + at + it * (kThreads / KT) * P * 4);
+      rvs[it] = *reinterpret_cast<const float *>(c.v + at + it * (kThreads / KT) * P * 4);
+    }
+  };
+  auto stage = [&](char *st) {
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) {
+      char *d = st + ((int)threadIdx.x + it * kThreads) * kPer * 16;
+      *reinterpret_cast<bf16x8_t *>(d) = i8x8_to_bf16(make_uint2(rk[it][0], rk[it][1]));
+      *reinterpret_cast<bf16x8_t *>(d + 16) = i8x8_to_bf16(make_uint2(rk[it][2], rk[it][3]));
+      *reinterpret_cast<bf16x8_t *>(d + kVal) = i8x8_to_bf16(make_uint2(rv[it][0], rv[it][1]));
+      *reinterpret_cast<bf16x8_t *>(d + kVal + 16) = i8x8_to_bf16(make_uint2(rv[it][2], rv[it][3]));
+    }
+    float *sc = reinterpret_cast<float *>(st + 2 * kVal);
+#pragma unroll
+    for (int it = 0; it < kSIt; ++it) {
+      const int p = (int)threadIdx.x + it * kThreads;
+      if (kScales % kThreads == 0 || p < kScales) {
+        sc[p] = rks[it];
+        sc[kScales + p] = rvs[it];
       }
     }
   };
@@ -210,67 +308,51 @@ attn_rows_kernel(AttnArgs a) {
     return (key0 + KT - 1 <= p0) & (uni(pages) >= 0) &
            ((a.window <= 0) | (key0 > p1 - a.window) | (key0 + KT <= a.sinks));
   };
-  // Registers -> LDS.  In a stage that is not whole (bf16), values of tokens
-  // past the sequence or on no page, whose bytes may be anything, become zero,
-  // and the return says whether a value of the others is infinite or NaN.
-  auto stage = [&](char *st, int u, int base, bool all) {
+  // bf16, a stage that is not whole: the thread's pieces of values of tokens
+  // past the sequence or on no page, whose bytes may be anything, become zero.
+  // Returns whether a value of the others is infinite or NaN.
+  auto clean = [&](char *st, int u, int base) {
     bool odd = false;
-    if (FMT == Q8_KV_BF16 && !all) {
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const int vc = ((int)threadIdx.x + it * kThreads) / D;
-        const int left = pids[(u - base) * (KT / 16) + vc / 2] < 0 ? 0 : len - sp.tile(u) * KT - 8 * vc;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          rv[it][e] &= (left > 2 * e ? 0xffffu : 0u) | (left > 2 * e + 1 ? 0xffff0000u : 0u);
-        odd |= not_finite(rv[it]);
-      }
-    }
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
-      char *d = st + ((int)threadIdx.x + it * kThreads) * kPer * 16;
-      if constexpr (FMT == Q8_KV_BF16) {
-        *reinterpret_cast<u32x4_t *>(d) = rk[it];
-        *reinterpret_cast<u32x4_t *>(d + kVal) = rv[it];
-      } else {
-        *reinterpret_cast<bf16x8_t *>(d) = i8x8_to_bf16(make_uint2(rk[it].x, rk[it].y));
-        *reinterpret_cast<bf16x8_t *>(d + 16) = i8x8_to_bf16(make_uint2(rk[it].z, rk[it].w));
-        *reinterpret_cast<bf16x8_t *>(d + kVal) = i8x8_to_bf16(make_uint2(rv[it].x, rv[it].y));
-        *reinterpret_cast<bf16x8_t *>(d + kVal + 16) = i8x8_to_bf16(make_uint2(rv[it].z, rv[it].w));
-      }
-    }
-    if constexpr (FMT == Q8_KV_Q8_0) {
-      float *sc = reinterpret_cast<float *>(st + 2 * kVal);
+      const int piece = here(threadIdx.x) + it * kThreads, vc = piece / D;
+      const int left = pids[(u - base) * (KT / 16) + vc / 2] < 0 ? 0 : len - sp.tile(u) * KT - 8 * vc;
+      u32x4_t *p = reinterpret_cast<u32x4_t *>(st + kVal + piece * 16);
+      u32x4_t v = *p;
 #pragma unroll
-      for (int it = 0; it < kSIt; ++it) {
-        const int p = (int)threadIdx.x + it * kThreads;
-        if (kScales % kThreads == 0 || p < kScales) {
-          sc[p] = rks[it];
-          sc[kScales + p] = rvs[it];
-        }
-      }
+      for (int e = 0; e < 4; ++e)
+        v[e] &= (left > 2 * e ? 0xffffu : 0u) | (left > 2 * e + 1 ? 0xffff0000u : 0u);
+      odd |= not_finite(v);
+      if (left < 8) *p = v;
     }
     return odd;
   };
   // row `col` of a key fragment is this key of its 32
   const int fkey = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
 
-  auto compute = [&](const char *st, int u, int base, bool all, bool odd, char *scratch) {
+  // One stage.  ODD (bf16): some value is infinite or NaN and not every column
+  // sees every token.
+  auto compute = [&](auto ODD, const char *st, int u, int base, bool all, char *scratch) {
     const int key0 = sp.tile(u) * KT;
-    const char *kb = st, *vb = st + kVal;
-    const float *ksc = reinterpret_cast<const float *>(st + 2 * kVal), *vsc = ksc + kScales;
+    const char *kb = st + (hf * KT + fkey) * 16, *vb = st + kVal + (hf * D + col) * 16;
+    const float *ksc = reinterpret_cast<const float *>(st + 2 * kVal) + 8 * hf, *vsc = ksc + kScales;
     f32x16_t x[NS];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[n][e] = 0.0f;
-      if constexpr (FMT == Q8_KV_BF16) {
+    if constexpr (FMT == Q8_KV_BF16) {
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(kb + ((2 * k + hf) * KT + 32 * n + fkey) * 16);
+      for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(kb + (2 * k * KT + 32 * n) * 16);
           x[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k], x[n], 0, 0, 0);
         }
-      } else {
+      read_ahead<NK * NS, 4>();
+    } else {
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           f32x16_t z;
@@ -278,34 +360,33 @@ attn_rows_kernel(AttnArgs a) {
           for (int e = 0; e < 16; ++e) z[e] = 0.0f;
 #pragma unroll
           for (int k = 2 * b; k < 2 * b + 2; ++k) {
-            const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(kb + ((2 * k + hf) * KT + 32 * n + fkey) * 16);
+            const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(kb + (2 * k * KT + 32 * n) * 16);
             z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k], z, 0, 0, 0);
           }
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const float4 w = *reinterpret_cast<const float4 *>(ksc + b * KT + 32 * n + 16 * (g >> 1) + 8 * hf + 4 * (g & 1));
+            const float4 w = *reinterpret_cast<const float4 *>(ksc + b * KT + 32 * n + 16 * (g >> 1) + 4 * (g & 1));
             x[n][4 * g] = fmaf(w.x, z[4 * g], x[n][4 * g]);
             x[n][4 * g + 1] = fmaf(w.y, z[4 * g + 1], x[n][4 * g + 1]);
             x[n][4 * g + 2] = fmaf(w.z, z[4 * g + 2], x[n][4 * g + 2]);
             x[n][4 * g + 3] = fmaf(w.w, z[4 * g + 3], x[n][4 * g + 3]);
           }
         }
-      }
     }
     // seen[n] bit e: key 32n + 16 (e/8) + 8 hf + e%8 is
-    const int *ids = pids + (u - base) * (KT / 16);
     unsigned seen[NS];
 #pragma unroll
     for (int n = 0; n < NS; ++n) seen[n] = 0xffffu;
     if (!all) {
-      const int from = a.window > 0 ? pos - a.window + 1 : 0;
+      const int *ids = pids + (u - base) * (KT / 16);
+      const int h8 = here(8 * hf), me = here(pos), from = a.window > 0 ? me - a.window + 1 : 0;
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         seen[n] = 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int key = key0 + 32 * n + 16 * (e >> 3) + 8 * hf + (e & 7);
-          const int stop = ids[2 * n + (e >> 3)] >= 0 ? min(pos, len - 1) : -1;
+          const int key = key0 + 32 * n + 16 * (e >> 3) + h8 + (e & 7);
+          const int stop = ids[2 * n + (e >> 3)] >= 0 ? min(me, len - 1) : -1;
           const bool in = (key <= stop) & ((key >= from) | (key < a.sinks));
           seen[n] |= in ? 1u << e : 0u;
           x[n][e] = in ? x[n][e] : -__builtin_inff();
@@ -326,90 +407,85 @@ attn_rows_kernel(AttnArgs a) {
 #pragma unroll
       for (int T = 0; T < NB; ++T) o[T] *= alpha;
     }
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[n][e] = exp2_fast(fmaf(x[n][e], scale, -m));
-    if (!all) {                          // also where the scale is zero
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[n][e] = seen[n] >> e & 1 ? x[n][e] : 0.0f;
-    }
     float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) ps[e & 3] += x[n][e];
-    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-
-    if (FMT == Q8_KV_BF16 && odd) {
-      // Some value is infinite or NaN and not every column sees every token: the
-      // matrix product would carry it, times zero, into columns that do not.
-      // Token by token instead, each column adding those it sees.
+    if constexpr (ODD) {
+      // The matrix product would carry such a value, times zero, into columns
+      // that do not see it.  Token by token instead, each column adding those
+      // it sees.
       uint16_t *mine = reinterpret_cast<uint16_t *>(scratch) + wave * KT * 32;
+      const int half = here(hf), at = here(col);
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          mine[(32 * n + 16 * (e >> 3) + 8 * hf + (e & 7)) * 32 + col] =
-              seen[n] >> e & 1 ? __builtin_bit_cast(uint16_t, (__bf16)x[n][e]) : 0xffffu;
+        for (int e = 0; e < 16; ++e) {
+          const float p = exp2_fast(fmaf(x[n][e], scale, -m));
+          ps[e & 3] += p;
+          mine[(32 * n + 16 * (e >> 3) + 8 * half + (e & 7)) * 32 + at] =
+              seen[n] >> e & 1 ? __builtin_bit_cast(uint16_t, (__bf16)p) : 0xffffu;
+        }
       __syncthreads();
-      const uint16_t *vals = reinterpret_cast<const uint16_t *>(vb);
+      const uint16_t *vals = reinterpret_cast<const uint16_t *>(st + kVal);
 #pragma unroll 1
       for (int k = 0; k < KT; ++k) {
-        const uint16_t bits = mine[k * 32 + col];
+        const uint16_t bits = mine[k * 32 + at];
         const float p = __uint_as_float((uint32_t)bits << 16);
 #pragma unroll
-        for (int T = 0; T < NB; ++T)
+        for (int T = 0; T < NB; ++T) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int d = 32 * T + 8 * (e >> 2) + 4 * hf + (e & 3);
+            const int d = 32 * T + 8 * (e >> 2) + 4 * half + (e & 3);
             const float v = __uint_as_float((uint32_t)vals[((k >> 3) * D + d) * 8 + (k & 7)] << 16);
             o[T][e] = bits != 0xffffu ? fmaf(p, v, o[T][e]) : o[T][e];
           }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
       __syncthreads();
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      if constexpr (FMT == Q8_KV_BF16) {
+      for (int n = 0; n < NS; ++n) {
         float p[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p[e] = x[n][e];
-        const bf16x8_t pb[2] = {to_bf16x8(p), to_bf16x8(p + 8)};
+        for (int e = 0; e < 16; ++e) {
+          p[e] = exp2_fast(fmaf(x[n][e], scale, -m));
+          ps[e & 3] += p[e];
+        }
+        if constexpr (FMT == Q8_KV_BF16) {
+          const bf16x8_t pb[2] = {to_bf16x8(p), to_bf16x8(p + 8)};
 #pragma unroll
-        for (int T = 0; T < NB; ++T)
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t + hf) * D + 32 * T + col) * 16);
-            o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[t], o[T], 0, 0, 0);
-          }
-      } else {
+            for (int T = 0; T < NB; ++T) {
+              const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t) * D + 32 * T) * 16);
+              o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[t], o[T], 0, 0, 0);
+            }
+        } else {
 #pragma unroll
-        for (int T = 0; T < NB; ++T) {
-          float p[16];
+          for (int T = 0; T < NB; ++T) {
+            float w[16];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const float4 w = *reinterpret_cast<const float4 *>(vsc + T * KT + 32 * n + 16 * (g >> 1) + 8 * hf + 4 * (g & 1));
-            p[4 * g] = x[n][4 * g] * w.x;
-            p[4 * g + 1] = x[n][4 * g + 1] * w.y;
-            p[4 * g + 2] = x[n][4 * g + 2] * w.z;
-            p[4 * g + 3] = x[n][4 * g + 3] * w.w;
-          }
-          if (!all) {
+            for (int g = 0; g < 4; ++g) {
+              const float4 s4 = *reinterpret_cast<const float4 *>(vsc + T * KT + 32 * n + 16 * (g >> 1) + 4 * (g & 1));
+              w[4 * g] = p[4 * g] * s4.x;
+              w[4 * g + 1] = p[4 * g + 1] * s4.y;
+              w[4 * g + 2] = p[4 * g + 2] * s4.z;
+              w[4 * g + 3] = p[4 * g + 3] * s4.w;
+            }
+            if (!all) {                  // an unseen token's scale may be anything
 #pragma unroll
-            for (int e = 0; e < 16; ++e) p[e] = seen[n] >> e & 1 ? p[e] : 0.0f;
-          }
+              for (int e = 0; e < 16; ++e) w[e] = seen[n] >> e & 1 ? w[e] : 0.0f;
+            }
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t + hf) * D + 32 * T + col) * 16);
-            o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, to_bf16x8(p + 8 * t), o[T], 0, 0, 0);
+            for (int t = 0; t < 2; ++t) {
+              const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t) * D + 32 * T) * 16);
+              o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, to_bf16x8(w + 8 * t), o[T], 0, 0, 0);
+            }
           }
         }
       }
+      if constexpr (FMT == Q8_KV_BF16) SCHED_PV
     }
+    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
   };
 
   constexpr int kListStages = kListGroups / (KT / 16);
@@ -422,19 +498,35 @@ attn_rows_kernel(AttnArgs a) {
       pids[g] = (unsigned)p < (unsigned)c.n_pages ? p : -1;
     }
     __syncthreads();
-    fetch(base, base);
-    bool all = whole(base, base);
-    bool odd = stage(lds, base, base, all);
-    odd = __syncthreads_or(odd);
-    int cur = 0;
-    for (int u = base; u < end; ++u) {
-      const int next = min(u + 1, end - 1);
-      fetch(next, base);
-      compute(lds + cur * kStage, u, base, all, odd, lds + (cur ^ 1) * kStage);
-      cur ^= 1;
-      all = whole(next, base);
-      odd = stage(lds + cur * kStage, next, base, all);
-      if (FMT == Q8_KV_BF16 && !all) odd = __syncthreads_or(odd); else __syncthreads();
+    if constexpr (FMT == Q8_KV_BF16) {
+      issue(base, base, 0);
+      for (int u = base; u < end; ++u) {
+        const int cur = (u - base) & 1;
+        char *st = lds + cur * kStage;
+        const bool all = whole(u, base);
+        loads_done();
+        __syncthreads();     // the stage is in LDS, and the last one has been computed
+        bool odd = false;
+        if (!all) odd = __syncthreads_or(clean(st, u, base));
+        if (!odd && u + 1 < end) issue(u + 1, base, cur ^ 1);
+        if (!odd) {
+          compute(std::false_type{}, st, u, base, all, nullptr);
+        } else {
+          compute(std::true_type{}, st, u, base, false, lds + (cur ^ 1) * kStage);
+          if (u + 1 < end) issue(u + 1, base, cur ^ 1);
+        }
+      }
+    } else {
+      fetch(base, base);
+      stage(lds);
+      __syncthreads();
+      for (int u = base; u < end; ++u) {
+        const int cur = (u - base) & 1;
+        fetch(min(u + 1, end - 1), base);
+        compute(std::false_type{}, lds + cur * kStage, u, base, whole(u, base), nullptr);
+        stage(lds + (cur ^ 1) * kStage);
+        __syncthreads();
+      }
     }
   }
   l += __shfl_xor(l, 32);
