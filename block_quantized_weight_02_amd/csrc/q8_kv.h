@@ -65,9 +65,10 @@ constexpr int kKvTile = 32;
 int attn_decode_chunks(int64_t n, int64_t units);
 size_t attn_decode_partial_bytes(int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim);
 // Key splits of a rows launch.
-int attn_rows_splits(int64_t m, int64_t n, int64_t q_heads, int64_t kv_heads);
+int attn_rows_splits(int64_t m, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim,
+                     int fmt);
 size_t attn_rows_partial_bytes(int64_t m, int64_t n, int64_t q_heads, int64_t kv_heads,
-                               int64_t dim);
+                               int64_t dim, int fmt);
 
 hipError_t launch_kv_step(const q8_kv_step_args &a, hipStream_t stream);
 hipError_t launch_rope_freqs(const q8_rope &r, double *freqs, hipStream_t stream);

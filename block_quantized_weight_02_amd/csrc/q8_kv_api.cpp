@@ -99,8 +99,9 @@ int done(hipError_t e, const char *what) {
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-size_t attn_ws_bytes(int64_t m, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim) {
-  const size_t p = m > 0 ? q8::attn_rows_partial_bytes(m, n, q_heads, kv_heads, dim)
+size_t attn_ws_bytes(int64_t m, int64_t n, int64_t q_heads, const q8_kv_cache *c) {
+  const int64_t kv_heads = c->kv_heads, dim = c->head_dim;
+  const size_t p = m > 0 ? q8::attn_rows_partial_bytes(m, n, q_heads, kv_heads, dim, c->fmt)
                          : q8::attn_decode_partial_bytes(n, q_heads, kv_heads, dim);
   return p ? kCounterBytes + (size_t)round_up((int64_t)p, 256) : 0;
 }
@@ -137,7 +138,7 @@ int run_attn(const uint16_t *q, int64_t m, int64_t q_heads, const q8_kv_cache *c
   if (!o && !o_q8) return report_error(Q8_ERR_NULL, "neither o nor o_q8 is given");
   if ((st = check_opt(o, "o")) || (st = check_opt(o_q8, "o_q8"))) return st;
   const int64_t M = rows ? m : n, K = q_heads * cache->head_dim;
-  const size_t need = attn_ws_bytes(rows ? m : 0, n, q_heads, cache->kv_heads, cache->head_dim);
+  const size_t need = attn_ws_bytes(rows ? m : 0, n, q_heads, cache);
   if (need) {
     if (!workspace || ws_bytes < need)
       return report_error(Q8_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed",
@@ -166,7 +167,7 @@ int run_attn(const uint16_t *q, int64_t m, int64_t q_heads, const q8_kv_cache *c
   }
   (void)hipGetLastError();  // clear a stale error so the launch's own is seen
   if (rows) {
-    a.chunks = q8::attn_rows_splits(m, n, q_heads, cache->kv_heads);
+    a.chunks = q8::attn_rows_splits(m, n, q_heads, cache->kv_heads, cache->head_dim, cache->fmt);
     return done(q8::launch_attn_rows(a, stream), "attn_rows launch");
   }
   const int64_t units = cache->kv_heads * ((a.group + 15) / 16);
@@ -293,7 +294,7 @@ int q8_kv_gather(const q8_kv_cache *cache, const int32_t *slots, int64_t rows, u
 
 size_t q8_attn_workspace_bytes(int64_t m, int64_t n, int64_t q_heads, const q8_kv_cache *cache) {
   if (m < 0 || check_attn_sizes(m, n, q_heads, cache, m > 0)) return 0;
-  return attn_ws_bytes(m, n, q_heads, cache->kv_heads, cache->head_dim);
+  return attn_ws_bytes(m, n, q_heads, cache);
 }
 
 int q8_attn_decode(const uint16_t *q, int64_t q_heads, const q8_kv_cache *cache,
