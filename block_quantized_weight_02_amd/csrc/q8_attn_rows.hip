@@ -35,6 +35,9 @@ template <int D> constexpr int kValBytes = kStageKeys<D> * D * 2;
 template <int D, int FMT>
 constexpr int kScaleBytes = FMT == Q8_KV_Q8_0 ? kStageKeys<D> * (D / 32) * 4 : 0;
 
+// Floats of a column's row of 64 dims in LDS, on its way out.
+constexpr int kOutRow = 68;
+
 struct Block {
   int i;         // sequence
   int block;     // its block of columns
@@ -69,19 +72,6 @@ __device__ __forceinline__ Block find_block(const AttnArgs &a, int x, int cols) 
   return Block{a.n, 0};
 }
 
-// Schedules a block of N fragment reads and N matrix products: AHEAD reads
-// first, then one more with each product.
-template <int N, int AHEAD>
-__device__ __forceinline__ void read_ahead() {
-  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
-#pragma unroll
-  for (int i = 0; i < N - AHEAD; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
-}
-
 __device__ __forceinline__ float swap_halves(float x) {   // lane l's value in lane l ^ 32
   typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
   const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -103,6 +93,12 @@ __device__ __forceinline__ bool not_finite(u32x4_t v) {
 __device__ __forceinline__ void load_to_lds(const void *p, unsigned at) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :: "v"(p), "s"(at) : "memory");
+}
+__device__ __forceinline__ void load_to_lds(const char *base, unsigned off, unsigned at) {
+  const uint64_t b = (uint64_t)base;     // one address for the wave, as a scalar
+  const uint64_t p = (uint64_t)(unsigned)uni((int)(b >> 32)) << 32 | (unsigned)uni((int)b);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(p), "s"(at) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void loads_done() {
@@ -153,6 +149,7 @@ attn_rows_kernel(AttnArgs a) {
   constexpr int kSIt = (kScales + kThreads - 1) / kThreads;
   static_assert(kScales % kThreads == 0 || kSIt == 1, "scales");
   constexpr int kListStages = kListGroups / (KT / 16);
+  constexpr bool kTurns = FMT == Q8_KV_BF16 && W == 8;
   extern __shared__ __align__(16) char lds[];              // keys, values, their scales: SL stages each
   __shared__ int pids[kListGroups];
   __shared__ int is_last;
@@ -224,26 +221,34 @@ attn_rows_kernel(AttnArgs a) {
            (tch * P + ((sp.tile(u) * KT + tkey) & (P - 1))) * kElem;
   };
   const int key_step = kThreads * kPer / KT * P * kElem;
-  auto value_piece = [&](int u, int it) Q8_INLINE {
+  auto value_piece = [&](int u, int it) Q8_INLINE {   // the wave's 64 pieces
     const int e = (wave * 64 + it * kThreads) * kPer, vc = e / D;
     return c.v + (size_t)max(uni(ids_of(u)[vc / 2]), 0) * page_bytes + head_off +
-           ((((sp.tile(u) * KT + 8 * vc) & (P - 1)) >> 3) * D + e % D) * kElem + lane * 16;
+           ((((sp.tile(u) * KT + 8 * vc) & (P - 1)) >> 3) * D + e % D) * kElem;
   };
   char *const vals = lds + SL * kVal, *const kscl = lds + 2 * SL * kVal, *const vscl = kscl + SL * kScl;
-  // bf16: straight into LDS, 2 kIt loads a stage.
+  // bf16: straight into LDS, 2 kIt loads a stage, from addresses that can be
+  // looked up a stage earlier.
+  struct Source {
+    const char *k, *v[kIt];
+  };
   const unsigned lds0 = (unsigned)(size_t)(__attribute__((address_space(3))) char *)lds + wave * 1024;
-  auto issue = [&](int u) Q8_INLINE {
+  auto source = [&](int u) Q8_INLINE {
+    Source from;
+    from.k = key_piece(u);
+#pragma unroll
+    for (int it = 0; it < kIt; ++it) from.v[it] = value_piece(u, it);
+    return from;
+  };
+  auto issue_from = [&](const Source &from, int u) Q8_INLINE {
     const unsigned at = lds0 + slot(u) * kVal;
-    const char *kp = key_piece(u);
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
-      load_to_lds(kp, at + it * kThreads * 16);
-      kp += key_step;
+      load_to_lds(from.k + (size_t)it * key_step, at + it * kThreads * 16);
+      load_to_lds(from.v[it], lane * 16, at + SL * kVal + it * kThreads * 16);
     }
-#pragma unroll
-    for (int it = 0; it < kIt; ++it)
-      load_to_lds(value_piece(u, it), at + SL * kVal + it * kThreads * 16);
   };
+  auto issue = [&](int u) Q8_INLINE { issue_from(source(u), u); };
   // Q8_0: through registers, where the codes are widened.
   u32x4_t rk[kIt], rv[kIt];
   float rks[kSIt], rvs[kSIt];
@@ -254,7 +259,7 @@ attn_rows_kernel(AttnArgs a) {
     for (int it = 0; it < kIt; ++it) {
       rk[it] = *reinterpret_cast<const u32x4_t *>(kp);
       kp += key_step;
-      rv[it] = *reinterpret_cast<const u32x4_t *>(value_piece(u, it));
+      rv[it] = *reinterpret_cast<const u32x4_t *>(value_piece(u, it) + lane * 16);
     }
     const size_t at = (size_t)max(ids_of(u)[skey / 16], 0) * page_bytes + head_off + (size_t)D * P +
                       (min(sblk, NB - 1) * P + ((sp.tile(u) * KT + skey) & (P - 1))) * 4;
@@ -325,17 +330,40 @@ attn_rows_kernel(AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[n][e] = 0.0f;
   };
-  auto scores_bf16 = [&](int u) Q8_INLINE {
-    const char *kb = kfrag + slot(u) * kVal;
-    zero_scores();
-#pragma unroll
-    for (int k = 0; k < NK; ++k)
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(kb + (2 * k * KT + 32 * n) * 16);
-        x[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[k], x[n], 0, 0, 0);
-      }
+  // The products of a stage's probabilities with its values (steps 0 .. NP-1, vb
+  // its value fragments) and of a stage's keys with the queries (the NK * NS after
+  // those, kb its key fragments): steps FROM .. TO-1, the fragments read kRead
+  // steps ahead.  Each step is fenced: left alone the compiler puts every read
+  // right before its product, which then waits for all of LDS's latency.
+  constexpr int NP = NS * 2 * NB, kRead = 3;
+  auto fragment = [&](int i, const char *vb, const char *kb) Q8_INLINE {
+    const int j = i - NP;
+    return *reinterpret_cast<const bf16x8_t *>(
+        i < NP ? vb + ((i / NB) * 2 * D + 32 * (i % NB)) * 16
+               : kb + (2 * (j / NS) * KT + 32 * (j % NS)) * 16);
   };
+  auto multiply = [&](auto FROM, auto TO, const char *vb, const char *kb) Q8_INLINE {
+    bf16x8_t f[kRead];
+    if constexpr (TO > NP) zero_scores();
+#pragma unroll
+    for (int i = FROM; i < FROM + kRead; ++i) f[i % kRead] = fragment(i, vb, kb);
+#pragma unroll
+    for (int i = FROM; i < TO; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int j = i - NP;
+      if (i < NP)
+        o[i % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kRead], pb[i / (2 * NB)][i / NB % 2], o[i % NB], 0, 0, 0);
+      else
+        x[j % NS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kRead], q[j / NS], x[j % NS], 0, 0, 0);
+      if (i + kRead < TO) f[i % kRead] = fragment(i + kRead, vb, kb);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  typedef std::integral_constant<int, 0> First;
+  typedef std::integral_constant<int, NP> Keys;
+  typedef std::integral_constant<int, NP + NK * NS> End;
+  auto scores_bf16 = [&](int u) Q8_INLINE { multiply(Keys{}, End{}, nullptr, kfrag + slot(u) * kVal); };
+  auto add_values = [&](int u) Q8_INLINE { multiply(First{}, Keys{}, vfrag + slot(u) * kVal, nullptr); };
   auto scores_q8 = [&](int u) Q8_INLINE {   // each 32-dim product times its key's scale
     const char *kb = kfrag + slot(u) * kVal;
     const float *ksc = reinterpret_cast<const float *>(kscl + slot(u) * kScl) + 8 * hf;
@@ -421,18 +449,6 @@ attn_rows_kernel(AttnArgs a) {
       pb[n][1] = to_bf16x8(p + 8);
     }
   };
-  auto add_values = [&](int u) Q8_INLINE {
-    const char *vb = vfrag + slot(u) * kVal;
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int T = 0; T < NB; ++T) {
-          const bf16x8_t f = *reinterpret_cast<const bf16x8_t *>(vb + ((4 * n + 2 * t) * D + 32 * T) * 16);
-          o[T] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[n][t], o[T], 0, 0, 0);
-        }
-  };
   // Q8_0: the probabilities take the value scales, for each 32 dims.
   auto add_values_q8 = [&](int u, bool all) Q8_INLINE {
     const char *vb = vfrag + slot(u) * kVal;
@@ -466,10 +482,16 @@ attn_rows_kernel(AttnArgs a) {
   // bf16, where some value is infinite or NaN and not every column sees every
   // token: the matrix product would carry it, times zero, into columns that do
   // not see it.  Token by token instead, each column adding those it sees, its
-  // probabilities laid out in `scratch`.
+  // probabilities laid out in `scratch` and its sums in memory meanwhile: this
+  // part is kept short, not fast.
   auto odd_values = [&](int u, char *scratch) Q8_INLINE {
     uint16_t *mine = reinterpret_cast<uint16_t *>(scratch) + wave * 32 * 32;
     const int half = here(hf), at = here(col);
+    float sums[NB * 16];
+#pragma unroll
+    for (int T = 0; T < NB; ++T)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sums[T * 16 + e] = o[T][e];
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       const unsigned seen = seen_keys(u, n);
@@ -484,18 +506,19 @@ attn_rows_kernel(AttnArgs a) {
       for (int k = 0; k < 32; ++k) {
         const uint16_t bits = mine[k * 32 + at];
         const float pk = __uint_as_float((uint32_t)bits << 16);
-#pragma unroll
-        for (int T = 0; T < NB; ++T) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int d = 32 * T + 8 * (e >> 2) + 4 * half + (e & 3);
-            const float v = __uint_as_float((uint32_t)vp[((k >> 3) * D + d) * 8 + (k & 7)] << 16);
-            o[T][e] = bits != 0xffffu ? fmaf(pk, v, o[T][e]) : o[T][e];
-          }
-          __builtin_amdgcn_sched_barrier(0);
+        if (bits == 0xffffu) continue;
+#pragma unroll 1
+        for (int i = 0; i < NB * 16; ++i) {
+          const int d = 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * half + (i & 3);
+          const float v = __uint_as_float((uint32_t)vp[((k >> 3) * D + d) * 8 + (k & 7)] << 16);
+          sums[i] = fmaf(pk, v, sums[i]);
         }
       }
     }
+#pragma unroll
+    for (int T = 0; T < NB; ++T)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[T][e] = sums[T * 16 + e];
   };
 
   // Stages from .. to-1 one after the other.
@@ -543,16 +566,23 @@ attn_rows_kernel(AttnArgs a) {
     }
     while (u < to) {
       float mx;
-      for (;;) {
+      if constexpr (kTurns) {  // few stages, those that in_turns leaves: short code
         first();
         mx = largest();
-        if (passes(mx)) break;
+        if (passes(mx)) raise(mx);
         second();
+      } else {
+        for (;;) {
+          first();
+          mx = largest();
+          if (passes(mx)) break;
+          second();
+          if (u == to) break;
+        }
         if (u == to) break;
+        raise(mx);
+        second();
       }
-      if (u == to) break;
-      raise(mx);
-      second();
     }
     __syncthreads();           // the last stage has been used
   };
@@ -565,13 +595,16 @@ attn_rows_kernel(AttnArgs a) {
   auto in_turns = [&](int from, int to) Q8_INLINE {
     static_assert(FMT != Q8_KV_BF16 || SL == 4, "two stages ahead");
     int u = from;
+    Source next;
     auto loaded = [&]() Q8_INLINE {
       __builtin_amdgcn_sched_barrier(0);
       loads_done<0>();
       turn();
-      if (u + 2 < to) issue(u + 2);
+      if (u + 2 < to) issue_from(next, u + 2);
+      __builtin_amdgcn_sched_barrier(0);
     };
     auto second = [&]() Q8_INLINE {
+      next = source(min(u + 3, to - 1));
       soften();
       turn();
       ++u;
@@ -579,19 +612,17 @@ attn_rows_kernel(AttnArgs a) {
     issue(from);
     loads_done<0>();
     if (from + 1 < to) issue(from + 1);
+    next = source(min(from + 2, to - 1));
     turn();
     if (wave >= W / 2) turn();
     scores_bf16(u);
-    read_ahead<NK * NS, 4>();
     loaded();
     raise(largest());
     second();
     while (u < to) {
       float mx;
       for (;;) {
-        add_values(u - 1);
-        scores_bf16(u);
-        read_ahead<NS * NB * 2 + NK * NS, 4>();
+        multiply(First{}, End{}, vfrag + slot(u - 1) * kVal, kfrag + slot(u) * kVal);
         loaded();
         mx = largest();
         if (passes(mx)) break;
@@ -607,20 +638,25 @@ attn_rows_kernel(AttnArgs a) {
     __syncthreads();
   };
 
+  // The stages after the kept first tokens' that every column sees whole (while
+  // all their pages are pages): of the last KT tokens' stages those up to p0,
+  // and under a window those past where p1's begins.
+  const int edge = a.window > 0 ? max((p1 - a.window + KT) / KT, 0) : 0;
+  const int whole0 = sp.a + max(edge - sp.t0, 0), whole1 = sp.a - sp.t0 + (p0 + 1) / KT;
   for (; base < u1; base += kListStages) {
     const int end = min(base + kListStages, u1);
+    bool lost = false;
     for (int g = threadIdx.x; g < (end - base) * (KT / 16); g += kThreads) {
       const int key = sp.tile(base + g / (KT / 16)) * KT + g % (KT / 16) * 16;
       const int p = trow[min(key, last) >> pl];
-      pids[g] = (unsigned)p < (unsigned)c.n_pages ? p : -1;
+      const bool ok = (unsigned)p < (unsigned)c.n_pages;
+      pids[g] = ok ? p : -1;
+      lost |= !ok;
     }
-    __syncthreads();
-    if constexpr (FMT == Q8_KV_BF16 && W == 8) {
-      // the first run of whole stages in turns, those before and after it not
-      int w0 = base, w1;
-      while (w0 < end && !whole(w0)) ++w0;
-      for (w1 = w0; w1 < end && whole(w1);) ++w1;
-      if (w1 - w0 < 3) w0 = w1 = base;
+    lost = __syncthreads_or(lost);
+    if constexpr (kTurns) {
+      int w0 = min(max(whole0, base), end), w1 = min(max(whole1, w0), end);
+      if (lost || w1 - w0 < 3) w0 = w1 = base;
       if (base < w0) in_step(base, w0);
       if (w0 < w1) in_turns(w0, w1);
       if (w1 < end) in_step(w1, end);
@@ -687,25 +723,27 @@ attn_rows_kernel(AttnArgs a) {
       __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
   }
 
-  // divide and write: 32 dims of the wave's columns at a time through LDS, so
+  // divide and write: 64 dims of the wave's columns at a time through LDS, so
   // that eight lanes hold a column's 32-value block
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  constexpr int kRowF = 36;
+  constexpr int kRowF = kOutRow;
   float *mylds = reinterpret_cast<float *>(lds) + wave * 32 * kRowF;
 #pragma unroll
-  for (int T = 0; T < NB; ++T) {
+  for (int T2 = 0; T2 < NB; T2 += 2) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h)
-      *reinterpret_cast<float4 *>(mylds + col * kRowF + 8 * h + 4 * hf) =
-          make_float4(o[T][4 * h] * inv, o[T][4 * h + 1] * inv, o[T][4 * h + 2] * inv, o[T][4 * h + 3] * inv);
+    for (int T = T2; T < T2 + 2; ++T)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        *reinterpret_cast<float4 *>(mylds + col * kRowF + 32 * (T - T2) + 8 * h + 4 * hf) = make_float4(
+            o[T][4 * h] * inv, o[T][4 * h + 1] * inv, o[T][4 * h + 2] * inv, o[T][4 * h + 3] * inv);
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int cc = h * 8 + (lane >> 3), d = (lane & 7) * 4;
+#pragma unroll 1
+    for (int h = 0; h < 8; ++h) {
+      const int cc = h * 4 + (lane >> 4), d = (lane & 15) * 4;
       const int mc = c0 + wave * 32 + cc;
       const float4 y = *reinterpret_cast<const float4 *>(mylds + cc * kRowF + d);
       if (mc < ncol)
-        store_out(a, start + mc / a.group, (hk * a.group + mc % a.group) * D + 32 * T + d, y);
+        store_out(a, start + mc / a.group, (hk * a.group + mc % a.group) * D + 32 * T2 + d, y);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -713,7 +751,7 @@ attn_rows_kernel(AttnArgs a) {
 
 template <int D, int FMT>
 hipError_t launch(const AttnArgs &a, hipStream_t stream) {
-  constexpr int out = kWaves<D, FMT> * 32 * 36 * 4;
+  constexpr int out = kWaves<D, FMT> * 32 * kOutRow * 4;
   constexpr int stages = 2 * kSlots<FMT> * (kValBytes<D> + kScaleBytes<D, FMT>);
   constexpr int lds = stages > out ? stages : out;
   if (lds > 48 * 1024) {
@@ -728,7 +766,9 @@ hipError_t launch(const AttnArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-int cols_of(int64_t dim, int fmt) { return fmt == Q8_KV_BF16 && dim < 256 ? 256 : 128; }
+int cols_of(int64_t dim, int fmt) {
+  return fmt == Q8_KV_BF16 && dim < 256 ? kCols<128, Q8_KV_BF16> : kCols<128, Q8_KV_Q8_0>;
+}
 
 int64_t blocks_bound(int64_t m, int64_t n, int64_t group, int cols) {
   return (m * group + cols - 1) / cols + n;
@@ -736,11 +776,15 @@ int64_t blocks_bound(int64_t m, int64_t n, int64_t group, int cols) {
 
 }  // namespace
 
-// Key splits: as many as bring the workgroups to two a CU (one a CU of those of
-// eight waves).
+// Key splits: as many as keep the workgroups to one a CU (eight waves), two
+// (256 dims) or, over Q8_0, six: there each is short of work for its barriers,
+// and a CU holds two at a time.  Measured on MI355X (us; one, two, three times
+// these): 512 rows behind 4096 tokens 47, 66, 64; 2048 rows of 256 dims 224,
+// 224, 304; Q8_0 (a third, two thirds, these), 3 x 509 rows behind 4096 171, 176,
+// 152, 2048 rows 107, 109, 99.
 int attn_rows_splits(int64_t m, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim, int fmt) {
-  const int cols = cols_of(dim, fmt);
-  const int64_t s = (cols == 256 ? 256 : 512) / (blocks_bound(m, n, q_heads / kv_heads, cols) * kv_heads);
+  const int cols = cols_of(dim, fmt), target = dim == 256 ? 512 : fmt == Q8_KV_BF16 ? 256 : 1536;
+  const int64_t s = target / (blocks_bound(m, n, q_heads / kv_heads, cols) * kv_heads);
   return (int)(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
 }
 
