@@ -86,7 +86,8 @@ kv_step_kernel(q8_kv_step_args a, int page_log2) {
     row += rows[e];
     const long long after = (long long)len[e] + rows[e];
     const int pages = (int)((after + P1) >> page_log2);
-    barred[e] = !ended[e] && (pages > most || row > m || after > 0x7fffffff);
+    barred[e] = tid * E + e < n && !ended[e] &&
+                (pages > most || row > m || after > 0x7fffffff);
     need[e] = (ended[e] || barred[e]) ? 0 : pages - held[e];
     sum_need += need[e];
   }

@@ -653,7 +653,7 @@ int q8_qkv_heads(const float *q, int64_t ldq, const float *k, int64_t ldk,
 
 /*
  * q8_kv_gather: the cache rows at slots[0..rows) as bf16 rows (rows x kv_heads
- * x head_dim, row-major; a Q8_0 row's code * scale rounded once).  Rows whose
+ * x head_dim, row-major; a Q8_0 row's code * scale in fp32, rounded).  Rows whose
  * slot lies outside the cache stay as they were.  k_out or v_out may be NULL
  * (not both).  Requires 1 <= rows <= 2^24.
  */

@@ -158,7 +158,7 @@ def write_rows(lay, buf, which, slots, rows):
         buf[at], buf[at + 1] = (bits & 255).astype(np.uint8), (bits >> 8).astype(np.uint8)
         return bf16_round(rows).astype(np.float64)
     from . import quantize_rows_f32
-    flat = np.ascontiguousarray(rows, np.float32).reshape(len(rows), -1)
+    flat = np.ascontiguousarray(rows, np.float32).reshape(len(rows), lay.heads * lay.dim)
     code, d = quantize_rows_f32(flat)
     code, d = code.reshape(rows.shape), d.reshape(*rows.shape[:2], lay.dim // 32)
     buf[at] = code.view(np.uint8)
@@ -182,13 +182,14 @@ def read_rows(lay, buf, which, slots):
 # ---- attention ------------------------------------------------------------------------
 
 def attention(q, k, v, positions, scale, window=0, sinks=0, present=None):
-    """(o, bound, score_bound) in 64 bits of rows q (rows x heads x dim) at their positions over the
-    tokens k, v (tokens x kv_heads x dim); present: which tokens exist.  bound = sum of p |v|, what a
-    rounding of the probabilities scales with; score_bound = for each (row, head) the largest |scale|
-    sum |q k| of a token that it sees."""
+    """(o, bound, spread, size) in 64 bits of rows q (rows x heads x dim) at their positions over the
+    tokens k, v (tokens x kv_heads x dim); present: which tokens exist.  bound = sum of p |v|, what
+    roundings of the probabilities scale with at the worst; spread = sqrt(sum of (p v)^2), what they
+    scale with when they are independent; size = for each (row, head) the largest |scale| sum |q k| of
+    a token that it sees."""
     rows, hq, dim = q.shape
     group = hq // k.shape[1] if len(k) else 1
-    o, bound = np.zeros((rows, hq, dim)), np.zeros((rows, hq, dim))
+    o, bound, spread = (np.zeros((rows, hq, dim)) for _ in range(3))
     size = np.zeros((rows, hq))
     t = np.arange(len(k))
     for r in range(rows):
@@ -206,4 +207,5 @@ def attention(q, k, v, positions, scale, window=0, sinks=0, present=None):
             p = np.exp(s - s.max())
             p /= p.sum()
             o[r, h], bound[r, h] = p @ vv, p @ np.abs(vv)
-    return o, bound, size
+            spread[r, h] = np.sqrt((p * p) @ (vv * vv))
+    return o, bound, spread, size

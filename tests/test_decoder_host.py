@@ -111,19 +111,19 @@ def test_attention_closed_forms():
     rng = np.random.default_rng(2)
     k, v = rng.standard_normal((9, 2, 64)), rng.standard_normal((9, 2, 64))
     q = rng.standard_normal((1, 4, 64))
-    o, _, _ = dec.attention(q, k, v, [0], 0.125)              # one token: its value
+    o = dec.attention(q, k, v, [0], 0.125)[0]              # one token: its value
     assert np.allclose(o[0], np.repeat(v[0], 2, 0))
-    o, _, _ = dec.attention(q * 0, k, v, [8], 0.125)          # equal scores: the mean
+    o = dec.attention(q * 0, k, v, [8], 0.125)[0]          # equal scores: the mean
     assert np.allclose(o[0], np.repeat(v.mean(0), 2, 0))
-    o, _, _ = dec.attention(q * 0, k, v, [8], 0.125, window=3, sinks=2)
+    o = dec.attention(q * 0, k, v, [8], 0.125, window=3, sinks=2)[0]
     assert np.allclose(o[0], np.repeat(v[[0, 1, 6, 7, 8]].mean(0), 2, 0))
-    o, _, _ = dec.attention(q, k, v, [-1], 0.125)             # no token
+    o = dec.attention(q, k, v, [-1], 0.125)[0]             # no token
     assert (o == 0).all()
-    whole, _, _ = dec.attention(q, k, v, [8], 0.125)
+    whole = dec.attention(q, k, v, [8], 0.125)[0]
     there = np.ones(9, bool)
     there[4] = False
-    less, _, _ = dec.attention(q, np.delete(k, 4, 0), np.delete(v, 4, 0), [7], 0.125)
-    got, _, _ = dec.attention(q, k, v, [8], 0.125, present=there)
+    less = dec.attention(q, np.delete(k, 4, 0), np.delete(v, 4, 0), [7], 0.125)[0]
+    got = dec.attention(q, k, v, [8], 0.125, present=there)[0]
     assert np.allclose(got, less) and not np.allclose(got, whole)
 
 
