@@ -412,7 +412,9 @@ attn_rows_kernel(AttnArgs a) {
   };
   // The largest score, and whether it passes the maximum in some column; raise
   // then raises the maxima to it.  Both loops below leave for it and come back:
-  // as a branch inside them it would cost a copy of all sums at every stage.
+  // as a branch inside them it would cost a copy of all sums at every stage.  A
+  // column whose own largest does not pass keeps its maximum, so that its
+  // roundings do not depend on the columns beside it.
   auto largest = [&]() Q8_INLINE {
     float t[4] = {x[0][0], x[0][1], x[0][2], x[0][3]};
 #pragma unroll
@@ -424,7 +426,7 @@ attn_rows_kernel(AttnArgs a) {
   };
   auto passes = [&](float mx) Q8_INLINE { return __any(mx > m + kSlack); };
   auto raise = [&](float mx) Q8_INLINE {
-    const float mn = fmaxf(m, mx);
+    const float mn = mx > m + kSlack ? mx : m;
     const float alpha = exp2_fast(m - mn);
     m = mn;
     l *= alpha;
@@ -482,10 +484,14 @@ attn_rows_kernel(AttnArgs a) {
   // bf16, where some value is infinite or NaN and not every column sees every
   // token: the matrix product would carry it, times zero, into columns that do
   // not see it.  Token by token instead, each column adding those it sees, its
-  // probabilities laid out in `scratch` and its sums in memory meanwhile: this
-  // part is kept short, not fast.
-  auto odd_values = [&](int u, char *scratch) Q8_INLINE {
-    uint16_t *mine = reinterpret_cast<uint16_t *>(scratch) + wave * 32 * 32;
+  // probabilities laid out in the place of stage u-1 (its keys' first, then its
+  // values': 2 KB a wave) and its sums in memory meanwhile: this part is kept
+  // short, not fast.
+  auto odd_values = [&](int u) Q8_INLINE {
+    static_assert(W * 2048 <= 2 * kVal, "a wave's probabilities");
+    constexpr int kInKeys = kVal / 2048;      // waves whose piece is in the keys' place
+    char *const scratch = lds + slot(u - 1) * kVal + (wave < kInKeys ? wave : wave - kInKeys) * 2048;
+    uint16_t *mine = reinterpret_cast<uint16_t *>(scratch + (wave < kInKeys ? 0 : SL * kVal));
     const int half = here(hf), at = here(col);
     float sums[NB * 16];
 #pragma unroll
@@ -543,7 +549,7 @@ attn_rows_kernel(AttnArgs a) {
     auto second = [&]() Q8_INLINE {        // its probabilities and values
       if constexpr (FMT == Q8_KV_BF16) {
         if (odd) {
-          odd_values(u, lds + slot(u - 1) * kVal);
+          odd_values(u);
           __syncthreads();
           if (u + SL - 1 < to) issue(u + SL - 1);
         } else {
