@@ -15,10 +15,6 @@ constexpr int kListGroups = 512;        // 16-token groups whose pages are held 
 
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 
-// The kernel's parts work on its registers: one that became a function would
-// move them to memory.
-#define Q8_INLINE __attribute__((always_inline))
-
 // Waves of a workgroup, 32 columns each: eight (two a SIMD, in turns, below)
 // where their registers allow it and the stages need no widening.
 template <int D, int FMT> constexpr int kWaves = FMT == Q8_KV_BF16 && D < 256 ? 8 : 4;

@@ -8,6 +8,10 @@
 
 #include "q8_internal.h"
 
+// For lambdas that are parts of a kernel: they work on its registers, and one
+// that became a function would move them to memory.
+#define Q8_INLINE __attribute__((always_inline))
+
 namespace q8 {
 namespace dev {
 
