@@ -20,9 +20,9 @@ LIB = os.path.join(HERE, "libq8gemv.so")
 SOURCES = ["q8_kernels.hip", "q8_mfma32.hip", "q8_tile16.hip", "q8_gemm.hip", "q8_measure.hip",
            "q8_noalloc.hip", "q8_kv.hip", "q8_attn.hip", "q8_attn_rows.hip", "q8_api.cpp",
            "q8_kv_api.cpp"]
-# Per-source device flags.  The GEMM writes its MFMA results to VGPRs (by
-# default the compiler routes them through one AGPR quad and serialises the
-# matrix core behind its reads).
+# Per-source device flags.  The GEMM and the attentions write their MFMA results
+# to VGPRs (by default the compiler routes them through one AGPR quad and
+# serialises the matrix core behind its reads).
 SOURCE_FLAGS = {s: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
                 for s in ("q8_gemm.hip", "q8_attn.hip", "q8_attn_rows.hip")}
 ARCH = os.environ.get("Q8_OFFLOAD_ARCH", "gfx950")

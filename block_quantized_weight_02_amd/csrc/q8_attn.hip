@@ -8,8 +8,13 @@ namespace q8 {
 namespace {
 
 constexpr int kHeadTile = 16;          // query heads of one matrix-core tile
+// One workgroup a CU: 1 x 131072 tokens take 85 us, with two 94, with four 133;
+// 32 x 8192 67, 72, 86 (8 key/value heads of 128, bf16; more workgroups only add
+// pieces to join, since one keeps enough loads on their way).
 constexpr int kTargetWorkgroups = 256;
-constexpr int kMinTiles = 4;           // fewest tiles of a workgroup's share
+// Fewest tiles of a workgroup's share: 512 tokens take 9.0 us, with eight tiles
+// 10.5, with sixteen 12.1.
+constexpr int kMinTiles = 4;
 constexpr int kListTiles = 256;        // tiles of a share listed in LDS at a time
 constexpr int kListSeqs = 64;          // and sequences
 
@@ -604,8 +609,7 @@ hipError_t launch(const AttnArgs &a, int units, hipStream_t stream) {
 
 }  // namespace
 
-int attn_decode_chunks(int64_t n, int64_t units) {
-  (void)n;
+int attn_decode_chunks(int64_t units) {
   const int64_t g = kTargetWorkgroups / units;
   return (int)(g < 1 ? 1 : g);
 }
@@ -613,7 +617,7 @@ int attn_decode_chunks(int64_t n, int64_t units) {
 size_t attn_decode_partial_bytes(int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim) {
   const int64_t group = q_heads / kv_heads;
   const int64_t units = kv_heads * ((group + kHeadTile - 1) / kHeadTile);
-  const int64_t chunks = attn_decode_chunks(n, units);
+  const int64_t chunks = attn_decode_chunks(units);
   return (size_t)(chunks + n) * units *
          record_floats((int)(group < kHeadTile ? group : kHeadTile), (int)dim) * 4;
 }

@@ -129,6 +129,16 @@ __host__ __device__ constexpr int record_floats(int cols, int dim) { return cols
 // take turns (in_turns): waves 0-3 run half a stage before waves 4-7, and
 // between two barriers the one half multiplies (a stage's values and the next
 // one's keys) while the other turns its scores into probabilities.
+//
+// Measured on MI355X, 8192 rows of 32 heads over 8, 128 dims, bf16, behind 0
+// tokens: 520 us, 1.06 PFLOP/s of 1.3 that a large library product reaches; four
+// waves in step with the maximum raised inside the loop took 627, stages through
+// registers 658.  Bound by LDS reads: a half's products take 128 KB of
+// fragments a turn, 1560 cycles at 85 bytes a clock, against 1340 for the other
+// half's probabilities.  Stages of 32 keys took 697 us against 633, waves of 64
+// columns spilled.  Q8_0, 3 x 509 rows behind 4096 tokens: 152 us; the codes are
+// widened once a stage and each 32 dims' scores scaled, so the vector unit bounds
+// it.
 constexpr float kSlack = 8.0f;
 
 template <int D, int FMT>

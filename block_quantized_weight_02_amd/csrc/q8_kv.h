@@ -62,7 +62,7 @@ constexpr int kKvTile = 32;
 
 // Workgroups a decode launch divides all tokens among, for each (key/value
 // head, group of 16 query heads) unit.
-int attn_decode_chunks(int64_t n, int64_t units);
+int attn_decode_chunks(int64_t units);
 size_t attn_decode_partial_bytes(int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim);
 // Key splits of a rows launch.
 int attn_rows_splits(int64_t m, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim,

@@ -171,7 +171,7 @@ int run_attn(const uint16_t *q, int64_t m, int64_t q_heads, const q8_kv_cache *c
     return done(q8::launch_attn_rows(a, stream), "attn_rows launch");
   }
   const int64_t units = cache->kv_heads * ((a.group + 15) / 16);
-  a.chunks = q8::attn_decode_chunks(n, units);
+  a.chunks = q8::attn_decode_chunks(units);
   return done(q8::launch_attn_decode(a, stream), "attn_decode launch");
 }
 
