@@ -2,6 +2,7 @@
 // include/q8gemv.h: argument validation before any launch, and errors.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/q8gemv.h"
@@ -16,6 +17,7 @@ using q8::report_error;
 // that one zeroed workspace serves both.
 constexpr size_t kCounterBytes = (size_t)4 << 20;
 constexpr int64_t kMaxInt = 0x7fffffff;
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;   // of a sequence that attention reads
 
 int ok() {
   report_error(Q8_OK, "%s", "");
@@ -120,13 +122,16 @@ int run_attn(const uint16_t *q, int64_t m, int64_t q_heads, const q8_kv_cache *c
              hipStream_t stream, void *workspace, size_t ws_bytes, bool rows) {
   int st;
   if ((st = check_attn_sizes(m, n, q_heads, cache, rows))) return st;
-  if ((st = check_range(max_pages, 1, kMaxInt / n, "max_pages"))) return st;
+  // positions, and a tile or a window past them, stay in 32 bits
+  if ((st = check_range(max_pages, 1, std::min(kMaxInt / n, kMaxTokens / cache->page),
+                        "max_pages"))) return st;
   if (n * max_pages > (int64_t(1) << 35) / cache->page)
     return report_error(Q8_ERR_SHAPE, "n * max_pages * page = %lld exceeds 2^35",
                         (long long)(n * max_pages * cache->page));
   if (!attn) return report_error(Q8_ERR_NULL, "attn is NULL");
-  if (!std::isfinite(attn->scale))
-    return report_error(Q8_ERR_SHAPE, "scale is not finite");
+  const float scale_log2 = (float)((double)attn->scale * 1.4426950408889634074);
+  if (!std::isfinite(scale_log2))
+    return report_error(Q8_ERR_SHAPE, "scale = %g: need |scale| < 2^127", (double)attn->scale);
   if ((st = check_range(attn->window, 0, kMaxInt, "window"))) return st;
   if ((st = check_range(attn->sinks, 0, kMaxInt, "sinks"))) return st;
   q8::AttnArgs a{};
@@ -156,9 +161,9 @@ int run_attn(const uint16_t *q, int64_t m, int64_t q_heads, const q8_kv_cache *c
   a.max_pages = max_pages;
   a.lens = lens;
   a.row_start = rows ? row_start : nullptr;
-  a.scale_log2 = (float)((double)attn->scale * 1.4426950408889634074);
-  a.window = attn->window;
-  a.sinks = attn->sinks;
+  a.scale_log2 = scale_log2;
+  a.window = (int)std::min<int64_t>(attn->window, kMaxTokens);   // all of a sequence, as it was
+  a.sinks = (int)std::min<int64_t>(attn->sinks, kMaxTokens);
   a.o = o;
   if (o_q8) {
     a.oq = static_cast<int8_t *>(o_q8);

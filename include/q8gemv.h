@@ -549,7 +549,7 @@ size_t q8_kv_bytes(int fmt, int64_t kv_heads, int64_t head_dim, int64_t page,
  * step advances in place); otherwise outputs must not overlap inputs.  table
  * and free_pages are updated in place: entries not named above stay as they
  * were.  Requires 1 <= n <= Q8_MAX_SEQS, 1 <= m <= Q8_MAX_GEMM_ROWS, page as in
- * q8_kv_cache, max_pages >= 1, n * max_pages and free_cap <= 2^31 - 1.  A
+ * q8_kv_cache, max_pages >= 1, n * max_pages < 2^30, free_cap <= 2^31 - 1.  A
  * length below 0 counts as 0 and one above max_pages * P as that, a
  * free_count outside 0 .. free_cap as the nearer of the two; pages past
  * free_cap are dropped.
@@ -629,7 +629,8 @@ int q8_rope_freqs(const q8_rope *rope /* host pointer */, double *freqs,
  * the cache's format.  Rows whose slot lies outside 0 .. n_pages * page - 1
  * are skipped: their q_out rows stay as they were.  Two rows of one call must
  * not have the same slot (which of them the cache then holds, or parts of
- * which, is not defined); a position below 0 counts as 0.  Requires 1 <= m <=
+ * which, is not defined); q_out must not overlap q, k or v; a position below 0
+ * counts as 0.  Requires 1 <= m <=
  * Q8_MAX_GEMM_ROWS, q_heads a multiple of kv_heads, at most 1024; rot % 8 == 0,
  * 0 <= rot <= head_dim, freqs when rot > 0; eps >= 0.
  */
@@ -673,7 +674,8 @@ int q8_kv_gather(const q8_kv_cache *cache /* host pointer */, const int32_t *slo
  * row that sees no token gets zeros.  Tokens not seen are not part of the
  * result whatever their cache bytes hold.  A length below 0 counts as 0, one
  * above max_pages * page as that; tokens on a page index outside 0 .. n_pages
- * - 1 are not seen.
+ * - 1 are not seen.  Requires max_pages * page <= 2^30, n * max_pages <= 2^31 - 1
+ * and n * max_pages * page <= 2^35.
  *
  * q is m x q_heads x head_dim bf16.  The output is written as o (m x q_heads *
  * head_dim bf16, may be NULL) and/or o_q8 (its quantized form from the fp32
@@ -688,7 +690,7 @@ int q8_kv_gather(const q8_kv_cache *cache /* host pointer */, const int32_t *slo
  * Results do not depend on timing: pieces of a sequence are joined in order.
  */
 typedef struct q8_attn {
-  float scale;     /* finite                                                  */
+  float scale;     /* finite, below 2^127 in size; negative and zero are fine */
   int32_t window;  /* tokens a row sees back, its own included; 0: all        */
   int32_t sinks;   /* first tokens always seen (with window > 0), >= 0        */
 } q8_attn;

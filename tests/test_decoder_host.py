@@ -212,7 +212,8 @@ def attn_args(kw):
 
 BAD_ATTENTION = [
     (dict(n=0), 1), (dict(n=8193), 1), (dict(q_heads=5), 1), (dict(q_heads=0), 1), (dict(max_pages=0), 1),
-    (dict(n=8192, max_pages=1 << 18), 1), (dict(attn=None), 3), (dict(scale=float("nan")), 1),
+    (dict(n=8192, max_pages=1 << 18), 1), (dict(max_pages=(1 << 26) + 1), 1), (dict(attn=None), 3),
+    (dict(scale=float("nan")), 1), (dict(scale=3e38), 1), (dict(scale=-3e38), 1),
     (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(q=None), 3), (dict(table=A + 4), 4), (dict(lens=None), 3),
     (dict(o=None), 3), (dict(o=A + 4), 4), (dict(o_q8=A + 4), 4), (dict(workspace=None), 5),
     (dict(ws_bytes=100), 5), (dict(workspace=A + 8), 4), (dict(cache=None), 3), (dict(cache=dict(head_dim=96)), 1)]

@@ -425,6 +425,49 @@ def test_two_streams():
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
 
 
+@pytest.mark.parametrize("fmt", [BF16, Q8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_replays_follow_the_lengths(fmt, dim):
+    """Both calls captured over one workspace; between the replays the lengths, rows and pages change and
+    the workspace serves eager calls; every replay equals the eager calls on the same state."""
+    s = u.Scene(fmt, 2, dim, 16, [900, 40, 0, 333], seed=111).to_device()
+    q = u.bf16_dev(queries(s, 60, 4, 3))
+    start = g.dev(np.array([0, 20, 25, 25, 60], np.int32))
+    attn = q8.make_attn(0.1, 200, 4)
+    b = max(s.workspace(0, 8)[1], s.workspace(60, 8)[1])
+    ws = torch.zeros(b, dtype=torch.uint8, device=g.DEV), b
+    bufs = [torch.zeros((r, 8, dim), dtype=torch.bfloat16, device=g.DEV) for r in (4, 60)]
+
+    def run(o, p):
+        u.decode(s, q[:4], attn, o, None, ws=ws)
+        u.rows(s, q, start, attn, p, None, ws=ws)
+
+    run(*bufs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(*bufs)
+    order = np.random.default_rng(5)
+    for lens, starts in (([900, 40, 0, 333], [0, 20, 25, 25, 60]), ([899, 39, 0, 1], [0, 0, 39, 39, 40]),
+                         ([31, 32, 0, 300], [0, 31, 40, 40, 60]), ([0, 0, 0, 0], [0, 0, 0, 0, 0]),
+                         ([900, 1, 0, 333], [0, 1, 2, 2, 3])):
+        s.lens_d.copy_(torch.tensor(lens))
+        start.copy_(torch.tensor(starts))
+        s.table[0, :56] = s.table[0, order.permutation(56)]
+        s.table_d.copy_(torch.from_numpy(s.table))
+        for o in bufs:
+            o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = [torch.full_like(o, 7.0) for o in bufs]
+        run(*want)
+        torch.cuda.synchronize()
+        for x, y in zip(bufs, want):
+            assert torch.equal(x, y), lens
+        assert (u.host(bufs[1])[starts[-1]:] == 7.0).all()
+        assert not ws[0][:4 << 20].any()
+
+
 def test_layer_replayed():
     """A step's calls as a serving loop captures them: tables, the q/k/v product, heads, attention and the
     output product, replayed while the cache grows, each replay against the same calls run eagerly from
