@@ -85,7 +85,8 @@ __device__ __forceinline__ bool not_finite(u32x4_t v) {
 // 16 bytes a lane from memory into LDS at `at` (a scalar) plus 16 times the
 // lane, without registers in between; loads_done waits for all but the last N.
 // They are written out because the compiler would make every read of LDS wait
-// for every such load, the next stages' too.
+// for every such load, the next stages' too.  m0, the load's base in LDS, is a
+// register that the compiler sets right before its own uses (here it has none).
 __device__ __forceinline__ void load_to_lds(const void *p, unsigned at) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :: "v"(p), "s"(at) : "memory");
