@@ -452,19 +452,19 @@ qkv_heads_kernel(HeadsArgs a, int passes) {
 // ---- rows read back -----------------------------------------------------------------
 
 // A thread reads eight dims of one (row, head): one 16-byte piece of the keys,
-// eight places of the values.
+// eight places of the values.  A launch holds fewer than 2^32 threads, the call
+// up to 2^36 pieces, so past kGatherBlocks workgroups a thread takes several.
+constexpr long long kGatherBlocks = 1 << 20;
+
 template <int FMT>
-__global__ void __launch_bounds__(256)
-kv_gather_kernel(KvCache c, const int32_t *__restrict__ slots, int rows,
-                 uint16_t *__restrict__ k_out, uint16_t *__restrict__ v_out) {
-  const int D = c.dim, per_row = c.heads * (D / 8);
-  const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int r = (int)(idx / per_row);
-  if (r >= rows) return;
+__device__ __forceinline__ void gather_piece(const KvCache &c, const int32_t *__restrict__ slots,
+                                             uint16_t *__restrict__ k_out,
+                                             uint16_t *__restrict__ v_out, int r, int piece) {
+  const int D = c.dim;
   const int slot = slots[r];
   const int P = 1 << c.page_log2;
   if (slot < 0 || (slot >> c.page_log2) >= c.n_pages) return;
-  const int h = (int)(idx % per_row) / (D / 8), ch = (int)(idx % per_row) % (D / 8);
+  const int h = piece / (D / 8), ch = piece % (D / 8);
   const int tok = slot & (P - 1);
   const size_t at = (size_t)(slot >> c.page_log2) * c.page_bytes() + (size_t)h * c.record();
   const size_t out = ((size_t)r * c.heads + h) * D + ch * 8;
@@ -490,6 +490,17 @@ kv_gather_kernel(KvCache c, const int32_t *__restrict__ slots, int rows,
     for (int e = 0; e < 4; ++e) w[e] = (uint32_t)y[2 * e] | (uint32_t)y[2 * e + 1] << 16;
     *reinterpret_cast<uint4 *>(dst + out) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(256)
+kv_gather_kernel(KvCache c, const int32_t *__restrict__ slots, int rows,
+                 uint16_t *__restrict__ k_out, uint16_t *__restrict__ v_out) {
+  const int per_row = c.heads * (c.dim / 8);
+  const long long total = (long long)rows * per_row;
+  for (long long idx = (long long)blockIdx.x * 256 + threadIdx.x; idx < total;
+       idx += (long long)gridDim.x * 256)
+    gather_piece<FMT>(c, slots, k_out, v_out, (int)(idx / per_row), (int)(idx % per_row));
 }
 
 int log2_of(int v) {
@@ -543,7 +554,8 @@ hipError_t launch_qkv_heads(const HeadsArgs &a, hipStream_t stream) {
 hipError_t launch_kv_gather(const KvCache &c, const int32_t *slots, int rows, uint16_t *k_out,
                             uint16_t *v_out, hipStream_t stream) {
   const long long total = (long long)rows * c.heads * (c.dim / 8);
-  const unsigned blocks = (unsigned)((total + 255) / 256);
+  const long long need = (total + 255) / 256;
+  const unsigned blocks = (unsigned)(need < kGatherBlocks ? need : kGatherBlocks);
   auto k = c.fmt == Q8_KV_BF16 ? kv_gather_kernel<0> : kv_gather_kernel<1>;
   k<<<blocks, 256, 0, stream>>>(c, slots, rows, k_out, v_out);
   return hipGetLastError();

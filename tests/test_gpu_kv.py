@@ -312,6 +312,29 @@ def test_gather(fmt, dim, page, hkv):
         assert torch.equal(a, b)
 
 
+def test_gather_of_many_rows():
+    """2^32 pieces of eight dims in one call, most rows' slots outside the cache, so that only a few of the
+    64 GiB of rows are written."""
+    rows, hkv, dim, page = 1 << 24, 16, 128, 16
+    if torch.cuda.mem_get_info()[0] < 72 << 30:
+        pytest.skip("needs 72 GiB of device memory")
+    s = u.Scene(BF16, hkv, dim, page, [3 * page], seed=1).to_device()
+    at = [0, 1, 12345, (1 << 23) - 1, 1 << 23, rows - 2, rows - 1]
+    slots = torch.full((rows,), -1, dtype=torch.int32, device=g.DEV)
+    slots[at] = g.dev(s.slots(0, 5, 5 + len(at)).astype(np.int32))
+    out = torch.empty((rows, hkv, dim), dtype=torch.bfloat16, device=g.DEV)
+    near = [r + d for r in at for d in (-1, 1) if 0 <= r + d < rows and r + d not in at]
+    out[near] = 7.0
+    try:
+        q8.q8_kv_gather(s.cache, slots, rows, out, None)
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(u.host(out[at]), s.k[0][5:5 + len(at)])
+        assert (out[near] == 7.0).all()
+    finally:
+        del out
+        torch.cuda.empty_cache()
+
+
 def test_other_stream():
     """The calls follow the stream that they are given, with nothing ordered by the default one."""
     st = torch.cuda.Stream()
