@@ -201,7 +201,10 @@ kv_step_kernel(q8_kv_step_args a, int page_log2) {
     pos[k] = 0, slot[k] = -1;
     if (b != kRefused) {
       pos[k] = b + r;
-      slot[k] = (a.table[(long long)i * most + (pos[k] >> page_log2)] << page_log2) + (pos[k] & P1);
+      // a page index past what slots can name has none: it must not wrap to another page's
+      const int page = a.table[(long long)i * most + (pos[k] >> page_log2)];
+      const long long s = ((long long)page << page_log2) + (pos[k] & P1);
+      slot[k] = s == (int)s ? (int)s : -1;
     }
   }
 #pragma unroll

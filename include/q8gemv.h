@@ -540,9 +540,10 @@ size_t q8_kv_bytes(int fmt, int64_t kv_heads, int64_t head_dim, int64_t page,
  * Row r of the step belongs to the sequence with row_start[i] <= r <
  * row_start[i+1], row_start the running sum of rows_i, cut at m.  positions[r]
  * = lens[i] + r - row_start[i], slots[r] = table[i][positions[r] / P] * P +
- * positions[r] % P; rows of refused sequences and rows past the last
- * sequence's get position 0 and slot -1 (q8_qkv_heads skips them), so a
- * captured step may have more rows than are used.
+ * positions[r] % P (-1 where that does not fit 32 bits); rows of refused
+ * sequences and rows past the last sequence's get position 0 and slot -1
+ * (q8_qkv_heads skips them), so a captured step may have more rows than are
+ * used.
  * status[0] = refused sequences, status[1] = pages lacking (what the sequences
  * refused for want of pages, and all others, need in all, less what the list
  * holds).  lens_out may be lens, and free_count_out free_count (a captured

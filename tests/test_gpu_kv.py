@@ -129,6 +129,17 @@ def test_step_clamps_its_inputs():
     same(s.got(), want)
 
 
+def test_step_slots_past_32_bits():
+    """A page index whose slots do not fit 32 bits gives slot -1, not the slot of another page; one below 0
+    gives slots below 0."""
+    big = 2 ** 31 // 16                                    # its first slot is 2^31
+    table = np.array([[big], [2 * big], [2 * big + 3], [big - 1], [-1], [-2 ** 31], [5]])
+    s = Step([3] * 7, [1] * 7, table, [0, 0], 2, 16, 8)
+    s.run()
+    slots = s.got()[6].tolist()
+    assert slots == [-1, -1, -1, (big - 1) * 16 + 3, -13, -1, 83, -1]
+
+
 def test_step_rows_past_the_end():
     table = np.full((5, 200), -1)
     for new in ([2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1, 0], [3, 9, 1, 0, 2], [8, 1, -1, 0, 0], [0, 0, 0, 0, 9]):
