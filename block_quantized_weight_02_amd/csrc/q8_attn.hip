@@ -159,7 +159,8 @@ struct Wave {
   }
 
   // Softmax step over the scores (s becomes probabilities); unseen keys hold
-  // -infinity.
+  // -infinity.  The scores' scaling is not joined with the subtraction here: the
+  // largest one's exponent is then 0 however large it is.
   __device__ __forceinline__ void soften(float *s) {
     float mx = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])),
                      fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
@@ -170,6 +171,7 @@ struct Wave {
     float ps = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+#pragma clang fp contract(off)
       s[j] = exp2_fast(s[j] - mn);
       ps += s[j];
     }

@@ -440,11 +440,16 @@ attn_rows_kernel(AttnArgs a) {
 #pragma unroll
     for (int T = 0; T < NB; ++T) o[T] *= alpha;
   };
+  // A score is rounded as the maximum was before they are subtracted, so that the
+  // largest one's exponent is 0 (or up to kSlack) however large it is: in one fma
+  // the maximum's own rounding stays, from scores of 2^31 on more than an
+  // exponent holds, and a row became zeros or NaN (8192 rows 500 us against 513).
   auto exponentials = [&](int n, float *p) Q8_INLINE {
     float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      p[e] = exp2_fast(fmaf(x[n][e], scale, -m));
+#pragma clang fp contract(off)
+      p[e] = exp2_fast(x[n][e] * scale - m);
       ps[e & 3] += p[e];
     }
     l += (ps[0] + ps[1]) + (ps[2] + ps[3]);

@@ -181,6 +181,74 @@ def test_scales_of_either_sign(fmt):
     check_rows(s, 4, [50, 1, 20, 3], scale=4.0, big=16.0)
 
 
+def leading(s, i, positions, score, window, sinks):
+    """The mean value of the seen tokens of the largest score: what the softmax of scores too far apart
+    to share leaves.  score: one number a token."""
+    t = np.arange(s.lens[i])
+    out = np.zeros((len(positions), s.lay.heads, s.lay.dim))
+    for j, p in enumerate(positions):
+        see = t <= p
+        if window:
+            see &= (t > p - window) | (t < sinks)
+        out[j] = s.v[i][see & (score == score[see].max())].mean(0)
+    return out
+
+
+def check_far_scores(fmt, dim, scales):
+    """Scores of the scales' size and either sign: the largest of a row counts in full, so equal ones share
+    evenly and smaller ones, this far apart, count nothing.  Every token's key is +-1.015625 in dim 0 and 0
+    elsewhere, the queries 1.0078125 there, so a product has bits that its fp32 score rounds away.
+
+    All tokens that count have the same probability, rounded to bf16 once; the values are whole numbers to
+    127, so a sum of n of them is off by at most n roundings of it; the output is rounded once."""
+    r = np.random.default_rng(dim)
+    lens, counts, group = [1, 2, 40, 700], [1, 2, 33, 300], 4
+    odd = [None, None, 3, 399]                     # a token of the other sign, near its sequence's first rows
+    for far in (False, True):
+        s = u.Scene(fmt, 2, dim, 16, lens, seed=dim)
+        score = []
+        for i, l in enumerate(lens):
+            v = r.integers(-100, 101, (l, 2, dim)).astype(np.float32)
+            v[..., ::32] = 127.0                   # Q8_0 codes are the values
+            s.v[i] = s.put("v", i, v)
+            k = np.zeros((l, 2, dim), np.float32)
+            k[..., 0] = 1.015625
+            if far and odd[i] is not None:
+                k[odd[i], :, 0] = -1.015625
+            s.k[i] = s.put("k", i, k)
+            score.append(np.sign(k[:, 0, 0]))
+        s.to_device()
+        m = sum(counts)
+        q = torch.zeros((m, 2 * group, dim), dtype=torch.bfloat16, device=g.DEV)
+        q[..., 0] = 1.0078125
+        start = g.dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+        for scale in scales:
+            for sign in (1, -1):
+                for window, sinks in ((0, 0), (40, 3)):
+                    attn = q8.make_attn(sign * scale, window, sinks)
+                    o, one = torch.zeros_like(q), torch.zeros_like(q[:4])
+                    u.rows(s, q, start, attn, o)
+                    u.decode(s, q[:4], attn, one)
+                    torch.cuda.synchronize()
+                    for got, rows in ((u.host(o), counts), (u.host(one), [1] * 4)):
+                        at = 0
+                        for i, c in enumerate(rows):
+                            pos = np.arange(lens[i] - c, lens[i])
+                            want = np.repeat(leading(s, i, pos, sign * score[i], window, sinks), group, 1)
+                            tol = np.abs(want) * u.HALF_BF16 * (2 + u.HALF_BF16) + (lens[i] + 8) * 127 * u.EPS32
+                            err = np.abs(got[at:at + c] - want)
+                            assert (err <= tol).all(), (far, sign * scale, window, i, c, float(np.nanmax(err)))
+                            at += c
+
+
+@pytest.mark.parametrize("fmt", [BF16, Q8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scores_of_any_size(fmt, dim):
+    """Also scores whose fp32 rounding is many powers of two."""
+    check_far_scores(fmt, dim, (3e6, 7e7, 1e9, 3e15, 1e38))
+
+
+
 def poison(s, which, i, first, end, kind):
     """Bytes of tokens first .. end of sequence i: NaN, infinities or the types' largest values."""
     buf = s.kbuf if which == "k" else s.vbuf
