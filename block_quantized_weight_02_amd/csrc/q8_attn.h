@@ -12,7 +12,8 @@ namespace {
 
 using namespace dev;
 
-constexpr float kLowest = -3.0e38f;   // below every score's running maximum, and finite
+// Where a running maximum starts: finite, and no finite score is below it.
+constexpr float kLowest = -3.402823466e38f;
 
 // A value all lanes hold alike, in a scalar register.
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }

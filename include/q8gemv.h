@@ -672,11 +672,11 @@ int q8_kv_gather(const q8_kv_cache *cache /* host pointer */, const int32_t *slo
  *     o[h] = sum_t softmax_t(scale * q[h] . k_t) v_t
  * the scores, softmax statistics and sums in fp32; the probabilities enter the
  * value product rounded to bf16 (times the value scale in a Q8_0 cache).  A
- * row that sees no token gets zeros.  Tokens not seen are not part of the
- * result whatever their cache bytes hold.  A length below 0 counts as 0, one
- * above max_pages * page as that; tokens on a page index outside 0 .. n_pages
- * - 1 are not seen.  Requires max_pages * page <= 2^30, n * max_pages <= 2^31 - 1
- * and n * max_pages * page <= 2^35.
+ * row that sees no token, or only scores of -infinity, gets zeros.  Tokens not
+ * seen are not part of the result whatever their cache bytes hold.  A length
+ * below 0 counts as 0, one above max_pages * page as that; tokens on a page
+ * index outside 0 .. n_pages - 1 are not seen.  Requires max_pages * page <=
+ * 2^30, n * max_pages <= 2^31 - 1 and n * max_pages * page <= 2^35.
  *
  * q is m x q_heads x head_dim bf16.  The output is written as o (m x q_heads *
  * head_dim bf16, may be NULL) and/or o_q8 (its quantized form from the fp32

@@ -248,6 +248,13 @@ def test_scores_of_any_size(fmt, dim):
     check_far_scores(fmt, dim, (3e6, 7e7, 1e9, 3e15, 1e38))
 
 
+@pytest.mark.parametrize("fmt", [BF16, Q8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scores_near_the_lowest(fmt, dim):
+    """Rows whose every score, in powers of two, lies between -3.4e38 and -3e38."""
+    check_far_scores(fmt, dim, (2.2e38,))
+
+
 
 def poison(s, which, i, first, end, kind):
     """Bytes of tokens first .. end of sequence i: NaN, infinities or the types' largest values."""
@@ -263,6 +270,26 @@ def poison(s, which, i, first, end, kind):
         for b in range(4):
             buf[sc + b] = np.float32(value).view(np.uint32) >> (8 * b) & 255
         buf[at] = 127
+
+
+@pytest.mark.parametrize("fmt", [BF16, Q8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scores_of_minus_infinity(fmt, dim):
+    """Tokens with such scores count nothing; rows that see no others get zeros."""
+    s = u.Scene(fmt, 2, dim, 16, [70, 300], seed=dim)
+    poison(s, "k", 0, 0, 70, "ninf")
+    poison(s, "k", 1, 0, 250, "ninf")
+    s.k[1][:250] = 0.0
+    s.to_device()
+    counts, seen = [40, 100], [np.zeros(70, bool), np.arange(300) >= 250]
+    q = np.ones((140, 8, dim))
+    o, one = (torch.full((r, 8, dim), 7.0, dtype=torch.bfloat16, device=g.DEV) for r in (140, 2))
+    attn = q8.make_attn(dim ** -0.5)
+    u.rows(s, u.bf16_dev(q), g.dev(np.array([0, 40, 140], np.int32)), attn, o)
+    u.decode(s, u.bf16_dev(q[:2]), attn, one)
+    u.compare(u.host(o), want_of(s, q, counts, dim ** -0.5, present=seen), 300, dim, "rows")
+    u.compare(u.host(one), want_rows(s, q[:2], dim ** -0.5, 0, 0, seen), 300, dim, "decode")
+    assert (u.host(o)[:90] == 0).all() and (u.host(one)[0] == 0).all()
 
 
 @pytest.mark.parametrize("fmt", [BF16, Q8])
