@@ -453,6 +453,32 @@ def test_rows_window(fmt, window, sinks):
     check_rows(s, 2, [400], window, sinks)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(300, 0), (300, 70), (512, 4), (1000, 0), (1000, 130)])
+def test_rows_long_window(dim, window, sinks):
+    """Windows that leave whole stages of keys between their edge and a block's first row, behind first
+    tokens that are kept: a few rows split along the tokens, and enough blocks that each takes its whole
+    window."""
+    s = u.Scene(BF16, 2, dim, 16, [1500, 3000], seed=window + sinks).to_device()
+    check_rows(s, 4, [130, 70], window, sinks)
+    s = u.Scene(BF16, 8, dim, 64, [1700], seed=window).to_device()
+    assert s.workspace(523, 64)[1] == 0
+    check_rows(s, 8, [520], window, sinks)
+
+
+@pytest.mark.parametrize("fmt", [BF16, Q8])
+def test_rows_one_long_among_many(fmt):
+    """A mixed step: single rows of many short sequences, one of a long one, and a chunk of a prompt."""
+    r = np.random.default_rng(13)
+    lens = r.integers(1, 60, 33).tolist()
+    lens[20], lens[30] = 9001, 400
+    counts = [1] * 33
+    counts[7], counts[30] = 0, 150
+    s = u.Scene(fmt, 2, 128, 16, lens, seed=14).to_device()
+    check_rows(s, 4, counts)
+    check_rows(s, 4, counts, 500, 4)
+
+
 def test_rows_many_sequences():
     r = np.random.default_rng(3)
     lens = r.integers(0, 30, 500)
