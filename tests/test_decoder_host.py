@@ -244,3 +244,20 @@ def test_workspace_sizes():
     assert q8.q8_attn_workspace_bytes(16, 1, 30, c) == 0           # invalid
     assert q8.q8_attn_workspace_bytes(16, 0, 32, c) == 0
     assert q8.q8_attn_workspace_bytes(-1, 1, 32, c) == 0
+
+
+@built
+@pytest.mark.parametrize("fmt,dim,mib", [(0, 64, 37), (0, 128, 37), (0, 256, 69), (1, 64, 102), (1, 128, 102),
+                                         (1, 256, 69)])
+def test_workspace_of_any_call(fmt, dim, mib):
+    """What serves every rows call, as the header says; and decode's grows with the sequences."""
+    for kv_heads in (1, 2, 3, 5, 8, 16, 31, 128):
+        c = cache(fmt=fmt, kv_heads=kv_heads, head_dim=dim)
+        for group in (1, 4, 5, 8, 33, 1024):
+            if kv_heads * group > 1024:
+                continue
+            for m in (1, 2, 3, 8, 17, 32, 64, 127, 128, 129, 256, 257, 500, 512, 1024, 2048, 8192):
+                for n in (1, 2, 3, 8, 15, 16, 31, 33, 64, 127, 128, 256, 1500, 8192):
+                    assert q8.q8_attn_workspace_bytes(m, n, kv_heads * group, c) <= mib << 20, (m, n)
+            sizes = [q8.q8_attn_workspace_bytes(0, n, kv_heads * group, c) for n in (1, 2, 33, 1000, 8192)]
+            assert sizes == sorted(sizes) and sizes[0] > 4 << 20
