@@ -514,6 +514,47 @@ def test_one_row_of_either_call(fmt):
     assert np.abs(u.host(o) - a).max() <= 4 * u.HALF_BF16 * max(np.abs(v).max() for v in s.v)
 
 
+@pytest.mark.parametrize("fmt", [BF16, Q8])
+def test_pages_past_4_gib(fmt):
+    """A cache of 5 GiB a buffer: the attentions, the heads' rows and rows read back equal those of a small
+    cache of the same pages."""
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GiB of device memory")
+    hkv, group, dim, page = 4, 4, 128, 256
+    s = u.Scene(fmt, hkv, dim, page, [700, 513, 30], seed=7, spare=1).to_device()
+    per_page = s.lay.nbytes(1)
+    pages = (5 << 30) // per_page
+    far = np.linspace(pages - 1, pages // 2, s.pages).astype(np.int64)   # where each page goes
+    big = [torch.empty(pages * per_page, dtype=torch.uint8, device=g.DEV) for _ in "kv"]
+    for b, small in zip(big, (s.kd, s.vd)):
+        for i, p in enumerate(far):
+            b[p * per_page:(p + 1) * per_page] = small[i * per_page:(i + 1) * per_page]
+    cache = q8.make_kv_cache(*big, pages, fmt, hkv, dim, page)
+    table = g.dev(np.where(s.table >= 0, far[s.table], -1).astype(np.int32))
+    q = u.bf16_dev(queries(s, 93, group, 5))
+    start = g.dev(np.array([0, 40, 63, 93], np.int32))
+    x = torch.randn((37, (hkv * group + 2 * hkv) * dim), device=g.DEV)
+    ld, free = x.shape[1], int(s.free[0])
+    heads = q8.make_heads(None, None, 0.0, None, 0, 0)
+    pos = torch.zeros(37, dtype=torch.int32, device=g.DEV)
+    outs = []
+    for c, t, at in ((s.cache, s.table_d, free), (cache, table, int(far[free]))):
+        slots = g.dev(np.array([at * page + 3 + i for i in range(37)], np.int32))
+        o, one, qo = torch.zeros_like(q), torch.zeros_like(q[:3]), torch.zeros_like(q[:37])
+        back = [torch.zeros((37, hkv, dim), dtype=torch.bfloat16, device=g.DEV) for _ in "kv"]
+        ws = s.workspace(93, hkv * group), s.workspace(0, hkv * group)
+        q8.q8_attn_rows(q, 93, hkv * group, c, t, s.max_pages, s.lens_d, start, 3, q8.make_attn(0.09), o, None, None,
+                        *ws[0])
+        q8.q8_attn_decode(q, hkv * group, c, t, s.max_pages, s.lens_d, 3, q8.make_attn(0.09), one, None, None, *ws[1])
+        q8.q8_qkv_heads(x, ld, x[:, hkv * group * dim:], ld, x[:, hkv * (group + 1) * dim:], ld, 37, hkv * group, heads,
+                        pos, slots, qo, c)
+        q8.q8_kv_gather(c, slots, 37, *back)
+        torch.cuda.synchronize()
+        outs.append((o, one, qo, *back))
+    for a, b in zip(*outs):
+        assert a.any() and torch.equal(a, b)
+
+
 # ---- streams, graphs, workspaces ------------------------------------------------------------------
 
 def test_two_streams():
