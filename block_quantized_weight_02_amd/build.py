@@ -22,7 +22,8 @@ SOURCES = ["q8_kernels.hip", "q8_mfma32.hip", "q8_tile16.hip", "q8_gemm.hip", "q
            "q8_kv_api.cpp"]
 # Per-source device flags.  The GEMM and the attentions write their MFMA results
 # to VGPRs (by default the compiler routes them through one AGPR quad and
-# serialises the matrix core behind its reads).
+# serialises the matrix core behind its reads); what does not fit there, as the
+# row attention's sums of 256 dims, is kept in AGPRs and copied.
 SOURCE_FLAGS = {s: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
                 for s in ("q8_gemm.hip", "q8_attn.hip", "q8_attn_rows.hip")}
 ARCH = os.environ.get("Q8_OFFLOAD_ARCH", "gfx950")

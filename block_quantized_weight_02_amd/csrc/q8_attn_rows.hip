@@ -16,7 +16,10 @@ constexpr int kListGroups = 512;        // 16-token groups whose pages are held 
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 
 // Waves of a workgroup, 32 columns each: eight (two a SIMD, in turns, below)
-// where their registers allow it and the stages need no widening.
+// where their registers allow it (not at 256 dims) and the stages need no
+// widening.  Over Q8_0 four, of which a CU holds two workgroups that do not wait
+// for each other: 128 dims, 3 x 509 rows behind 4096 tokens 153 us, 2048 rows
+// 101; with eight 173 and 101 at as many splits, 184 and 112 at twice as many.
 template <int D, int FMT> constexpr int kWaves = FMT == Q8_KV_BF16 && D < 256 ? 8 : 4;
 template <int D, int FMT> constexpr int kCols = 32 * kWaves<D, FMT>;
 
@@ -132,14 +135,16 @@ __host__ __device__ constexpr int record_floats(int cols, int dim) { return cols
 // one's keys) while the other turns its scores into probabilities.
 //
 // Measured on MI355X, 8192 rows of 32 heads over 8, 128 dims, bf16, behind 0
-// tokens: 520 us, 1.06 PFLOP/s of 1.3 that a large library product reaches; four
+// tokens: 516 us, 1.07 PFLOP/s of 1.3 that a large library product reaches; four
 // waves in step with the maximum raised inside the loop took 627, stages through
 // registers 658.  Bound by LDS reads: a half's products take 128 KB of
-// fragments a turn, 1560 cycles at 85 bytes a clock, against 1340 for the other
+// fragments a turn, 1560 cycles at 85 bytes a clock, against 1470 for the other
 // half's probabilities.  Stages of 32 keys took 697 us against 633, waves of 64
-// columns spilled.  Q8_0, 3 x 509 rows behind 4096 tokens: 152 us; the codes are
+// columns spilled.  Q8_0, 3 x 509 rows behind 4096 tokens: 155 us; the codes are
 // widened once a stage and each 32 dims' scores scaled, so the vector unit bounds
-// it.
+// it.  256 dims: 2048 rows 164 us, 0.42 PFLOP/s; four waves, one a SIMD, with
+// nothing beside their waits, and sums that move between the two halves of the
+// register file around each product.
 constexpr float kSlack = 8.0f;
 
 template <int D, int FMT>
@@ -796,10 +801,17 @@ int64_t blocks_bound(int64_t m, int64_t n, int64_t group, int cols) {
 
 // Key splits: as many as keep the workgroups to one a CU (eight waves), two
 // (256 dims) or, over Q8_0, six: there each is short of work for its barriers,
-// and a CU holds two at a time.  Measured on MI355X (us; one, two, three times
-// these): 512 rows behind 4096 tokens 47, 66, 64; 2048 rows of 256 dims 224,
-// 224, 304; Q8_0 (a third, two thirds, these), 3 x 509 rows behind 4096 171, 176,
-// 152, 2048 rows 107, 109, 99.
+// and a CU holds two at a time.  Measured on MI355X (us; half, one, two, three
+// times these): 512 rows behind 4096 tokens 97, 54, 67, 67; 256 dims, 2048 rows
+// 164, 164, 163, 230, 512 rows behind 3000 181, 151, 186, 220; Q8_0 (a third, two
+// thirds, these, twice), 3 x 509 rows behind 4096 171, 177, 153, 161, 2048 rows
+// 110, 110, 101, 104.
+// The host knows m and n, not the lengths, so the rule counts every sequence's
+// last block as one more, and never gives more than kMaxSplits: one sequence of
+// few rows gets half of the workgroups it could use, and of many sequences none
+// is split, however long.  32 single rows over contexts of 1000 tokens and one
+// of 131072 take 2.8 ms, as the long one's tokens pass through eight workgroups
+// (of four such rows, 0.49 ms); all of them in q8_attn_decode 0.1 ms.
 int attn_rows_splits(int64_t m, int64_t n, int64_t q_heads, int64_t kv_heads, int64_t dim, int fmt) {
   const int cols = cols_of(dim, fmt), target = dim == 256 ? 512 : fmt == Q8_KV_BF16 ? 256 : 1536;
   const int64_t s = target / (blocks_bound(m, n, q_heads / kv_heads, cols) * kv_heads);
