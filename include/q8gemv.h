@@ -528,7 +528,9 @@ size_t q8_kv_bytes(int fmt, int64_t kv_heads, int64_t head_dim, int64_t page,
  * host round trip.  Per sequence i (all integers, P = page):
  *     rows_i = max(new_rows[i], 0)            held_i = ceil(lens[i] / P)
  *   - new_rows[i] < 0: the sequence ends.  Its held_i pages table[i][0..] are
- *     appended to free_pages (in sequence order), lens_out[i] = 0.
+ *     appended to free_pages (in sequence order), lens_out[i] = 0.  Pages are
+ *     not counted: one that several sequences' tables name is appended for each
+ *     that ends, and would be granted as often.
  *   - otherwise it needs ceil((lens[i] + rows_i) / P) - held_i new pages.  They
  *     are taken from the end of free_pages, in sequence order and page order
  *     (the pages of ended sequences included), and written to table[i][held_i
