@@ -331,20 +331,20 @@ def _prepare_own(s):
     c = s["case"]
     if c["op"] in ("mul", "pair"):
         k, n, zeros = c["k"], c["n"], c["zeros"]
-        fmt = q8.Q4_SCALE_F16 if c["scale"] == "f16" else q8.Q4_SCALE_BF16
+        fmt = q8.Q8_W4_SCALE_F16 if c["scale"] == "f16" else q8.Q8_W4_SCALE_BF16
         s["packed"] = []
         for u, scale, z in s["w"]:
-            values = torch.empty(q8.q4_values_bytes(k, n), dtype=torch.uint8, device=DEV)
-            scales = torch.empty(q8.q4_scales_bytes(k, n, c["group"], zeros), dtype=torch.uint8, device=DEV)
-            w = q8.make_q4_weight(values, scales, k, n, c["group"], fmt, zeros)
-            q8.q4_repack(u, scale, z, w)
+            values = torch.empty(q8.q8_w4_values_bytes(k, n), dtype=torch.uint8, device=DEV)
+            scales = torch.empty(q8.q8_w4_scales_bytes(k, n, c["group"], zeros), dtype=torch.uint8, device=DEV)
+            w = q8.make_w4_weight(values, scales, k, n, c["group"], fmt, zeros)
+            q8.q8_w4_repack(u, scale, z, w)
             s["packed"].append((w, values, scales))
         s["act"] = q8.Q8_ACT_BF16 if c["act"] == "bf16" else q8.Q8_ACT_Q8_0
         s["in"] = s["x"] if c["act"] == "bf16" else s["x_q8"]
         s["epilogue"] = q8.make_epilogue(s["bias"], s["residual"]) if c["extra"] else None
         s["need"] = 0
         if c["m"] <= q8.Q8_MAX_ROWS:
-            size = q8.q4_gemv_workspace_bytes if c["op"] == "mul" else q8.q4_glu_workspace_bytes
+            size = q8.q8_w4_gemv_workspace_bytes if c["op"] == "mul" else q8.q8_w4_glu_workspace_bytes
             s["need"] = size(c["m"], s["packed"][0][0], s["act"])
         s["ws"] = torch.zeros(max(16, s["need"]), dtype=torch.uint8, device=DEV)
     elif c["op"] == "rules":
@@ -367,16 +367,16 @@ def _own(s):
     if c["op"] == "mul":
         w = s["packed"][0][0]
         if c["m"] <= q8.Q8_MAX_ROWS:
-            q8.q4_gemv(s["in"], w, s["y"], c["m"], s["act"], s["epilogue"], None, s["ws"], s["need"])
+            q8.q8_w4_gemv(s["in"], w, s["y"], c["m"], s["act"], s["epilogue"], None, s["ws"], s["need"])
         else:
-            q8.q4_gemm(s["in"], w, s["y"], c["m"], s["act"])
+            q8.q8_w4_gemm(s["in"], w, s["y"], c["m"], s["act"])
         return s["y"]
     if c["op"] == "pair":
         g, u = s["packed"][0][0], s["packed"][1][0]
         if c["m"] <= q8.Q8_MAX_ROWS:
-            q8.q4_gemv_glu(s["in"], g, u, s["y"], c["m"], s["act"], None, None, s["ws"], s["need"])
+            q8.q8_w4_gemv_glu(s["in"], g, u, s["y"], c["m"], s["act"], None, None, s["ws"], s["need"])
         else:
-            q8.q4_gemm_glu(s["in"], g, u, s["y"], c["m"], s["act"])
+            q8.q8_w4_gemm_glu(s["in"], g, u, s["y"], c["m"], s["act"])
         return s["y"]
     if c["op"] == "rules":
         q8.q8_logits_rules(s["logits"], s["ld"], c["m"], c["vocab"], s["rules"], s["out"], s["ld"])
