@@ -40,6 +40,8 @@ Q8_ROPE_SCALE_NONE = 0
 Q8_ROPE_SCALE_LINEAR = 1
 Q8_ROPE_SCALE_TURNS = 2
 Q8_ROPE_SCALE_INDEX = 3
+Q8_W4_SCALE_F16 = 0
+Q8_W4_SCALE_BF16 = 1
 
 STATUS = {0: "Q8_OK", 1: "Q8_ERR_SHAPE", 2: "Q8_ERR_ACT_FMT", 3: "Q8_ERR_NULL",
           4: "Q8_ERR_ALIGN", 5: "Q8_ERR_WORKSPACE", 6: "Q8_ERR_HIP", 7: "Q8_ERR_PLAN"}
@@ -106,6 +108,12 @@ class q8_heads(ctypes.Structure):
 
 class q8_attn(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
+class q8_w4_weight(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("K", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("group", ctypes.c_int32), ("scale_fmt", ctypes.c_int32),
+                ("has_zeros", ctypes.c_int32)]
 
 
 _i64 = ctypes.c_int64
@@ -179,6 +187,19 @@ _SIGS = {
                               ctypes.POINTER(q8_attn), _p, _p, _p, _p, _sz]),
     "q8_attn_rows": (_int, [_p, _i64, _i64, ctypes.POINTER(q8_kv_cache), _p, _i64, _p, _p, _i64,
                             ctypes.POINTER(q8_attn), _p, _p, _p, _p, _sz]),
+    "q8_w4_values_bytes": (_sz, [_i64, _i64]),
+    "q8_w4_scales_bytes": (_sz, [_i64, _i64, _int, _int]),
+    "q8_w4_repack": (_int, [_p, _p, _p, ctypes.POINTER(q8_w4_weight), _p]),
+    "q8_w4_unpack": (_int, [ctypes.POINTER(q8_w4_weight), _p, _p, _p, _p]),
+    "q8_w4_gemv_workspace_bytes": (_sz, [_i64, ctypes.POINTER(q8_w4_weight), _int]),
+    "q8_w4_gemv": (_int, [_p, ctypes.POINTER(q8_w4_weight), _p, _i64, _int,
+                          ctypes.POINTER(q8_epilogue), _p, _p, _sz]),
+    "q8_w4_glu_workspace_bytes": (_sz, [_i64, ctypes.POINTER(q8_w4_weight), _int]),
+    "q8_w4_gemv_glu": (_int, [_p, ctypes.POINTER(q8_w4_weight), ctypes.POINTER(q8_w4_weight), _p,
+                              _i64, _int, ctypes.POINTER(q8_glu_epilogue), _p, _p, _sz]),
+    "q8_w4_gemm": (_int, [_p, ctypes.POINTER(q8_w4_weight), _p, _i64, _int, _p]),
+    "q8_w4_gemm_glu": (_int, [_p, ctypes.POINTER(q8_w4_weight), ctypes.POINTER(q8_w4_weight), _p,
+                              _i64, _int, ctypes.POINTER(q8_glu_epilogue), _p]),
 }
 
 _lib = None
@@ -442,6 +463,60 @@ def q8_gemm(x, W_q8, W_q8_scale, y, m, K, N, act_fmt, stream=None) -> None:
 def q8_gemm_block_dots(x_q8, W_q8, dots, m, K, N, stream=None) -> None:
     _check(lib().q8_gemm_block_dots(_addr(x_q8), _addr(W_q8), _addr(dots), m, K, N,
                                     _stream(stream)))
+
+
+# ---- 4-bit weights -----------------------------------------------------------------
+
+def q8_w4_values_bytes(K: int, N: int) -> int:
+    return int(lib().q8_w4_values_bytes(K, N))
+
+
+def q8_w4_scales_bytes(K: int, N: int, group: int, has_zeros) -> int:
+    return int(lib().q8_w4_scales_bytes(K, N, group, 1 if has_zeros else 0))
+
+
+def make_w4_weight(values, scales, K, N, group, scale_fmt=Q8_W4_SCALE_F16,
+                   has_zeros=False) -> q8_w4_weight:
+    """A ``q8_w4_weight`` over two device tensors (or raw addresses)."""
+    return q8_w4_weight(_addr(values), _addr(scales), K, N, group, scale_fmt, 1 if has_zeros else 0)
+
+
+def q8_w4_repack(u_kn, s_kn, z_kn, W: q8_w4_weight, stream=None) -> None:
+    _check(lib().q8_w4_repack(_addr(u_kn), _addr(s_kn), _addr(z_kn), _ref(W), _stream(stream)))
+
+
+def q8_w4_unpack(W: q8_w4_weight, u_kn, s_kn, z_kn, stream=None) -> None:
+    _check(lib().q8_w4_unpack(_ref(W), _addr(u_kn), _addr(s_kn), _addr(z_kn), _stream(stream)))
+
+
+def q8_w4_gemv_workspace_bytes(m, W: q8_w4_weight, act_fmt) -> int:
+    return int(lib().q8_w4_gemv_workspace_bytes(m, _ref(W), act_fmt))
+
+
+def q8_w4_gemv(x, W: q8_w4_weight, y, m, act_fmt, epilogue: q8_epilogue = None, stream=None,
+               workspace=None, ws_bytes=0) -> None:
+    _check(lib().q8_w4_gemv(_addr(x), _ref(W), _addr(y), m, act_fmt, _ref(epilogue),
+                            _stream(stream), _addr(workspace), ws_bytes))
+
+
+def q8_w4_glu_workspace_bytes(m, W: q8_w4_weight, act_fmt) -> int:
+    return int(lib().q8_w4_glu_workspace_bytes(m, _ref(W), act_fmt))
+
+
+def q8_w4_gemv_glu(x, Wg: q8_w4_weight, Wu: q8_w4_weight, y, m, act_fmt,
+                   epilogue: q8_glu_epilogue = None, stream=None, workspace=None, ws_bytes=0) -> None:
+    _check(lib().q8_w4_gemv_glu(_addr(x), _ref(Wg), _ref(Wu), _addr(y), m, act_fmt, _ref(epilogue),
+                                _stream(stream), _addr(workspace), ws_bytes))
+
+
+def q8_w4_gemm(x, W: q8_w4_weight, y, m, act_fmt, stream=None) -> None:
+    _check(lib().q8_w4_gemm(_addr(x), _ref(W), _addr(y), m, act_fmt, _stream(stream)))
+
+
+def q8_w4_gemm_glu(x, Wg: q8_w4_weight, Wu: q8_w4_weight, y, m, act_fmt,
+                   epilogue: q8_glu_epilogue = None, stream=None) -> None:
+    _check(lib().q8_w4_gemm_glu(_addr(x), _ref(Wg), _ref(Wu), _addr(y), m, act_fmt, _ref(epilogue),
+                                _stream(stream)))
 
 
 # ---- between the projections ------------------------------------------------------

@@ -66,6 +66,7 @@ struct Epi {
   int8_t *yq;
   float *yq_scale;
   int8_t *yq_view;       // the quantized output's block-interleaved view (with yq)
+  int view_rows;         // rows of that view, where the launch's m is a chunk of them (0: m)
   int N;
   int write_y;
   int nw;                // weights: 1, or 2 for the gated pair

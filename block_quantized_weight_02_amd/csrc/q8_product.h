@@ -61,7 +61,7 @@ __device__ __forceinline__ void store_final(const Epi &ep, float *__restrict__ y
     const float d = q8_scale_of(a);
     const int8_t c = q8_code_of(z, d);
     ep.yq[(size_t)r * Npad + col] = c;
-    ep.yq_view[((col / 32) * m + r) * 32 + (col & 31)] = c;
+    ep.yq_view[((col / 32) * (ep.view_rows ? ep.view_rows : m) + r) * 32 + (col & 31)] = c;
     if ((col & 31) == 0) ep.yq_scale[(size_t)r * (Npad / 32) + col / 32] = d;
   }
 }
@@ -238,13 +238,14 @@ __device__ __forceinline__ void finish_tile(const float *red, const TileOut &o,
 // summed in order; with one split the gate is applied here, otherwise both
 // weights' partials are published and the last of the tile's S arrivals sums
 // each weight's S partials in split order (the protocol of finish_tile).
-template <int MR, int W>
+// NT: the workgroup's threads, as there.
+template <int MR, int W, int NT = 64 * W>
 __device__ __forceinline__ void finish_pair_tile(const float *red, const TileOut &o,
                                                  float *__restrict__ partial,
                                                  unsigned *__restrict__ counters, int m, int s,
                                                  int S, const Epi &ep) {
   constexpr int WH = W / 2;
-  for (int idx = threadIdx.x; idx < MR * 64; idx += 64 * W) {
+  for (int idx = threadIdx.x; idx < MR * 64; idx += NT) {
     const int r = idx >> 6, c = idx & 63;
     if (r < m) {
       float vg = red[idx], vu = red[WH * MR * 64 + idx];
@@ -276,7 +277,7 @@ __device__ __forceinline__ void finish_pair_tile(const float *red, const TileOut
                        ? 1 : 0;
   __syncthreads();
   if (!is_last_pair) return;
-  for (int idx = threadIdx.x; idx < MR * 64; idx += 64 * W) {
+  for (int idx = threadIdx.x; idx < MR * 64; idx += NT) {
     const int r = idx >> 6, c = idx & 63;
     if (r < m) {
       const float vg = sum_partials(partial, m, o.pstride, S, 0, r, o.pcol0 + c);

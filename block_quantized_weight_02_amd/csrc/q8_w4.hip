@@ -1,0 +1,130 @@
+// q8_w4.hip -- a 4-bit weight into its packed layout and back (q8_w4.h).  Both move
+// each byte once: a thread takes one dword of values (eight rows of a column), the
+// columns side by side over the lanes.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q8_w4.h"
+
+namespace q8 {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct W4Dims {
+  int64_t N, NB, T, NG, NGp;   // NG: groups of the canonical form
+  int group;
+};
+
+// Value dword d of the packed weight: tile, block, rows 8q .., column.
+__device__ __forceinline__ void value_place(int64_t d, const W4Dims &w, int64_t &row2, int64_t &n,
+                                            int64_t &at) {
+  const int c = (int)(d & 63), q = (int)(d >> 6) & 3;
+  const int64_t tb = d >> 8, t = tb / w.NB, b = tb - t * w.NB;
+  n = t * kTile + c;
+  row2 = b * 16 + q * 4;        // row pairs
+  at = tb * kW4Chunk + (16 * q + (c & 15)) * 16 + (c >> 4) * 4;
+}
+
+__global__ void __launch_bounds__(kThreads)
+w4_repack_kernel(const uint8_t *__restrict__ u, const uint16_t *__restrict__ s,
+                 const uint8_t *__restrict__ z, char *__restrict__ values,
+                 uint16_t *__restrict__ scales, uint8_t *__restrict__ zeros, W4Dims w) {
+  const int64_t nv = w.T * w.NB * 256, ns = w.T * w.NGp * kTile;
+  for (int64_t d = (int64_t)blockIdx.x * kThreads + threadIdx.x; d < nv + ns;
+       d += (int64_t)gridDim.x * kThreads) {
+    if (d < nv) {
+      int64_t row2, n, at;
+      value_place(d, w, row2, n, at);
+      uint32_t word = 0;
+      if (n < w.N) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t byte = u[(row2 + p) * w.N + n];
+          word |= (byte & 15u) << (4 * p) | (byte >> 4) << (16 + 4 * p);
+        }
+      }
+      *reinterpret_cast<uint32_t *>(values + at) = word;
+    } else {
+      const int64_t e = d - nv, t = e / (w.NGp * kTile), in = e - t * (w.NGp * kTile);
+      const int64_t j = in / kTile;
+      const int c = (int)(in & 63);
+      const int64_t n = t * kTile + c;
+      const bool live = n < w.N && j < w.NG;
+      const int64_t at = t * w.NGp * kTile + w4_scale_pos(j, c, w.group);
+      scales[at] = live ? s[j * w.N + n] : (uint16_t)0;
+      if (zeros) zeros[at] = live ? z[j * w.N + n] : (uint8_t)0;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+w4_unpack_kernel(const char *__restrict__ values, const uint16_t *__restrict__ scales,
+                 const uint8_t *__restrict__ zeros, uint8_t *__restrict__ u,
+                 uint16_t *__restrict__ s, uint8_t *__restrict__ z, W4Dims w) {
+  const int64_t nv = w.T * w.NB * 256, ns = w.T * w.NGp * kTile;
+  for (int64_t d = (int64_t)blockIdx.x * kThreads + threadIdx.x; d < nv + ns;
+       d += (int64_t)gridDim.x * kThreads) {
+    if (d < nv) {
+      int64_t row2, n, at;
+      value_place(d, w, row2, n, at);
+      if (n >= w.N) continue;
+      const uint32_t word = *reinterpret_cast<const uint32_t *>(values + at);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        u[(row2 + p) * w.N + n] =
+            (uint8_t)((word >> (4 * p) & 15u) | (word >> (16 + 4 * p) & 15u) << 4);
+    } else {
+      const int64_t e = d - nv, t = e / (w.NGp * kTile), in = e - t * (w.NGp * kTile);
+      const int64_t j = in / kTile;
+      const int c = (int)(in & 63);
+      const int64_t n = t * kTile + c;
+      if (n >= w.N || j >= w.NG) continue;
+      const int64_t at = t * w.NGp * kTile + w4_scale_pos(j, c, w.group);
+      s[j * w.N + n] = scales[at];
+      if (zeros) z[j * w.N + n] = zeros[at];
+    }
+  }
+}
+
+W4Dims dims(int64_t K, int64_t N, int group) {
+  W4Dims w;
+  w.N = N;
+  w.NB = K / kBlock;
+  w.T = (N + kTile - 1) / kTile;
+  w.NG = (K + group - 1) / group;
+  w.NGp = w4_groups(K, group);
+  w.group = group;
+  return w;
+}
+
+unsigned grid(const W4Dims &w) {
+  const int64_t n = (w.T * w.NB * 256 + w.T * w.NGp * kTile + kThreads - 1) / kThreads;
+  return (unsigned)(n < (1 << 20) ? n : (1 << 20));   // a thread takes several past that
+}
+
+}  // namespace
+
+hipError_t launch_w4_repack(const uint8_t *u, const uint16_t *s, const uint8_t *z, int64_t K,
+                            int64_t N, int group, char *values, char *scales, char *zeros,
+                            hipStream_t stream) {
+  const W4Dims w = dims(K, N, group);
+  (void)hipGetLastError();
+  w4_repack_kernel<<<grid(w), kThreads, 0, stream>>>(u, s, z, values,
+                                                     reinterpret_cast<uint16_t *>(scales),
+                                                     reinterpret_cast<uint8_t *>(zeros), w);
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_unpack(const char *values, const char *scales, const char *zeros, int64_t K,
+                            int64_t N, int group, uint8_t *u, uint16_t *s, uint8_t *z,
+                            hipStream_t stream) {
+  const W4Dims w = dims(K, N, group);
+  (void)hipGetLastError();
+  w4_unpack_kernel<<<grid(w), kThreads, 0, stream>>>(values,
+                                                     reinterpret_cast<const uint16_t *>(scales),
+                                                     reinterpret_cast<const uint8_t *>(zeros), u, s, z, w);
+  return hipGetLastError();
+}
+
+}  // namespace q8

@@ -468,6 +468,86 @@ int q8_gemm_block_dots(const void *x_q8, const int8_t *W_q8, int32_t *dots,
 int q8_gemm_parts(const void *x, const q8_part *parts, int n_parts, int64_t m,
                   int64_t K, int act_fmt, hipStream_t stream);
 
+/* ---- 4-bit weights ------------------------------------------------------------ */
+
+/*
+ * The products over a weight of 4 bits a value: K x N values u of 0 .. 15, and per
+ * group of 32, 64 or 128 rows of a column one scale s (fp16 or bf16) and, where the
+ * weight has them, one zero point z (a byte; any of 0 .. 255):
+ *     w[k,n] = s[j,n] * (u[k,n] - z[j,n]),  j = k / group,  z = 8 without zero points
+ * The last group may be shorter.  K > 0, K % 32 == 0, N >= 1, limits as above.
+ *
+ * Canonical form: u_kn, K/2 x N bytes, row 2j of the weight in the low four bits of
+ * row j and row 2j + 1 in the high ones; s_kn, ceil(K/group) x N 16-bit patterns;
+ * z_kn, ceil(K/group) x N bytes.  q8_w4_repack brings it into the packed layout,
+ * library-private: q8_w4_values_bytes and q8_w4_scales_bytes (zero points among
+ * them) bytes, all written.  Half a byte a value, and 2 (with zero points 3) bytes a
+ * scale, N padded to q8_padded_cols(N).
+ */
+typedef enum { Q8_W4_SCALE_F16 = 0, Q8_W4_SCALE_BF16 = 1 } q8_w4_scale_fmt;
+
+typedef struct q8_w4_weight {
+  void *values;       /* q8_w4_values_bytes(K, N) bytes                        */
+  void *scales;       /* q8_w4_scales_bytes(K, N, group, has_zeros) bytes      */
+  int64_t K;
+  int64_t N;
+  int32_t group;      /* rows a scale: 32, 64 or 128                           */
+  int32_t scale_fmt;  /* q8_w4_scale_fmt                                       */
+  int32_t has_zeros;  /* nonzero: zero points follow the scales                */
+} q8_w4_weight;
+
+/* Bytes of a packed weight's two buffers; 0 on a bad shape. */
+size_t q8_w4_values_bytes(int64_t K, int64_t N);
+size_t q8_w4_scales_bytes(int64_t K, int64_t N, int group, int has_zeros);
+
+/* Canonical -> packed, and back (the N real columns).  z_kn only with zero points
+ * (else it is not read or written and may be NULL). */
+int q8_w4_repack(const uint8_t *u_kn, const uint16_t *s_kn, const uint8_t *z_kn,
+                 const q8_w4_weight *W /* host pointer */, hipStream_t stream);
+int q8_w4_unpack(const q8_w4_weight *W /* host pointer */, uint8_t *u_kn, uint16_t *s_kn,
+                 uint8_t *z_kn, hipStream_t stream);
+
+/*
+ * q8_w4_gemv: y = x . W for 1 <= m <= 32 rows, with q8_gemv_fused's epilogue (NULL:
+ * y only), layouts and activation formats bf16 and Q8_0 (two words: Q8_ERR_ACT_FMT).
+ * The sums are fp32: bf16 activations are multiplied exactly and added in fp32, a
+ * group's sum is scaled once; Q8_0 activations' dots are exact int32 per 32 rows.
+ * An infinity or NaN in a row of a bf16 activation makes that row's outputs NaN or
+ * infinite, no other row's.
+ *
+ * The workspace is the caller's, as in q8_gemv_ws: q8_w4_gemv_workspace_bytes(...)
+ * bytes, 16-byte aligned, NULL when that is 0; its first 4 MiB are counters, zero at
+ * the first use and left at zero (one zeroed workspace serves the products' and the
+ * attention's calls too); calls that share it must be ordered, graphs captured over
+ * it included.  Q8_ERR_WORKSPACE when too small.
+ */
+size_t q8_w4_gemv_workspace_bytes(int64_t m, const q8_w4_weight *W /* host pointer */, int act_fmt);
+int q8_w4_gemv(const void *x, const q8_w4_weight *W /* host pointer */, float *y, int64_t m,
+               int act_fmt, const q8_epilogue *epilogue /* host pointer */, hipStream_t stream,
+               void *workspace, size_t ws_bytes);
+
+/*
+ * q8_w4_gemv_glu: the gated pair silu(x . Wg + bias_g) * (x . Wu + bias_u) over two
+ * weights of the same K, N, group, scale_fmt and has_zeros (else Q8_ERR_SHAPE), in one
+ * launch, for 1 <= m <= 32 rows; epilogue as in q8_gemv_glu, workspace as above.
+ */
+size_t q8_w4_glu_workspace_bytes(int64_t m, const q8_w4_weight *W /* host pointer */, int act_fmt);
+int q8_w4_gemv_glu(const void *x, const q8_w4_weight *Wg /* host pointer */,
+                   const q8_w4_weight *Wu /* host pointer */, float *y, int64_t m, int act_fmt,
+                   const q8_glu_epilogue *epilogue /* host pointer */, hipStream_t stream,
+                   void *workspace, size_t ws_bytes);
+
+/*
+ * The same for 1 <= m <= Q8_MAX_GEMM_ROWS rows (a prompt's), without a workspace.
+ * q8_w4_gemm has no epilogue; q8_w4_gemm_glu takes the pair's, its quantized output
+ * being the next product's activation for all m rows.
+ */
+int q8_w4_gemm(const void *x, const q8_w4_weight *W /* host pointer */, float *y, int64_t m,
+               int act_fmt, hipStream_t stream);
+int q8_w4_gemm_glu(const void *x, const q8_w4_weight *Wg /* host pointer */,
+                   const q8_w4_weight *Wu /* host pointer */, float *y, int64_t m, int act_fmt,
+                   const q8_glu_epilogue *epilogue /* host pointer */, hipStream_t stream);
+
 /* ---- between the projections: head norms, rotation, cache, attention -------- */
 
 /*
