@@ -32,6 +32,7 @@ Q8_MAX_GEMM_ROWS = 8192
 Q8_MAX_PARTS = 4
 Q8_MAX_TWO_WORD_ROWS = 16
 Q8_MAX_SEQS = 8192
+Q8_MAX_VOCAB = 1 << 20
 Q8_KV_BF16 = 0
 Q8_KV_Q8_0 = 1
 Q8_ROPE_HALF = 0
@@ -114,6 +115,18 @@ class q8_w4_weight(ctypes.Structure):
     _fields_ = [("values", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("K", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("group", ctypes.c_int32), ("scale_fmt", ctypes.c_int32),
                 ("has_zeros", ctypes.c_int32)]
+
+
+class q8_logit_rules(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in
+                ("tokens", "lens", "prompt_lens", "repetition", "presence", "frequency",
+                 "bias_start", "bias_token", "bias_value", "mask", "mask_row")] + \
+               [("ld_tokens", ctypes.c_int64), ("bias_entries", ctypes.c_int64),
+                ("ld_mask", ctypes.c_int64), ("mask_rows", ctypes.c_int64)]
+
+
+class q8_sampling(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("temperature", "top_k", "top_p", "min_p", "u")]
 
 
 _i64 = ctypes.c_int64
@@ -200,6 +213,9 @@ _SIGS = {
     "q8_w4_gemm": (_int, [_p, ctypes.POINTER(q8_w4_weight), _p, _i64, _int, _p]),
     "q8_w4_gemm_glu": (_int, [_p, ctypes.POINTER(q8_w4_weight), ctypes.POINTER(q8_w4_weight), _p,
                               _i64, _int, ctypes.POINTER(q8_glu_epilogue), _p]),
+    "q8_logits_rules": (_int, [_p, _i64, _i64, _i64, ctypes.POINTER(q8_logit_rules), _p, _i64, _p]),
+    "q8_sample_workspace_bytes": (_sz, [_i64, _i64]),
+    "q8_sample": (_int, [_p, _i64, _i64, _i64, ctypes.POINTER(q8_sampling), _p, _p, _p, _p, _sz]),
 }
 
 _lib = None
@@ -594,6 +610,42 @@ def q8_attn_rows(q, m, q_heads, cache: q8_kv_cache, table, max_pages, lens, row_
     _check(lib().q8_attn_rows(_addr(q), m, q_heads, _ref(cache), _addr(table), max_pages,
                               _addr(lens), _addr(row_start), n, _ref(attn), _addr(o),
                               _addr(o_q8), _stream(stream), _addr(workspace), ws_bytes))
+
+
+# ---- from logits to tokens ---------------------------------------------------------
+
+def make_logit_rules(tokens=None, ld_tokens=0, lens=None, prompt_lens=None, repetition=None,
+                     presence=None, frequency=None, bias_start=None, bias_token=None,
+                     bias_value=None, bias_entries=None, mask=None, ld_mask=0, mask_row=None,
+                     mask_rows=0) -> q8_logit_rules:
+    """A ``q8_logit_rules`` over device tensors (or raw addresses, or None); ``bias_entries``
+    defaults to the elements of the tensor ``bias_token``."""
+    if bias_entries is None:
+        bias_entries = bias_token.numel() if hasattr(bias_token, "numel") else 0
+    return q8_logit_rules(*(_addr(t) for t in (tokens, lens, prompt_lens, repetition, presence,
+                                               frequency, bias_start, bias_token, bias_value, mask,
+                                               mask_row)),
+                          ld_tokens, bias_entries, ld_mask, mask_rows)
+
+
+def make_sampling(u, temperature=None, top_k=None, top_p=None, min_p=None) -> q8_sampling:
+    """A ``q8_sampling`` over device tensors (or raw addresses, or None)."""
+    return q8_sampling(_addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p), _addr(u))
+
+
+def q8_logits_rules(logits, ld, m, V, rules: q8_logit_rules, out, ld_out, stream=None) -> None:
+    _check(lib().q8_logits_rules(_addr(logits), ld, m, V, _ref(rules), _addr(out), ld_out,
+                                 _stream(stream)))
+
+
+def q8_sample_workspace_bytes(m, V) -> int:
+    return int(lib().q8_sample_workspace_bytes(m, V))
+
+
+def q8_sample(logits, ld, m, V, sampling: q8_sampling, token, logprob=None, stream=None,
+              workspace=None, ws_bytes=0) -> None:
+    _check(lib().q8_sample(_addr(logits), ld, m, V, _ref(sampling), _addr(token), _addr(logprob),
+                           _stream(stream), _addr(workspace), ws_bytes))
 
 
 def q8_status_string(status: int) -> str:

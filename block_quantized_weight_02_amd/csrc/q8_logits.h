@@ -1,0 +1,50 @@
+// q8_logits.h -- what the host side of the logits' calls (q8_logits_api.cpp) and
+// their kernels (q8_logits.hip: the rules; q8_sample.hip: the draw) share.
+#pragma once
+
+#include <stdint.h>
+
+#include <hip/hip_runtime.h>
+
+namespace q8 {
+
+struct LogitRules {
+  const int32_t *tokens;        // m x ld_tokens, or null
+  int64_t ld_tokens;
+  const int32_t *lens;          // m
+  const int32_t *prompt_lens;   // m, or null: 0
+  const float *repetition, *presence, *frequency;   // m each, or null
+  const int32_t *bias_start;    // m + 1, or null
+  const int32_t *bias_token;
+  const float *bias_value;
+  const uint32_t *mask;         // mask_rows x ld_mask words, or null
+  int64_t ld_mask;
+  const int32_t *mask_row;      // m, or null: row r's is r
+  int mask_rows;
+  int64_t n_bias;               // entries of bias_token and bias_value
+};
+
+struct LogitRulesArgs {
+  const float *logits;
+  float *out;
+  int64_t ld, ld_out;
+  int m, V;
+  LogitRules r;
+};
+hipError_t launch_logit_rules(const LogitRulesArgs &a, hipStream_t stream);
+
+struct SampleArgs {
+  const float *logits;
+  int64_t ld;
+  int m, V;
+  const float *temperature, *top_p, *min_p;   // m each, or null: 1, 1, 0
+  const int32_t *top_k;                       // m, or null: all
+  const double *u;                            // m
+  int32_t *token;
+  float *logprob;                             // m, or null
+};
+constexpr int kSampleTile = 1024;             // tokens a wave takes at a time
+constexpr int kMaxVocab = 1 << 20;
+hipError_t launch_sample(const SampleArgs &a, hipStream_t stream);
+
+}  // namespace q8

@@ -1,0 +1,153 @@
+// q8_logits.hip -- the rules on a step's logits: penalties of the tokens that a
+// request holds, biases and grammar masks, in one pass over the rows.
+//
+// A workgroup takes a slice of one row's vocabulary.  It walks the whole of the
+// row's history (from the caches: every slice's workgroup reads it) and counts, in
+// LDS, the tokens that fall into its slice, and notes the last bias entry of each;
+// then it reads, changes and writes the slice.  So no counts are kept between calls
+// and none leave the chip, and integer counts do not depend on the order of the
+// additions.  Bound by the rows' bytes, read once and written once; four tokens a
+// thread and load.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "q8_logits.h"
+
+namespace q8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxSlice = 4096;
+constexpr uint32_t kPrompt = 0x80000000u;   // the token stands in the prompt
+
+// HELD: rows may have a history; BIASED: biases.  Without either no LDS is used.
+template <bool HELD, bool BIASED>
+__global__ void __launch_bounds__(kThreads)
+logit_rules_kernel(const LogitRulesArgs a, int slice) {
+  __shared__ uint32_t count[HELD ? kMaxSlice : 1];
+  __shared__ int last[BIASED ? kMaxSlice : 1];
+  const int r = blockIdx.y, tid = threadIdx.x;
+  const int base = blockIdx.x * slice;
+  const int n = min(slice, a.V - base);
+  const LogitRules &u = a.r;
+
+  int held = 0, bias_lo = 0, bias_hi = 0;
+  if constexpr (HELD) held = (int)min((int64_t)max(u.lens[r], 0), u.ld_tokens);
+  if constexpr (BIASED) {
+    bias_lo = max(u.bias_start[r], 0);
+    bias_hi = (int)min((int64_t)u.bias_start[r + 1], u.n_bias);
+  }
+  const bool any = (HELD && held > 0) || (BIASED && bias_hi > bias_lo);
+  if (any) {
+    for (int i = tid; i < n; i += kThreads) {
+      if constexpr (HELD) count[i] = 0;
+      if constexpr (BIASED) last[i] = -1;
+    }
+    __syncthreads();
+    if constexpr (HELD) {
+      const int prompt = u.prompt_lens ? u.prompt_lens[r] : 0;
+      const int32_t *tok = u.tokens + (size_t)r * u.ld_tokens;
+      for (int j0 = tid; j0 < held; j0 += 4 * kThreads) {
+        int t[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) t[c] = tok[min(j0 + c * kThreads, held - 1)];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int j = j0 + c * kThreads;
+          const int64_t at = (int64_t)t[c] - base;
+          if (j < held && at >= 0 && at < n) {
+            if (j >= prompt)
+              atomicAdd(&count[at], 1u);
+            else
+              atomicOr(&count[at], kPrompt);
+          }
+        }
+      }
+    }
+    if constexpr (BIASED) {
+      for (int j = bias_lo + tid; j < bias_hi; j += kThreads) {
+        const int64_t at = (int64_t)u.bias_token[j] - base;
+        if (at >= 0 && at < n) atomicMax(&last[at], j);
+      }
+    }
+    __syncthreads();
+  }
+
+  const float rep = HELD && u.repetition ? u.repetition[r] : 1.0f;
+  const float pres = HELD && u.presence ? u.presence[r] : 0.0f;
+  const float freq = HELD && u.frequency ? u.frequency[r] : 0.0f;
+  const uint32_t *mask = nullptr;
+  if (u.mask) {
+    const int mr = u.mask_row ? u.mask_row[r] : r;
+    if (mr >= 0 && mr < u.mask_rows) mask = u.mask + (size_t)mr * u.ld_mask;
+  }
+  const float *in = a.logits + (size_t)r * a.ld + base;
+  float *out = a.out + (size_t)r * a.ld_out + base;
+  const bool in_place = in == out;
+  for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+    const int live = min(4, n - i);
+    uint32_t allowed = 15u;
+    if (mask) allowed = mask[(base + i) >> 5] >> ((base + i) & 31) & 15u;
+    uint32_t cnt[4] = {0, 0, 0, 0};
+    int bias[4] = {-1, -1, -1, -1};
+    bool touched = allowed != 15u;
+    if (any) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < live) {
+          if constexpr (HELD) cnt[c] = count[i + c];
+          if constexpr (BIASED) bias[c] = last[i + c];
+          touched |= cnt[c] != 0 || bias[c] >= 0;
+        }
+    }
+    if (in_place && !touched) continue;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (allowed) v = *reinterpret_cast<const float4 *>(in + i);   // (a row's stride is whole fours)
+    float x[4] = {v.x, v.y, v.z, v.w};
+    if (touched) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if constexpr (HELD) {
+          if (cnt[c]) {
+            if (rep != 1.0f) x[c] = x[c] > 0.0f ? x[c] / rep : x[c] * rep;
+            const uint32_t made = cnt[c] & ~kPrompt;
+            if (made) x[c] = x[c] - freq * (float)made - pres;
+          }
+        }
+        if constexpr (BIASED)
+          if (bias[c] >= 0) x[c] += u.bias_value[bias[c]];
+        if (!(allowed >> c & 1u)) x[c] = -INFINITY;
+      }
+    }
+    if (live == 4) {
+      *reinterpret_cast<float4 *>(out + i) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+      for (int c = 0; c < live; ++c) out[i + c] = x[c];
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_logit_rules(const LogitRulesArgs &a, hipStream_t stream) {
+  // the largest slice that still gives two workgroups a CU; a smaller one reads the
+  // histories more often
+  int slice = kMaxSlice;
+  while (slice > 1024 && (int64_t)a.m * ((a.V + slice - 1) / slice) < 512) slice /= 2;
+  const dim3 grid((unsigned)((a.V + slice - 1) / slice), (unsigned)a.m);
+  (void)hipGetLastError();
+  const bool held = a.r.tokens != nullptr, biased = a.r.bias_start != nullptr;
+  if (held && biased)
+    logit_rules_kernel<true, true><<<grid, kThreads, 0, stream>>>(a, slice);
+  else if (held)
+    logit_rules_kernel<true, false><<<grid, kThreads, 0, stream>>>(a, slice);
+  else if (biased)
+    logit_rules_kernel<false, true><<<grid, kThreads, 0, stream>>>(a, slice);
+  else
+    logit_rules_kernel<false, false><<<grid, kThreads, 0, stream>>>(a, slice);
+  return hipGetLastError();
+}
+
+}  // namespace q8

@@ -810,6 +810,89 @@ int q8_attn_rows(const uint16_t *q, int64_t m, int64_t q_heads,
                  int64_t n, const q8_attn *attn /* host pointer */, uint16_t *o,
                  void *o_q8, hipStream_t stream, void *workspace, size_t ws_bytes);
 
+/* ---- from logits to tokens ---------------------------------------------------- */
+
+/*
+ * What follows a step's last product: its rows of logits (m x ld fp32, V real
+ * columns; a product's y as it is, ld = N_pad) under the requests' rules, and the
+ * token that each draws.  1 <= m <= Q8_MAX_GEMM_ROWS, 1 <= V <= Q8_MAX_VOCAB, ld a
+ * multiple of 4 and at least V.
+ */
+#define Q8_MAX_VOCAB (1 << 20)
+
+/*
+ * q8_logits_rules: out[r, t] from logits[r, t], per row r and token t < V, in this
+ * order, each rule where its pointer is given:
+ *   - repetition: l / f where l > 0, else l * f (f = repetition[r]), if t is among
+ *     the row's tokens;
+ *   - frequency and presence: l - frequency[r] * c - presence[r], if t is c > 0 times
+ *     among the tokens the row made: those from prompt_lens[r] on;
+ *   - bias: l + value of the last of the entries bias_start[r] .. bias_start[r+1]-1
+ *     whose token is t;
+ *   - mask: -infinity where bit t % 32 of word t / 32 of mask row mask_row[r] is 0
+ *     (a row of -1, or any outside 0 .. mask_rows - 1: no mask).
+ * In fp32 (a value past its range becomes infinite).  A row's tokens are tokens[r * ld_tokens + 0 .. lens[r] - 1]; lengths below
+ * 0 count as 0, above ld_tokens as that; tokens outside 0 .. V - 1 (of a history or a
+ * bias) are ignored.  Entries past bias_entries are not read.  Columns V .. ld_out - 1
+ * stay as they were.  out may be logits (then ld_out = ld; only what a rule changes is
+ * read and written), else it must not overlap it.
+ */
+typedef struct q8_logit_rules {
+  const int32_t *tokens;      /* m x ld_tokens, or NULL: no penalties            */
+  const int32_t *lens;        /* m; with tokens                                  */
+  const int32_t *prompt_lens; /* m, or NULL: 0 (every token was made)            */
+  const float *repetition;    /* m, or NULL: 1                                   */
+  const float *presence;      /* m, or NULL: 0                                   */
+  const float *frequency;     /* m, or NULL: 0                                   */
+  const int32_t *bias_start;  /* m + 1, or NULL: no biases                       */
+  const int32_t *bias_token;  /* bias_entries                                    */
+  const float *bias_value;    /* bias_entries                                    */
+  const uint32_t *mask;       /* mask_rows x ld_mask words, or NULL: no masks    */
+  const int32_t *mask_row;    /* m, or NULL: row r's is r (mask_rows >= m)       */
+  int64_t ld_tokens;
+  int64_t bias_entries;
+  int64_t ld_mask;            /* words, at least ceil(V / 32)                    */
+  int64_t mask_rows;
+} q8_logit_rules;
+
+int q8_logits_rules(const float *logits, int64_t ld, int64_t m, int64_t V,
+                    const q8_logit_rules *rules /* host pointer */, float *out, int64_t ld_out,
+                    hipStream_t stream);
+
+/*
+ * q8_sample: token[r] of each row, and the log-probability of it, in fp32,
+ *     logprob[r] = l[token] - log sum_t exp(l[t])      (over the whole row, T = 1)
+ * With T = temperature[r] > 0 a token weighs w = exp((l - max l) / T).  In the order of
+ * falling l, the lower index first among equal ones (-0 is +0), a limit keeps a prefix:
+ *   top_k  the first top_k[r] tokens (<= 0: all);
+ *   top_p  the tokens whose predecessors weigh less than top_p[r] of the whole row's
+ *          weight (>= 1: all; the first always);
+ *   min_p  the tokens of w >= min_p[r] (<= 0: all; above 1 counts as 1).
+ * Each limit is taken over the whole row, and the shortest prefix is kept.  The token is
+ * the lowest t whose kept tokens 0 .. t weigh more than u[r] times the kept weight,
+ * u[r] in [0, 1) (numbers outside count as the nearer end, NaN as 0).  Weights are
+ * whole multiples of 2^-min(51, 62 - ceil(log2(V + 1))) of the largest, computed to
+ * 1e-13 and summed exactly, so a token does not depend on the order of additions; ones
+ * that round to 0 are not drawn.  T <= 0 (or NaN): the largest logit, the lowest index
+ * among equal ones.  NaN and -infinity have no weight; a row of nothing else gets token
+ * -1 and log-probability -infinity.  Among logits of +infinity only those are drawn.
+ *
+ * q8_sample_workspace_bytes: bytes of the caller's workspace (may be 0, then NULL is
+ * fine), 16-byte aligned.
+ */
+typedef struct q8_sampling {
+  const float *temperature; /* m, or NULL: 1                                     */
+  const int32_t *top_k;     /* m, or NULL                                        */
+  const float *top_p;       /* m, or NULL                                        */
+  const float *min_p;       /* m, or NULL                                        */
+  const double *u;          /* m uniform numbers                                 */
+} q8_sampling;
+
+size_t q8_sample_workspace_bytes(int64_t m, int64_t V);
+int q8_sample(const float *logits, int64_t ld, int64_t m, int64_t V,
+              const q8_sampling *sampling /* host pointer */, int32_t *token, float *logprob,
+              hipStream_t stream, void *workspace, size_t ws_bytes);
+
 /* ---- errors and resources ------------------------------------------------ */
 
 /* Static name of a status code. */

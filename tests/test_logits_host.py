@@ -1,0 +1,85 @@
+"""The logits' calls on the host: the arguments they refuse before any device work, and the oracle."""
+import math
+import os
+
+import numpy as np
+import pytest
+
+import block_quantized_weight_02_amd as q8
+from block_quantized_weight_02_amd import binding
+from oracle import logits as ol
+
+pytestmark = pytest.mark.skipif(not os.path.exists(binding.LIB_PATH), reason="libq8gemv.so not built")
+
+A, S0 = 1 << 20, 0     # an aligned address that is never read; the null stream, never reached
+
+
+def refuse(status, fn, *args, part=""):
+    with pytest.raises(q8.Q8Error) as e:
+        fn(*args)
+    assert e.value.status == status, e.value
+    assert part in e.value.message
+
+
+def rules(logits=A, ld=128, m=2, v=100, r=None, out=A + 4096, ld_out=128, **fields):
+    r = q8.make_logit_rules(**fields) if r is None else r
+    q8.q8_logits_rules(logits, ld, m, v, r, out, ld_out, S0)
+
+
+def sample(logits=A, ld=128, m=2, v=100, token=A, logprob=A, ws=None, **fields):
+    q8.q8_sample(logits, ld, m, v, q8.make_sampling(fields.pop("u", A), **fields), token, logprob, S0, ws, 0)
+
+
+@pytest.mark.parametrize("call", [rules, sample])
+def test_sizes_are_refused(call):
+    for bad, part in ((dict(m=0), "m ="), (dict(m=8193), "m ="), (dict(v=0), "V ="), (dict(v=-1), "V ="),
+                      (dict(v=(1 << 20) + 1, ld=1 << 21), "V ="), (dict(ld=99), "ld ="), (dict(ld=102), "ld ="),
+                      (dict(ld=1 << 32), "ld =")):
+        refuse(1, lambda b=bad: call(**b), part=part)
+    refuse(3, lambda: call(logits=None), part="logits")
+    refuse(4, lambda: call(logits=A + 4), part="logits")
+
+
+def test_rules_refuse():
+    refuse(1, lambda: rules(ld_out=100 - 4), part="ld_out")
+    refuse(1, lambda: rules(out=A, ld_out=256), part="in place")
+    refuse(3, lambda: rules(out=None), part="out")
+    refuse(3, lambda: q8.q8_logits_rules(A, 128, 2, 100, None, A + 4096, 128, S0), part="rules")
+    refuse(3, lambda: rules(tokens=A, ld_tokens=4), part="lens")
+    refuse(1, lambda: rules(tokens=A, lens=A), part="ld_tokens")
+    for k in ("repetition", "presence", "frequency"):
+        refuse(3, lambda k=k: rules(**{k: A}), part="tokens")
+        refuse(4, lambda k=k: rules(tokens=A, lens=A, ld_tokens=4, **{k: A + 4}), part=k)
+    refuse(4, lambda: rules(tokens=A, lens=A, ld_tokens=4, prompt_lens=A + 8), part="prompt_lens")
+    refuse(1, lambda: rules(bias_start=A, bias_entries=-1), part="bias_entries")
+    refuse(3, lambda: rules(bias_start=A, bias_entries=3), part="bias_token")
+    refuse(3, lambda: rules(bias_start=A, bias_entries=3, bias_token=A), part="bias_value")
+    refuse(1, lambda: rules(mask=A, ld_mask=3, mask_rows=2), part="ld_mask")
+    refuse(1, lambda: rules(mask=A, ld_mask=4, mask_rows=1), part="mask_rows")
+    refuse(1, lambda: rules(mask=A, ld_mask=4, mask_rows=-1, mask_row=A), part="mask_rows")
+
+
+def test_sample_refuses():
+    refuse(3, lambda: sample(u=None), part="u is NULL")
+    refuse(3, lambda: sample(token=None), part="token")
+    refuse(3, lambda: q8.q8_sample(A, 128, 2, 100, None, A, A, S0), part="sampling")
+    for k in ("temperature", "top_k", "top_p", "min_p", "u", "token", "logprob", "ws"):
+        refuse(4, lambda k=k: sample(**{k: A + 4}))
+
+
+def test_oracle_of_the_rules():
+    x = np.array([1.0, -1.0, 2.0, 3.0, 4.0], np.float32)
+    y, _ = ol.rules(x, [0, 1, 3, 3, 9, -1], 2, 2.0, 0.5, 0.25, [(2, 1.0), (2, 5.0), (7, 1.0)], np.array([0b01111]))
+    np.testing.assert_array_equal(y, [0.5, -2.0, 7.0, 1.5 - 0.5 - 0.5, -math.inf])
+
+
+def test_oracle_of_the_draw():
+    x = np.log(np.array([0.1, 0.4, 0.2, 0.3])).astype(np.float32)
+    assert [ol.sample(x, u) for u in (0.05, 0.2, 0.6, 0.9)] == [{0}, {1}, {2}, {3}]
+    assert ol.sample(x, 0.99, top_k=2) == {3} and ol.sample(x, 0.5, top_k=2) == {1}
+    assert ol.sample(x, 0.99, top_p=0.39) == {1} and ol.sample(x, 0.99, top_p=0.41) == {3}
+    assert ol.sample(x, 0.0, min_p=0.6) == {1} and ol.sample(x, 0.99, min_p=0.6) == {3}
+    assert ol.sample(x, 0.3, temperature=0.0) == {1}
+    assert ol.sample(np.full(4, -np.inf, np.float32), 0.5) == {-1}
+    assert ol.sample(np.zeros(4, np.float32), 0.25) == {0, 1}          # on the boundary itself
+    assert ol.logprob(x, 1) == pytest.approx(math.log(0.4), abs=1e-6)
