@@ -19,15 +19,15 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libq8gemv.so")
 SOURCES = ["q8_kernels.hip", "q8_mfma32.hip", "q8_tile16.hip", "q8_gemm.hip", "q8_measure.hip",
            "q8_noalloc.hip", "q8_kv.hip", "q8_attn.hip", "q8_attn_rows.hip", "q8_w4.hip",
-           "q8_w4_bf16.hip", "q8_w4_q8.hip", "q8_logits.hip", "q8_sample.hip", "q8_api.cpp",
-           "q8_kv_api.cpp", "q8_w4_api.cpp", "q8_logits_api.cpp"]
+           "q8_w4_bf16.hip", "q8_w4_q8.hip", "q8_w4_gemm.hip", "q8_logits.hip", "q8_sample.hip",
+           "q8_api.cpp", "q8_kv_api.cpp", "q8_w4_api.cpp", "q8_logits_api.cpp"]
 # Per-source device flags.  The GEMM, the attentions and the 4-bit products write their MFMA results
 # to VGPRs (by default the compiler routes them through one AGPR quad and
 # serialises the matrix core behind its reads); what does not fit there, as the
 # row attention's sums of 256 dims, is kept in AGPRs and copied.
 SOURCE_FLAGS = {s: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
                 for s in ("q8_gemm.hip", "q8_attn.hip", "q8_attn_rows.hip", "q8_w4_bf16.hip",
-                          "q8_w4_q8.hip")}
+                          "q8_w4_q8.hip", "q8_w4_gemm.hip")}
 ARCH = os.environ.get("Q8_OFFLOAD_ARCH", "gfx950")
 
 

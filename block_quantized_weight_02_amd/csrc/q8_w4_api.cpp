@@ -147,6 +147,14 @@ int run_tile(W4Args &a, int act_fmt, bool pair, int splits, int64_t m, hipStream
   return done(launch(tile_rows(m), pair, a, stream), "4-bit product launch");
 }
 
+// Many rows: the GEMM, or the tile kernel in chunks of 64 rows.
+bool gemm_route(int64_t m, int64_t N, bool pair) { return m > 64; }
+
+int run_many(W4Args &a, int act_fmt, bool pair, hipStream_t stream) {
+  if (!gemm_route(a.m, a.ep.N, pair)) return run_tile(a, act_fmt, pair, 1, a.m, stream, nullptr, 0);
+  return done(launch_w4_gemm(act_fmt, pair, a, stream), "4-bit product launch");
+}
+
 int check_pair_args(const void *x, const q8_w4_weight *Wg, const q8_w4_weight *Wu, const float *y,
                     int64_t m, int64_t most, int act_fmt, const q8_glu_epilogue *ep, W4 *g, W4 *u) {
   int st;
@@ -266,7 +274,7 @@ int q8_w4_gemm(const void *x, const q8_w4_weight *W, float *y, int64_t m, int ac
     return st;
   W4Args a = args_of(x, W, y, m, act_fmt);
   a.w = w;
-  return run_tile(a, act_fmt, false, 1, m, stream, nullptr, 0);
+  return run_many(a, act_fmt, false, stream);
 }
 
 int q8_w4_gemm_glu(const void *x, const q8_w4_weight *Wg, const q8_w4_weight *Wu, float *y, int64_t m,
@@ -275,7 +283,7 @@ int q8_w4_gemm_glu(const void *x, const q8_w4_weight *Wg, const q8_w4_weight *Wu
   const int st = check_pair_args(x, Wg, Wu, y, m, Q8_MAX_GEMM_ROWS, act_fmt, epilogue, &g, &u);
   if (st) return st;
   W4Args a = pair_args(x, Wg, g, u, y, m, act_fmt, epilogue);
-  return run_tile(a, act_fmt, true, 1, m, stream, nullptr, 0);
+  return run_many(a, act_fmt, true, stream);
 }
 
 }  // extern "C"

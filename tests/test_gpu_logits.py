@@ -153,9 +153,9 @@ def draw(x, u, temperature=None, top_k=None, top_p=None, min_p=None, logprob=Tru
     ld = ld_of(v)
     rows = np.full((m, ld), 1e30, np.float32)      # past V nothing counts
     rows[:, :v] = x
-    f = lambda a: None if a is None else g.dev(np.broadcast_to(np.asarray(a, np.float32), m))  # noqa: E731
-    keep = [g.dev(rows), g.dev(np.broadcast_to(np.asarray(u, np.float64), m)), f(temperature),
-            None if top_k is None else g.dev(np.broadcast_to(np.asarray(top_k, np.int32), m)), f(top_p), f(min_p)]
+    f = lambda a: None if a is None else g.dev(np.array(np.broadcast_to(np.asarray(a, np.float32), m)))  # noqa: E731
+    keep = [g.dev(rows), g.dev(np.array(np.broadcast_to(np.asarray(u, np.float64), m))), f(temperature),
+            None if top_k is None else g.dev(np.array(np.broadcast_to(np.asarray(top_k, np.int32), m))), f(top_p), f(min_p)]
     token = torch.full((m,), -9, dtype=torch.int32, device=g.DEV)
     lp = torch.full((m,), float("nan"), device=g.DEV) if logprob else None
     need = q8.q8_sample_workspace_bytes(m, v)
@@ -339,6 +339,6 @@ def test_a_step_from_activation_to_token_captured():
             slack = 1.3 * (a.times(w)[1][i] + 2.0 ** -23 * np.abs(a.times(w)[0][i]))
             fine = np.isfinite(want)
             np.testing.assert_array_equal(np.isfinite(y[i]), fine)
-            assert (np.abs(y[i] - want)[fine] <= (off + slack)[fine]).all()
+            assert (np.abs(y[i][fine] - want[fine]) <= (off + slack)[fine]).all()
         tokens.scatter_(1, lens.long()[:, None], out[1][:, None])      # the drawn token joins the history
         lens += 1

@@ -171,12 +171,14 @@ def pair_tolerance(gate, up, bg, bu):
     return out, worst, spread
 
 
+PAIRS = [(1, 32, 1, 32, False, 0), (1, 4096, 1000, 64, False, 0), (4, 1056, 130, 128, True, 1),
+         (16, 2048, 9000, 32, True, 0), (29, 1024, 200, 64, True, 1), (32, 512, 64, 128, False, 0),
+         (40, 512, 300, 32, False, 1), (128, 1024, 200, 128, True, 0), (257, 288, 520, 64, False, 0)]
+
+
 @pytest.mark.parametrize("act", [BF16, Q8])
-@pytest.mark.parametrize("many", [False, True])
-@pytest.mark.parametrize("m,K,N,group,zeros,fmt", [
-    (1, 32, 1, 32, False, 0), (1, 4096, 1000, 64, False, 0), (4, 1056, 130, 128, True, 1),
-    (16, 2048, 9000, 32, True, 0), (29, 1024, 200, 64, True, 1), (32, 512, 64, 128, False, 0),
-    (40, 512, 300, 32, False, 1), (128, 1024, 200, 128, True, 0), (257, 288, 520, 64, False, 0)])
+@pytest.mark.parametrize("m,K,N,group,zeros,fmt,many", [(*p, b) for p in PAIRS for b in (False, True)
+                                                        if b or p[0] <= q8.Q8_MAX_ROWS])
 def test_pair(m, K, N, group, zeros, fmt, many, act):
     wg, wu = (Weight(K, N, group, zeros, fmt, s).pack() for s in (47, 53))
     a = Act(m, K, act, 59)
