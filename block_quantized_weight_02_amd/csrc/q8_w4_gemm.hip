@@ -262,6 +262,9 @@ w4_gemm_kernel(const W4Args a, int MB, int NBN) {
         for (int g = 0; g < 4; ++g) asm volatile("" : "+v"(acc[rg][g]));
       };
       read(0);
+      // products before other waves' conversions: the SIMD's two waves then take turns
+      // (2048 rows, K 4096, N 14336: 249 -> 222 us)
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int rg = 0; rg < kRG; ++rg) {
         const int p = rg & 1;
@@ -291,8 +294,18 @@ w4_gemm_kernel(const W4Args a, int MB, int NBN) {
           if (rg + 1 < kRG) read(rg + 1);
           if (rg > 0) scale(rg - 1);
         }
+        if constexpr (!kQ8 && CH == 2) {
+          // operand reads first, then two FMAs behind each matrix instruction
+          if (rg + 1 < kRG) __builtin_amdgcn_sched_group_barrier(0x100, CH, 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+          }
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_s_setprio(0);
       scale(kRG - 1);
     }
   };
