@@ -25,6 +25,7 @@
 #include "q8_device.h"
 #include "q8_product.h"
 #include "q8_w4.h"
+#include "q8_w4_device.h"
 
 namespace q8 {
 namespace {
@@ -42,14 +43,6 @@ constexpr int kDx = kCB * kRows * 4;       // staged activation scales (Q8_0)
 // p ^ (row / 2 % 4): the operand read (lane (q, i): part q of row i) and the staging
 // writes spread over all LDS banks.
 __device__ __forceinline__ int a_place(int r, int p) { return (p ^ ((r >> 1) & 3)) * 16; }
-
-// 16 bytes a lane straight into LDS at `at` + 16 lane (wave-uniform `at`).  Written out
-// because the compiler would make every read of LDS wait for every such load; m0, the
-// load's base in LDS, is a register that the compiler sets right before its own uses.
-__device__ __forceinline__ void load_to_lds(const char *base, unsigned off, unsigned at) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               ::"v"(off), "s"(base), "s"(at) : "memory");
-}
 
 // Eight nibbles -> bf16 (u - 8) / 16, plus `add` where there are zero points
 // ((8 - z) / 16: then (u - z) / 16).
@@ -114,7 +107,7 @@ w4_gemm_kernel(const W4Args a, int MB, int NBN) {
   // bf16: a wave loads 16 rows x 64 bytes at a time straight into LDS, lane L place
   // L % 4 of row L / 4; 4 such pieces a wave and stage.  Rows past m: the last row.
   constexpr int kPieces = kA / 1024 / 4;
-  const unsigned lds0 = (unsigned)(size_t)(__attribute__((address_space(3))) char *)lds;
+  const unsigned lds0 = lds_offset(lds);
   unsigned aoff[kQ8 ? 1 : kPieces];
   const char *abase = static_cast<const char *>(a.x) + (size_t)row0 * a.K * (kQ8 ? 1 : 2);
   if constexpr (!kQ8) {
@@ -146,7 +139,7 @@ w4_gemm_kernel(const W4Args a, int MB, int NBN) {
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int piece = k * 4 + wave;
-        load_to_lds(base, aoff[k] - (piece >= kRG ? (unsigned)step : 0u),
+        load_to_lds16(base, aoff[k] - (piece >= kRG ? (unsigned)step : 0u),
                     lds0 + (unsigned)(buf * kStage + piece * 1024));
       }
     }
@@ -210,18 +203,9 @@ w4_gemm_kernel(const W4Args a, int MB, int NBN) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       float sc[4];
-      {
-        // (both conversions and a choice: a branch would end the straight line that the
-        // stage is scheduled in)
-        const uint32_t bits[4] = {st.sc[n].x & 0xffffu, st.sc[n].x >> 16, st.sc[n].y & 0xffffu, st.sc[n].y >> 16};
+      w4_scales4(st.sc[n], a.scale_bf16 ? ~0u : 0u, sc);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float h = (float)__builtin_bit_cast(_Float16, (unsigned short)bits[g]);
-          sc[g] = a.scale_bf16 ? __uint_as_float(bits[g] << 16) : h;
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) sc[g] *= 16.0f;
-      }
+      for (int g = 0; g < 4; ++g) sc[g] *= 16.0f;
       bf16x8_t bw[CH][4];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {

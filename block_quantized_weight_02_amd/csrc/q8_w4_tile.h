@@ -21,51 +21,39 @@
 //   * a group's blocks chain in one accumulator and are scaled once.
 //   * activation row 4 e + q sits in operand row 4 q + e, so that with up to 4 rows
 //     only the first of a lane's four results counts, and is scaled.
-// A wave has two stages in flight, taking turns in two register sets; the waves'
-// carries meet in LDS, the splits' through finish_tile.
+// A wave has two stages in flight, taking turns: the weight's in two register sets, the
+// activation's rows (and Q8_0 scales) loaded straight into two places in LDS of the
+// wave's own, so that the registers hold weight alone and no wave waits for another.
+// The waves' carries meet in LDS, the splits' through finish_tile.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "q8_device.h"
 #include "q8_internal.h"
 #include "q8_product.h"
 #include "q8_w4.h"
+#include "q8_w4_device.h"
 
 namespace q8 {
 namespace {
 
 using namespace dev;
 
-// A 16-bit scale's value.
-__device__ __forceinline__ float w4_scale(uint32_t bits, bool bf16) {
-  return bf16 ? __uint_as_float(bits << 16)
-              : (float)__builtin_bit_cast(_Float16, (unsigned short)bits);
-}
-__device__ __forceinline__ void w4_scales4(uint2 v, int bf16, float (&f)[4]) {
-  if (bf16) {
-    f[0] = bf16_lo(v.x);
-    f[1] = bf16_hi(v.x);
-    f[2] = bf16_lo(v.y);
-    f[3] = bf16_hi(v.y);
-  } else {
-    f[0] = w4_scale(v.x & 0xffffu, false);
-    f[1] = w4_scale(v.x >> 16, false);
-    f[2] = w4_scale(v.y & 0xffffu, false);
-    f[3] = w4_scale(v.y >> 16, false);
-  }
-}
-
-// Eight nibbles -> the bf16 numbers 16 + u, in row order.
-__device__ __forceinline__ bf16x8_t w4_bf16(uint32_t w) {
-  const uint32_t p0 = ((w << 3) & 0x00780078u) | 0x41804180u;
-  const uint32_t p1 = ((w >> 1) & 0x00780078u) | 0x41804180u;
-  const uint32_t p2 = ((w >> 5) & 0x00780078u) | 0x41804180u;
-  const uint32_t p3 = ((w >> 9) & 0x00780078u) | 0x41804180u;
-  return __builtin_bit_cast(bf16x8_t, make_uint4(p0, p1, p2, p3));
+// Eight nibbles -> the bf16 numbers 16 + u, in row order.  The constants are held in
+// registers that the compiler does not look into: written out, each would be a literal,
+// and the and-or two instructions.
+struct Bf16Consts {
+  uint32_t nibble = 0x00780078u, sixteen = 0x41804180u;
+  __device__ Bf16Consts() { asm("" : "+s"(nibble), "+v"(sixteen)); }
+};
+__device__ __forceinline__ bf16x8_t w4_bf16(uint32_t w, const Bf16Consts &k) {
+  return __builtin_bit_cast(bf16x8_t, make_uint4(((w << 3) & k.nibble) | k.sixteen, ((w >> 1) & k.nibble) | k.sixteen,
+                                                 ((w >> 5) & k.nibble) | k.sixteen, ((w >> 9) & k.nibble) | k.sixteen));
 }
 // Eight nibbles -> int8, rows 0,4,1,5 and 2,6,3,7.
 __device__ __forceinline__ long w4_i8(uint32_t w) {
@@ -86,17 +74,31 @@ constexpr int w4_lds_bytes(int W, int NW, int rows) {
   return (n < W / NW && first > n ? first : n) * NW * rows * 256;
 }
 
+// Blocks a stage, and the bytes of LDS that a stage's activation takes.
+constexpr int w4_stage_blocks(int RG) { return RG == 4 ? 2 : 4; }
+constexpr int w4_slot_x(int ACT, int RG, int EL) {
+  return EL < 4 ? 1024 : RG * w4_stage_blocks(RG) * (ACT == kActQ8 ? 512 : 1024);
+}
+constexpr int w4_slot(int ACT, int RG, int EL) {
+  return w4_slot_x(ACT, RG, EL) + (ACT == kActQ8 ? RG * 256 : 0);
+}
+constexpr int w4_lds(int ACT, int W, int RG, int EL, int NW) {
+  const int stages = 2 * W * w4_slot(ACT, RG, EL), carries = w4_lds_bytes(W, NW, w4_rows(RG, EL));
+  return stages > carries ? stages : carries;
+}
+
 template <int ACT, int W, int RG, int EL, int GB, bool ZEROS, bool PAIR>
 __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
   constexpr bool kQ8 = ACT == kActQ8;
   constexpr int MR = w4_rows(RG, EL);
   constexpr int NW = PAIR ? 2 : 1;
   constexpr int WK = W / NW;                 // waves that split a weight's K range
-  constexpr int QB = RG > 1 ? 2 : 4;         // blocks a stage (more rows: their operands fill the registers)
+  constexpr int QB = w4_stage_blocks(RG);
   constexpr int CH = GB < QB ? GB : QB;      // of them, blocks that share a scale
   constexpr int NS = QB / CH;                // scales a stage and column
-  __shared__ __attribute__((aligned(16))) char lds[w4_lds_bytes(W, NW, MR)];
-  float *red = reinterpret_cast<float *>(lds);
+  constexpr int kSlotX = w4_slot_x(ACT, RG, EL), kSlot = w4_slot(ACT, RG, EL);
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  float *const red = reinterpret_cast<float *>(lds);
 
   const int lane = threadIdx.x & 63;
   const int q = lane >> 4, i = lane & 15;
@@ -122,43 +124,77 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
   const buf_t zr = ZEROS ? make_buf(w.zeros + (size_t)t * groups * 64, groups * 64u) : wr;
   const unsigned lw = (unsigned)lane * 16u;
 
-  // operand row i of a group holds the activation's row 4 (i % 4) + i / 4; rows
-  // past the chunk load its first row, and their results are never read
-  const int ri = 4 * (i & 3) + (i >> 2);
-  unsigned xoff[RG];
-  const buf_t xr = kQ8 ? make_buf(static_cast<const char *>(a.x) + a.act_view_off,
-                                  (unsigned)a.m * (unsigned)a.K)
-                       : make_buf(static_cast<const char *>(a.x) + (size_t)r0 * a.K * 2,
-                                  (unsigned)mz * (unsigned)a.K * 2u);
+  // ---- the activation's stages.  Operand row o of a row group holds the activation's
+  // row 4 (o % 4) + o / 4 (with 4 rows in all, LDS holds just these); rows past the chunk
+  // load its last one, and their results are never read; blocks past K load the last.
+  const auto row_of = [&](int rg, int o) { return r0 + min(16 * rg + 4 * (o & 3) + (o >> 2), mz - 1); };
+  char *const mine = lds + (size_t)wave * 2 * kSlot;
+  const unsigned mine_at = __builtin_amdgcn_readfirstlane(lds_offset(mine));
+  const char *const xb = static_cast<const char *>(a.x) + (kQ8 ? a.act_view_off : 0u);
+  const char *const db = static_cast<const char *>(a.x) + a.act_scale_off;
+  constexpr int kRowLoads = EL < 4 ? 1 : RG;
+  unsigned xoff[kRowLoads], doff[kQ8 ? RG : 1];
+  // the lane's block within a load (bf16: one block a load; 4 rows: the whole stage's)
+  const int xu = kQ8 ? (EL < 4 ? (lane >> 3) & 3 : lane >> 5) : (EL < 4 ? lane >> 4 : 0);
+  const unsigned xstep = kQ8 ? (unsigned)a.m * 32u : 64u;
 #pragma unroll
-  for (int rg = 0; rg < RG; ++rg) {
-    const int r = 16 * rg + ri < mz ? 16 * rg + ri : 0;
-    xoff[rg] = kQ8 ? (unsigned)(r0 + r) * 32u + (unsigned)q * 8u
-                   : (unsigned)r * (unsigned)a.K * 2u + (unsigned)q * 16u;
+  for (int rg = 0; rg < kRowLoads; ++rg) {
+    if constexpr (kQ8) {
+      const int o = EL < 4 ? (lane >> 1) & 3 : (lane & 31) >> 1;
+      const int r = EL < 4 ? r0 + min(o, mz - 1) : row_of(rg, o);
+      xoff[rg] = (unsigned)r * 32u + (unsigned)(lane & 1) * 16u;
+    } else {
+      // 16-byte part p of a row's block is at place p ^ (row / 2 % 4), so that the
+      // operand reads spread over all LDS banks
+      const int o = EL < 4 ? (lane & 15) >> 2 : lane >> 2;
+      const int r = EL < 4 ? r0 + min(o, mz - 1) : row_of(rg, o);
+      xoff[rg] = (unsigned)(r - r0) * (unsigned)a.K * 2u + (unsigned)(((lane & 3) ^ ((o >> 1) & 3)) * 16);
+    }
   }
-  // int8: the scales of the rows whose results the lane holds
-  const buf_t dr = kQ8 ? make_buf(static_cast<const char *>(a.x) + a.act_scale_off,
-                                  (unsigned)a.m * (unsigned)a.NB * 4u) : xr;
-  unsigned doff[RG][EL];
   if constexpr (kQ8) {
 #pragma unroll
-    for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-      for (int e = 0; e < EL; ++e) {
-        const int r = min(16 * rg + 4 * e + q, mz - 1);
-        doff[rg][e] = (unsigned)(r0 + r) * (unsigned)a.NB * 4u;
-      }
+    for (int rg = 0; rg < RG; ++rg) doff[rg] = (unsigned)row_of(rg, lane & 15) * (unsigned)a.NB * 4u;
   }
+  const char *const xrow = kQ8 ? xb : xb + (size_t)r0 * a.K * 2;
+  const auto fetch = [&](int b, int slot) Q8_INLINE {
+    const unsigned at = mine_at + (unsigned)slot * kSlot;
+    const int last = a.NB - 1;
+    if constexpr (EL < 4) {
+      load_to_lds16(xrow, (unsigned)min(b + xu, last) * xstep + xoff[0], at);
+    } else if constexpr (kQ8) {
+#pragma unroll
+      for (int j = 0; j < QB / 2; ++j) {
+        const unsigned bo = (unsigned)min(b + 2 * j + xu, last) * xstep;
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) load_to_lds16(xrow, bo + xoff[rg], at + (j * RG + rg) * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < QB; ++u) {
+        const char *base = xrow + (size_t)min(b + u, last) * 64;
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) load_to_lds16(base, xoff[rg], at + (u * RG + rg) * 1024);
+      }
+    }
+    if constexpr (kQ8) {
+      const unsigned bo = (unsigned)min(b + (lane >> 4) % QB, last) * 4u;
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg) load_to_lds4(db, doff[rg] + bo, at + kSlotX + rg * 256);
+    }
+  };
+  // loads that a stage surely issues: what may be left when the one before is computed
+  constexpr int kFetch = (EL < 4 ? 1 : kQ8 ? RG * QB / 2 : RG * QB) + (kQ8 ? RG : 0);
+  constexpr int kStageLoads = kFetch + QB;
 
   struct Stage {
     uint4 v[QB];
     uint2 sc[NS];
     uint32_t z[NS];
-    uint4 xa[QB][RG];                  // int8: .xy
-    float dx[kQ8 ? RG : 1][kQ8 ? EL : 1][QB];
   };
-  auto load = [&](Stage &st, int bv) Q8_INLINE {
+  auto load = [&](Stage &st, int bv, int slot) Q8_INLINE {
     const int b = __builtin_amdgcn_readfirstlane(bv);
+    __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the slot's last reads have returned
+    fetch(b, slot);
 #pragma unroll
     for (int u = 0; u < QB; ++u) st.v[u] = buf_ld16(wr, lw, (unsigned)(b + u) * kW4Chunk);
     if constexpr (NS >= 2) {           // two groups a load
@@ -182,28 +218,6 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
       if constexpr (ZEROS)
         st.z[0] = __builtin_amdgcn_raw_buffer_load_b32(zr, (unsigned)i * (GB == 4 ? 4u : 8u), at / 2u, 0);
     }
-#pragma unroll
-    for (int u = 0; u < QB; ++u)
-#pragma unroll
-      for (int rg = 0; rg < RG; ++rg) {
-        if constexpr (kQ8) {
-          const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(
-              xr, xoff[rg], (unsigned)(b + u) * (unsigned)a.m * 32u, 0);
-          st.xa[u][rg] = make_uint4(v.x, v.y, 0u, 0u);
-        } else {
-          const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(xr, xoff[rg], (unsigned)(b + u) * 64u, 0);
-          st.xa[u][rg] = make_uint4(v.x, v.y, v.z, v.w);
-        }
-      }
-    if constexpr (kQ8) {
-#pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-        for (int e = 0; e < EL; ++e)
-#pragma unroll
-          for (int u = 0; u < QB; ++u)
-            st.dx[rg][e][u] = buf_ld4f(dr, doff[rg][e], (unsigned)(b + u) * 4u);
-    }
   };
 
   f32x4_t acc[RG][4];
@@ -212,14 +226,24 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) acc[rg][g] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
+  const Bf16Consts consts;
+  // the lane's operand bytes of block u, row group rg of a stage
+  const int xlane = kQ8 ? (EL < 4 ? (i >> 2) * 32 + q * 8 : i * 32 + q * 8)
+                        : (EL < 4 ? (i >> 2) * 64 + ((q ^ ((i >> 3) & 3)) * 16) : i * 64 + ((q ^ ((i >> 1) & 3)) * 16));
+  const auto x_at = [&](const char *slot, int u, int rg) Q8_INLINE {
+    if constexpr (EL < 4) return slot + u * (kQ8 ? 128 : 256) + xlane;
+    else if constexpr (kQ8) return slot + ((u >> 1) * RG + rg) * 1024 + (u & 1) * 512 + xlane;
+    else return slot + (u * RG + rg) * 1024 + xlane;
+  };
   // WHOLE: all of the stage's blocks are the range's (else the first nb)
-  auto compute = [&](auto whole, const Stage &st, int nb) Q8_INLINE {
+  auto compute = [&](auto whole, const Stage &st, int slot, int nb) Q8_INLINE {
     constexpr bool WHOLE = decltype(whole)::value;
+    const char *const xs = mine + slot * kSlot;
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       if (!WHOLE && n * CH >= nb) break;
       float sc[4];
-      w4_scales4(st.sc[n], a.scale_bf16, sc);
+      w4_scales4(st.sc[n], a.scale_bf16 ? ~0u : 0u, sc);
       if constexpr (kQ8) {
         float tt[RG][4][EL];
 #pragma unroll
@@ -229,10 +253,20 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
           const uint32_t wd[4] = {st.v[u].x, st.v[u].y, st.v[u].z, st.v[u].w};
 #pragma unroll
           for (int rg = 0; rg < RG; ++rg) {
-            const uint32_t x0 = st.xa[u][rg].x, x1 = st.xa[u][rg].y;
+            const uint2 xw = *reinterpret_cast<const uint2 *>(x_at(xs, u, rg));
             const long xv = __builtin_bit_cast(
-                long, make_uint2(__builtin_amdgcn_perm(x1, x0, 0x05010400u),
-                                 __builtin_amdgcn_perm(x1, x0, 0x07030602u)));
+                long, make_uint2(__builtin_amdgcn_perm(xw.y, xw.x, 0x05010400u),
+                                 __builtin_amdgcn_perm(xw.y, xw.x, 0x07030602u)));
+            // scales of rows 4e + q: places 4q + e
+            const float *dp = reinterpret_cast<const float *>(xs + kSlotX + rg * 256) + u * 16 + 4 * q;
+            float dx[EL];
+            if constexpr (EL == 4) {
+              const float4 v = *reinterpret_cast<const float4 *>(dp);
+              dx[0] = v.x; dx[1] = v.y; dx[2] = v.z; dx[3] = v.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < EL; ++e) dx[e] = dp[e];
+            }
             const long cst = ZEROS ? 0x0101010101010101l : (long)0xf8f8f8f8f8f8f8f8ul;
             const i32x4_t X = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, cst, i32x4_t{0, 0, 0, 0}, 0, 0, 0);
 #pragma unroll
@@ -246,11 +280,11 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
               const i32x4_t D = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, w4_i8(wd[g]), C, 0, 0, 0);
 #pragma unroll
               for (int e = 0; e < EL; ++e) {
-                const float d = (float)D[e], dx = st.dx[rg][e][u];
+                const float d = (float)D[e];
                 if constexpr (CH == 1)
-                  acc[rg][g][e] = fmaf(dx * sc[g], d, acc[rg][g][e]);
+                  acc[rg][g][e] = fmaf(dx[e] * sc[g], d, acc[rg][g][e]);
                 else
-                  tt[rg][g][e] = c == 0 ? dx * d : fmaf(dx, d, tt[rg][g][e]);
+                  tt[rg][g][e] = c == 0 ? dx[e] * d : fmaf(dx[e], d, tt[rg][g][e]);
               }
             }
           }
@@ -267,15 +301,20 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
         // -24 (16 + the 8 that u stands above), or 1 where zero points are given
         const uint32_t cw = ZEROS ? 0x3f803f80u : 0xc1c0c1c0u;
         const bf16x8_t cst = __builtin_bit_cast(bf16x8_t, make_uint4(cw, cw, cw, cw));
+        bf16x8_t xv[CH][RG];
         f32x4_t D[RG][4];
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int rg = 0; rg < RG; ++rg)
+            xv[c][rg] = *reinterpret_cast<const bf16x8_t *>(x_at(xs, n * CH + c, rg));
 #pragma unroll
         for (int rg = 0; rg < RG; ++rg) {
           f32x4_t X = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
             if (!WHOLE && n * CH + c >= nb) break;
-            X = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8_t, st.xa[n * CH + c][rg]), cst, X, 0, 0, 0);
+            X = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[c][rg], cst, X, 0, 0, 0);
           }
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -294,11 +333,10 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
           const uint32_t wd[4] = {st.v[u].x, st.v[u].y, st.v[u].z, st.v[u].w};
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const bf16x8_t bw = w4_bf16(wd[g]);
+            const bf16x8_t bw = w4_bf16(wd[g], consts);
 #pragma unroll
             for (int rg = 0; rg < RG; ++rg)
-              D[rg][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(bf16x8_t, st.xa[u][rg]), bw, D[rg][g], 0, 0, 0);
+              D[rg][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[c][rg], bw, D[rg][g], 0, 0, 0);
           }
         }
 #pragma unroll
@@ -310,37 +348,34 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
       }
     }
   };
-  auto step = [&](const Stage &st, int b) Q8_INLINE {
-    if (b + QB <= b_hi)
-      compute(std::true_type{}, st, QB);
-    else
-      compute(std::false_type{}, st, b_hi - b);
-  };
 
   {
+    // stages n of this wave, two in flight; only the last may be cut short
     Stage A, B;
     constexpr int stride = WK * QB;
     int b = b_lo + QB * wk;
-    if (b < b_hi) {
-      load(A, b);
-      while (true) {
-        if (b + stride >= b_hi) {
-          step(A, b);
-          break;
-        }
-        load(B, b + stride);
-        compute(std::true_type{}, A, QB);
-        b += stride;
-        if (b + stride >= b_hi) {
-          step(B, b);
-          break;
-        }
-        load(A, b + stride);
-        compute(std::true_type{}, B, QB);
-        b += stride;
-      }
+    int n = (b_hi - b + stride - 1) / stride;
+    if (n > 0) load(A, b, 0);
+    for (; n > 2; n -= 2, b += 2 * stride) {
+      load(B, b + stride, 1);
+      loads_left<kStageLoads>();
+      compute(std::true_type{}, A, 0, QB);
+      load(A, b + 2 * stride, 0);
+      loads_left<kStageLoads>();
+      compute(std::true_type{}, B, 1, QB);
+    }
+    if (n == 2) {
+      load(B, b + stride, 1);
+      loads_left<kStageLoads>();
+      compute(std::true_type{}, A, 0, QB);
+      loads_left<0>();
+      compute(std::false_type{}, B, 1, min(QB, b_hi - b - stride));
+    } else if (n == 1) {
+      loads_left<0>();
+      compute(std::false_type{}, A, 0, min(QB, b_hi - b));
     }
   }
+  __syncthreads();       // the stages' room is the carries' now
 
   // the waves' carries: halved until the rest fits, then side by side in LDS
   constexpr int WF = w4_final_waves(W, NW, MR);
@@ -395,10 +430,25 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
 
 template <int ACT, int W, int RG, int EL, int GB, bool ZEROS, bool PAIR>
 hipError_t launch_w4_k(const W4Args &a, hipStream_t stream) {
-  const unsigned chunks = (unsigned)((a.m + w4_rows(RG, EL) - 1) / w4_rows(RG, EL));
+  constexpr int MR = w4_rows(RG, EL), lds = w4_lds(ACT, W, RG, EL, PAIR ? 2 : 1);
+  const auto kern = w4_tile_kernel<ACT, W, RG, EL, GB, ZEROS, PAIR>;
+  if constexpr (lds > 64 * 1024) {
+    // once a device: dynamic LDS above the default 64 KiB
+    static std::atomic<uint64_t> granted{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev > 63 || !(granted.load(std::memory_order_relaxed) & bit)) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (e != hipSuccess) return e;
+      granted.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  const unsigned chunks = (unsigned)((a.m + MR - 1) / MR);
   (void)hipGetLastError();
-  w4_tile_kernel<ACT, W, RG, EL, GB, ZEROS, PAIR>
-      <<<dim3((unsigned)a.T, (unsigned)a.split_k, chunks), dim3(64 * W), 0, stream>>>(a);
+  kern<<<dim3((unsigned)a.T, (unsigned)a.split_k, chunks), dim3(64 * W), lds, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -427,8 +477,8 @@ hipError_t launch_w4_tile(int rows, bool pair, const W4Args &a, hipStream_t stre
                          : launch_w4_g<ACT, 8, 1, 4, false>(a, stream);
     case 32: return pair ? launch_w4_g<ACT, 8, 2, 4, true>(a, stream)
                          : launch_w4_g<ACT, 8, 2, 4, false>(a, stream);
-    case 64: return pair ? launch_w4_g<ACT, 4, 4, 4, true>(a, stream)
-                         : launch_w4_g<ACT, 4, 4, 4, false>(a, stream);
+    case 64: return pair ? launch_w4_g<ACT, 8, 4, 4, true>(a, stream)
+                         : launch_w4_g<ACT, 8, 4, 4, false>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }
