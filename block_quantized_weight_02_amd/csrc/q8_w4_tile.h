@@ -88,7 +88,7 @@ constexpr int w4_lds(int ACT, int W, int RG, int EL, int NW) {
 }
 
 template <int ACT, int W, int RG, int EL, int GB, bool ZEROS, bool PAIR>
-__global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
+__global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const W4Args a) {
   constexpr bool kQ8 = ACT == kActQ8;
   constexpr int MR = w4_rows(RG, EL);
   constexpr int NW = PAIR ? 2 : 1;
@@ -132,24 +132,34 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
   const unsigned mine_at = __builtin_amdgcn_readfirstlane(lds_offset(mine));
   const char *const xb = static_cast<const char *>(a.x) + (kQ8 ? a.act_view_off : 0u);
   const char *const db = static_cast<const char *>(a.x) + a.act_scale_off;
-  constexpr int kRowLoads = EL < 4 ? 1 : RG;
+  // A load takes two blocks (4 rows: the whole stage): of 8 rows of bf16, whole cache
+  // lines of 128 bytes (a load of 16 rows' 64 bytes reads every line twice: m = 32, N =
+  // 32001, loads alone 28 us), or of 16 rows of Q8_0 codes, which lie side by side.
+  constexpr int kRowLoads = EL < 4 ? 1 : kQ8 ? RG : 2 * RG;
   unsigned xoff[kRowLoads], doff[kQ8 ? RG : 1];
-  // the lane's block within a load (bf16: one block a load; 4 rows: the whole stage's)
-  const int xu = kQ8 ? (EL < 4 ? (lane >> 3) & 3 : lane >> 5) : (EL < 4 ? lane >> 4 : 0);
   const unsigned xstep = kQ8 ? (unsigned)a.m * 32u : 64u;
+  int xu;                // the lane's block within a load
+  if constexpr (kQ8) {
+    xu = EL < 4 ? (lane >> 3) & 3 : lane >> 5;
 #pragma unroll
-  for (int rg = 0; rg < kRowLoads; ++rg) {
-    if constexpr (kQ8) {
+    for (int k = 0; k < kRowLoads; ++k) {
       const int o = EL < 4 ? (lane >> 1) & 3 : (lane & 31) >> 1;
-      const int r = EL < 4 ? r0 + min(o, mz - 1) : row_of(rg, o);
-      xoff[rg] = (unsigned)r * 32u + (unsigned)(lane & 1) * 16u;
-    } else {
-      // 16-byte part p of a row's block is at place p ^ (row / 2 % 4), so that the
-      // operand reads spread over all LDS banks
-      const int o = EL < 4 ? (lane & 15) >> 2 : lane >> 2;
-      const int r = EL < 4 ? r0 + min(o, mz - 1) : row_of(rg, o);
-      xoff[rg] = (unsigned)(r - r0) * (unsigned)a.K * 2u + (unsigned)(((lane & 3) ^ ((o >> 1) & 3)) * 16);
+      const int r = EL < 4 ? r0 + min(o, mz - 1) : row_of(k, o);
+      xoff[k] = (unsigned)r * 32u + (unsigned)(lane & 1) * 16u;
     }
+  } else if constexpr (EL < 4) {
+    // [block][row][4 parts of 16 bytes], part p of row o at place p ^ (o / 2)
+    const int o = (lane & 15) >> 2;
+    xu = lane >> 4;
+    xoff[0] = (unsigned)min(o, mz - 1) * (unsigned)a.K * 2u + (unsigned)(((lane & 3) ^ (o >> 1)) * 16);
+  } else {
+    // [row][8 parts of two blocks], part p of row o at place p ^ (o / 2): the operand
+    // reads (16 rows' part p) spread over all LDS banks
+    const int part = (lane & 7) ^ (lane >> 4);       // (rows 8 .. 15: ^ 4 more, below)
+    xu = part >> 2;
+#pragma unroll
+    for (int k = 0; k < kRowLoads; ++k)
+      xoff[k] = (unsigned)(row_of(k >> 1, 8 * (k & 1) + (lane >> 3)) - r0) * (unsigned)a.K * 2u + (unsigned)(part & 3) * 16u;
   }
   if constexpr (kQ8) {
 #pragma unroll
@@ -170,10 +180,13 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
       }
     } else {
 #pragma unroll
-      for (int u = 0; u < QB; ++u) {
-        const char *base = xrow + (size_t)min(b + u, last) * 64;
+      for (int j = 0; j < QB / 2; ++j) {
+        // rows 8 .. 15 have the two blocks' places the other way round
+        const unsigned bo[2] = {(unsigned)min(b + 2 * j + xu, last) * 64u,
+                                (unsigned)min(b + 2 * j + (xu ^ 1), last) * 64u};
 #pragma unroll
-        for (int rg = 0; rg < RG; ++rg) load_to_lds16(base, xoff[rg], at + (u * RG + rg) * 1024);
+        for (int k = 0; k < kRowLoads; ++k)
+          load_to_lds16(xrow, bo[k & 1] + xoff[k], at + (j * kRowLoads + k) * 1024);
       }
     }
     if constexpr (kQ8) {
@@ -220,20 +233,22 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
     }
   };
 
-  f32x4_t acc[RG][4];
+  float acc[RG][4][EL];
 #pragma unroll
   for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) acc[rg][g] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int e = 0; e < EL; ++e) acc[rg][g][e] = 0.0f;
 
   const Bf16Consts consts;
   // the lane's operand bytes of block u, row group rg of a stage
   const int xlane = kQ8 ? (EL < 4 ? (i >> 2) * 32 + q * 8 : i * 32 + q * 8)
-                        : (EL < 4 ? (i >> 2) * 64 + ((q ^ ((i >> 3) & 3)) * 16) : i * 64 + ((q ^ ((i >> 1) & 3)) * 16));
+                        : (EL < 4 ? (i >> 2) * 64 + ((q ^ (i >> 3)) * 16) : i * 128 + ((q ^ (i >> 1)) * 16));
   const auto x_at = [&](const char *slot, int u, int rg) Q8_INLINE {
     if constexpr (EL < 4) return slot + u * (kQ8 ? 128 : 256) + xlane;
     else if constexpr (kQ8) return slot + ((u >> 1) * RG + rg) * 1024 + (u & 1) * 512 + xlane;
-    else return slot + (u * RG + rg) * 1024 + xlane;
+    else return slot + ((u >> 1) * RG + rg) * 2048 + (xlane ^ (u & 1) * 64);
   };
   // WHOLE: all of the stage's blocks are the range's (else the first nb)
   auto compute = [&](auto whole, const Stage &st, int slot, int nb) Q8_INLINE {
@@ -346,6 +361,15 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
 #pragma unroll
             for (int e = 0; e < EL; ++e) acc[rg][g][e] = fmaf(sc[g], D[rg][g][e], acc[rg][g][e]);
       }
+      // (the sums are taken here: left to the loop's end, a stage's products fill the
+      // registers)
+#pragma unroll
+      for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) asm volatile("" : "+v"(acc[rg][g][e]));
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -379,7 +403,6 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
 
   // the waves' carries: halved until the rest fits, then side by side in LDS
   constexpr int WF = w4_final_waves(W, NW, MR);
-  static_assert(EL == 4 || WF == WK, "halving moves all four of a lane's results");
 #pragma unroll
   for (int half = WK / 2; half >= WF; half /= 2) {
     if (wk >= half && wk < 2 * half) {
@@ -388,7 +411,8 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
       for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<f32x4_t *>(rw + (rg * 4 + g) * 256 + lane * 4) = acc[rg][g];
+#pragma unroll
+          for (int e = 0; e < EL; ++e) rw[((rg * 4 + g) * EL + e) * 64 + lane] = acc[rg][g][e];
     }
     __syncthreads();
     if (wk < half) {
@@ -397,7 +421,8 @@ __global__ void __launch_bounds__(64 * W) w4_tile_kernel(const W4Args a) {
       for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          acc[rg][g] += *reinterpret_cast<const f32x4_t *>(rw + (rg * 4 + g) * 256 + lane * 4);
+#pragma unroll
+          for (int e = 0; e < EL; ++e) acc[rg][g][e] += rw[((rg * 4 + g) * EL + e) * 64 + lane];
     }
     __syncthreads();
   }
