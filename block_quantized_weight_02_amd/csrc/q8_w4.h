@@ -71,9 +71,13 @@ hipError_t launch_w4_unpack(const char *values, const char *scales, const char *
                             int64_t N, int group, uint8_t *u, uint16_t *s, uint8_t *z,
                             hipStream_t stream);
 
-// The tile kernel: rows 4, 16, 32 or 64 a workgroup, more rows in chunks.
-hipError_t launch_w4_tile_bf16(int rows, bool pair, const W4Args &a, hipStream_t stream);
-hipError_t launch_w4_tile_q8(int rows, bool pair, const W4Args &a, hipStream_t stream);
+// The tile kernel: rows 4, 16, 32 or 64 a workgroup (more rows in chunks), its waves (8
+// or 16) splitting K, each over `tiles` column tiles (the pair: both weights' tile).
+struct W4Plan {
+  int rows, waves, tiles;
+};
+hipError_t launch_w4_tile_bf16(const W4Plan &p, bool pair, const W4Args &a, hipStream_t stream);
+hipError_t launch_w4_tile_q8(const W4Plan &p, bool pair, const W4Args &a, hipStream_t stream);
 
 // The GEMM: blocks of 128 rows.
 hipError_t launch_w4_gemm(int act, bool pair, const W4Args &a, hipStream_t stream);

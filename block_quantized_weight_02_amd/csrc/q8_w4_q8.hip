@@ -3,8 +3,8 @@
 
 namespace q8 {
 
-hipError_t launch_w4_tile_q8(int rows, bool pair, const W4Args &a, hipStream_t stream) {
-  return launch_w4_tile<kActQ8>(rows, pair, a, stream);
+hipError_t launch_w4_tile_q8(const W4Plan &p, bool pair, const W4Args &a, hipStream_t stream) {
+  return launch_w4_tile<kActQ8>(p, pair, a, stream);
 }
 
 }  // namespace q8

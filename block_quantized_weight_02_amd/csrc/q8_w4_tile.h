@@ -62,49 +62,55 @@ __device__ __forceinline__ long w4_i8(uint32_t w) {
 
 // Rows of carries that a wave keeps.
 constexpr int w4_rows(int RG, int EL) { return RG == 1 ? 4 * EL : 16 * RG; }
-// Waves a weight whose carries still stand apart when the tile is finished: its
-// W/NW waves, halved until all of them fit 32 KiB.
-constexpr int w4_final_waves(int W, int NW, int rows) {
-  int n = W / NW;
-  while (n > 1 && n * NW * rows * 256 > 32 * 1024) n /= 2;
+// Waves whose carries still stand apart when the NT tiles are finished: W, halved until
+// all of them fit 32 KiB; and the LDS that they (and the halves before) take.
+constexpr int w4_final_waves(int W, int NT, int rows) {
+  int n = W;
+  while (n > 1 && n * NT * rows * 256 > 32 * 1024) n /= 2;
   return n;
 }
-constexpr int w4_lds_bytes(int W, int NW, int rows) {
-  const int n = w4_final_waves(W, NW, rows), first = W / NW / 2;
-  return (n < W / NW && first > n ? first : n) * NW * rows * 256;
+constexpr int w4_carry_bytes(int W, int NT, int rows) {
+  const int n = w4_final_waves(W, NT, rows);
+  return (n < W ? W / 2 : W) * NT * rows * 256;
 }
 
 // Blocks a stage, and the bytes of LDS that a stage's activation takes.
-constexpr int w4_stage_blocks(int RG) { return RG == 4 ? 2 : 4; }
-constexpr int w4_slot_x(int ACT, int RG, int EL) {
-  return EL < 4 ? 1024 : RG * w4_stage_blocks(RG) * (ACT == kActQ8 ? 512 : 1024);
+constexpr int w4_stage_blocks(int RG, int NT) { return RG * NT > 1 ? 2 : 4; }
+constexpr int w4_slot_x(int ACT, int RG, int EL, int NT) {
+  return EL < 4 ? 1024 : RG * w4_stage_blocks(RG, NT) * (ACT == kActQ8 ? 512 : 1024);
 }
-constexpr int w4_slot(int ACT, int RG, int EL) {
-  return w4_slot_x(ACT, RG, EL) + (ACT == kActQ8 ? RG * 256 : 0);
+constexpr int w4_slot(int ACT, int RG, int EL, int NT) {
+  return w4_slot_x(ACT, RG, EL, NT) + (ACT == kActQ8 ? RG * 256 : 0);
 }
-constexpr int w4_lds(int ACT, int W, int RG, int EL, int NW) {
-  const int stages = 2 * W * w4_slot(ACT, RG, EL), carries = w4_lds_bytes(W, NW, w4_rows(RG, EL));
+constexpr int w4_lds(int ACT, int W, int RG, int EL, int NT) {
+  const int stages = 2 * W * w4_slot(ACT, RG, EL, NT), carries = w4_carry_bytes(W, NT, w4_rows(RG, EL));
   return stages > carries ? stages : carries;
 }
 
-template <int ACT, int W, int RG, int EL, int GB, bool ZEROS, bool PAIR>
-__global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const W4Args a) {
+// Waves a SIMD that the registers are kept to: four (128 registers) where the carries and
+// stages fit, else two.
+constexpr int w4_waves_per_simd(int ACT, int RG, int EL, int NT, int GB) {
+  return EL < 4 || (RG * NT == 1 && !(ACT == kActQ8 && GB == 4)) ? 4 : 2;
+}
+
+// NT: column tiles a wave covers, sharing its activation stage: the pair's two weights'
+// (PAIR), or two of one weight side by side.
+template <int ACT, int W, int RG, int EL, int NT, int GB, bool ZEROS, bool PAIR>
+__global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)) w4_tile_kernel(const W4Args a) {
   constexpr bool kQ8 = ACT == kActQ8;
   constexpr int MR = w4_rows(RG, EL);
-  constexpr int NW = PAIR ? 2 : 1;
-  constexpr int WK = W / NW;                 // waves that split a weight's K range
-  constexpr int QB = w4_stage_blocks(RG);
+  static_assert(!PAIR || NT == 2, "the pair's tiles of both weights");
+  constexpr int QB = w4_stage_blocks(RG, NT);
   constexpr int CH = GB < QB ? GB : QB;      // of them, blocks that share a scale
   constexpr int NS = QB / CH;                // scales a stage and column
-  constexpr int kSlotX = w4_slot_x(ACT, RG, EL), kSlot = w4_slot(ACT, RG, EL);
+  constexpr int kSlotX = w4_slot_x(ACT, RG, EL, NT), kSlot = w4_slot(ACT, RG, EL, NT);
   extern __shared__ __attribute__((aligned(16))) char lds[];
   float *const red = reinterpret_cast<float *>(lds);
 
   const int lane = threadIdx.x & 63;
   const int q = lane >> 4, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int sel = PAIR ? wave / WK : 0, wk = PAIR ? wave % WK : wave;
-  const int t = blockIdx.x, s = blockIdx.y;
+  const int s = blockIdx.y;
   const int r0 = blockIdx.z * MR;
   const int mz = min(a.m - r0, MR);
   // a split is whole quads of blocks
@@ -116,13 +122,20 @@ __global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const 
     b_hi = min(b_hi * 4, a.NB);
   }
 
-  const W4 w = PAIR && sel ? a.w_u : a.w;
-  constexpr int kGroupRows = GB * 32;
-  const unsigned groups = (unsigned)w4_groups((int64_t)a.NB * 32, kGroupRows);
-  const buf_t wr = make_buf(w.values + (size_t)t * a.NB * kW4Chunk, (unsigned)a.NB * kW4Chunk);
-  const buf_t sr = make_buf(w.scales + (size_t)t * groups * 128, groups * 128u);
-  const buf_t zr = ZEROS ? make_buf(w.zeros + (size_t)t * groups * 64, groups * 64u) : wr;
+  // the wave's tiles (past the weight's last: that one again, not stored)
+  const unsigned groups = (unsigned)w4_groups((int64_t)a.NB * 32, GB * 32);
   const unsigned lw = (unsigned)lane * 16u;
+  buf_t wr[NT], sr[NT], zr[NT];
+  int tile[NT];
+#pragma unroll
+  for (int k = 0; k < NT; ++k) {
+    const W4 &w = PAIR && k ? a.w_u : a.w;
+    tile[k] = PAIR ? (int)blockIdx.x : NT * (int)blockIdx.x + k;
+    const size_t t = (size_t)min(tile[k], a.T - 1);
+    wr[k] = make_buf(w.values + t * a.NB * kW4Chunk, (unsigned)a.NB * kW4Chunk);
+    sr[k] = make_buf(w.scales + t * groups * 128, groups * 128u);
+    zr[k] = ZEROS ? make_buf(w.zeros + t * groups * 64, groups * 64u) : wr[k];
+  }
 
   // ---- the activation's stages.  Operand row o of a row group holds the activation's
   // row 4 (o % 4) + o / 4 (with 4 rows in all, LDS holds just these); rows past the chunk
@@ -197,49 +210,58 @@ __global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const 
   };
   // loads that a stage surely issues: what may be left when the one before is computed
   constexpr int kFetch = (EL < 4 ? 1 : kQ8 ? RG * QB / 2 : RG * QB) + (kQ8 ? RG : 0);
-  constexpr int kStageLoads = kFetch + QB;
+  constexpr int kStageLoads = kFetch + NT * QB;
 
-  struct Stage {
+  struct Weight {
     uint4 v[QB];
     uint2 sc[NS];
     uint32_t z[NS];
+  };
+  struct Stage {
+    Weight w[NT];
   };
   auto load = [&](Stage &st, int bv, int slot) Q8_INLINE {
     const int b = __builtin_amdgcn_readfirstlane(bv);
     __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the slot's last reads have returned
     fetch(b, slot);
 #pragma unroll
-    for (int u = 0; u < QB; ++u) st.v[u] = buf_ld16(wr, lw, (unsigned)(b + u) * kW4Chunk);
-    if constexpr (NS >= 2) {           // two groups a load
+    for (int k = 0; k < NT; ++k) {
+      Weight &w = st.w[k];
 #pragma unroll
-      for (int p = 0; p < NS / 2; ++p) {
-        const unsigned pair = (unsigned)(b / GB / 2 + p);
-        const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(sr, (unsigned)i * 16u, pair * 256u, 0);
-        st.sc[2 * p] = make_uint2(v.x, v.y);
-        st.sc[2 * p + 1] = make_uint2(v.z, v.w);
-        if constexpr (ZEROS) {
-          const u32x2_t zz = __builtin_amdgcn_raw_buffer_load_b64(zr, (unsigned)i * 8u, pair * 128u, 0);
-          st.z[2 * p] = zz.x;
-          st.z[2 * p + 1] = zz.y;
+      for (int u = 0; u < QB; ++u) w.v[u] = buf_ld16(wr[k], lw, (unsigned)(b + u) * kW4Chunk);
+      if constexpr (NS >= 2) {           // two groups a load
+#pragma unroll
+        for (int p = 0; p < NS / 2; ++p) {
+          const unsigned pair = (unsigned)(b / GB / 2 + p);
+          const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(sr[k], (unsigned)i * 16u, pair * 256u, 0);
+          w.sc[2 * p] = make_uint2(v.x, v.y);
+          w.sc[2 * p + 1] = make_uint2(v.z, v.w);
+          if constexpr (ZEROS) {
+            const u32x2_t zz = __builtin_amdgcn_raw_buffer_load_b64(zr[k], (unsigned)i * 8u, pair * 128u, 0);
+            w.z[2 * p] = zz.x;
+            w.z[2 * p + 1] = zz.y;
+          }
         }
+      } else {
+        const unsigned j = (unsigned)(b / GB);
+        const unsigned at = GB == 4 ? j * 128u : (j >> 1) * 256u + (j & 1u) * 8u;
+        const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(sr[k], (unsigned)i * (GB == 4 ? 8u : 16u), at, 0);
+        w.sc[0] = make_uint2(v.x, v.y);
+        if constexpr (ZEROS)
+          w.z[0] = __builtin_amdgcn_raw_buffer_load_b32(zr[k], (unsigned)i * (GB == 4 ? 4u : 8u), at / 2u, 0);
       }
-    } else {
-      const unsigned j = (unsigned)(b / GB);
-      const unsigned at = GB == 4 ? j * 128u : (j >> 1) * 256u + (j & 1u) * 8u;
-      const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(sr, (unsigned)i * (GB == 4 ? 8u : 16u), at, 0);
-      st.sc[0] = make_uint2(v.x, v.y);
-      if constexpr (ZEROS)
-        st.z[0] = __builtin_amdgcn_raw_buffer_load_b32(zr, (unsigned)i * (GB == 4 ? 4u : 8u), at / 2u, 0);
     }
   };
 
-  float acc[RG][4][EL];
+  float acc[NT][RG][4][EL];
 #pragma unroll
-  for (int rg = 0; rg < RG; ++rg)
+  for (int k = 0; k < NT; ++k)
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-      for (int e = 0; e < EL; ++e) acc[rg][g][e] = 0.0f;
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < EL; ++e) acc[k][rg][g][e] = 0.0f;
 
   const Bf16Consts consts;
   // the lane's operand bytes of block u, row group rg of a stage
@@ -257,15 +279,15 @@ __global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const 
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       if (!WHOLE && n * CH >= nb) break;
-      float sc[4];
-      w4_scales4(st.sc[n], a.scale_bf16 ? ~0u : 0u, sc);
+      float sc[NT][4];
+#pragma unroll
+      for (int k = 0; k < NT; ++k) w4_scales4(st.w[k].sc[n], a.scale_bf16 ? ~0u : 0u, sc[k]);
       if constexpr (kQ8) {
-        float tt[RG][4][EL];
+        float tt[NT][RG][4][EL];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           const int u = n * CH + c;
           if (!WHOLE && u >= nb) break;
-          const uint32_t wd[4] = {st.v[u].x, st.v[u].y, st.v[u].z, st.v[u].w};
 #pragma unroll
           for (int rg = 0; rg < RG; ++rg) {
             const uint2 xw = *reinterpret_cast<const uint2 *>(x_at(xs, u, rg));
@@ -282,42 +304,51 @@ __global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const 
 #pragma unroll
               for (int e = 0; e < EL; ++e) dx[e] = dp[e];
             }
-            const long cst = ZEROS ? 0x0101010101010101l : (long)0xf8f8f8f8f8f8f8f8ul;
+            // -8 sum x, or -sum x where zero points multiply it
+            const long cst = ZEROS ? -1l : (long)0xf8f8f8f8f8f8f8f8ul;
             const i32x4_t X = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, cst, i32x4_t{0, 0, 0, 0}, 0, 0, 0);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              i32x4_t C = X;
-              if constexpr (ZEROS) {
-                const int z = -(int)((st.z[n] >> (8 * g)) & 0xffu);
+            for (int k = 0; k < NT; ++k) {
+              const uint4 v = st.w[k].v[u];
+              const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < EL; ++e) C[e] = __mul24(X[e], z);
-              }
-              const i32x4_t D = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, w4_i8(wd[g]), C, 0, 0, 0);
+              for (int g = 0; g < 4; ++g) {
+                i32x4_t C = X;
+                if constexpr (ZEROS) {
+                  const int z = (int)((st.w[k].z[n] >> (8 * g)) & 0xffu);
 #pragma unroll
-              for (int e = 0; e < EL; ++e) {
-                const float d = (float)D[e];
-                if constexpr (CH == 1)
-                  acc[rg][g][e] = fmaf(dx[e] * sc[g], d, acc[rg][g][e]);
-                else
-                  tt[rg][g][e] = c == 0 ? dx[e] * d : fmaf(dx[e], d, tt[rg][g][e]);
+                  for (int e = 0; e < EL; ++e) C[e] = __mul24(X[e], z);
+                }
+                const i32x4_t D = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, w4_i8(wd[g]), C, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < EL; ++e) {
+                  const float d = (float)D[e];
+                  if constexpr (CH == 1)
+                    acc[k][rg][g][e] = fmaf(dx[e] * sc[k][g], d, acc[k][rg][g][e]);
+                  else
+                    tt[k][rg][g][e] = c == 0 ? dx[e] * d : fmaf(dx[e], d, tt[k][rg][g][e]);
+                }
               }
             }
           }
         }
         if constexpr (CH > 1) {
 #pragma unroll
-          for (int rg = 0; rg < RG; ++rg)
+          for (int k = 0; k < NT; ++k)
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
+            for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-              for (int e = 0; e < EL; ++e) acc[rg][g][e] = fmaf(sc[g], tt[rg][g][e], acc[rg][g][e]);
+              for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int e = 0; e < EL; ++e)
+                  acc[k][rg][g][e] = fmaf(sc[k][g], tt[k][rg][g][e], acc[k][rg][g][e]);
         }
       } else {
         // -24 (16 + the 8 that u stands above), or 1 where zero points are given
         const uint32_t cw = ZEROS ? 0x3f803f80u : 0xc1c0c1c0u;
         const bf16x8_t cst = __builtin_bit_cast(bf16x8_t, make_uint4(cw, cw, cw, cw));
         bf16x8_t xv[CH][RG];
-        f32x4_t D[RG][4];
+        f32x4_t X[RG];
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -325,50 +356,60 @@ __global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const 
             xv[c][rg] = *reinterpret_cast<const bf16x8_t *>(x_at(xs, n * CH + c, rg));
 #pragma unroll
         for (int rg = 0; rg < RG; ++rg) {
-          f32x4_t X = {0.0f, 0.0f, 0.0f, 0.0f};
+          X[rg] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
             if (!WHOLE && n * CH + c >= nb) break;
-            X = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[c][rg], cst, X, 0, 0, 0);
+            X[rg] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[c][rg], cst, X[rg], 0, 0, 0);
           }
+        }
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            D[rg][g] = X;
-            if constexpr (ZEROS) {
-              const float z = -16.0f - (float)((st.z[n] >> (8 * g)) & 0xffu);
+        for (int k = 0; k < NT; ++k) {
+          f32x4_t D[RG][4];
 #pragma unroll
-              for (int e = 0; e < EL; ++e) D[rg][g][e] = z * X[e];
+          for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              D[rg][g] = X[rg];
+              if constexpr (ZEROS) {
+                const float z = -16.0f - (float)((st.w[k].z[n] >> (8 * g)) & 0xffu);
+#pragma unroll
+                for (int e = 0; e < EL; ++e) D[rg][g][e] = z * X[rg][e];
+              }
+            }
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            const int u = n * CH + c;
+            if (!WHOLE && u >= nb) break;
+            const uint4 v = st.w[k].v[u];
+            const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const bf16x8_t bw = w4_bf16(wd[g], consts);
+#pragma unroll
+              for (int rg = 0; rg < RG; ++rg)
+                D[rg][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[c][rg], bw, D[rg][g], 0, 0, 0);
             }
           }
+#pragma unroll
+          for (int rg = 0; rg < RG; ++rg)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int e = 0; e < EL; ++e)
+                acc[k][rg][g][e] = fmaf(sc[k][g], D[rg][g][e], acc[k][rg][g][e]);
         }
+      }
+      // (the sums are taken here: left to the loop's end, a stage's products fill the
+      // registers)
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int u = n * CH + c;
-          if (!WHOLE && u >= nb) break;
-          const uint32_t wd[4] = {st.v[u].x, st.v[u].y, st.v[u].z, st.v[u].w};
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const bf16x8_t bw = w4_bf16(wd[g], consts);
-#pragma unroll
-            for (int rg = 0; rg < RG; ++rg)
-              D[rg][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[c][rg], bw, D[rg][g], 0, 0, 0);
-          }
-        }
+      for (int k = 0; k < NT; ++k)
 #pragma unroll
         for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int e = 0; e < EL; ++e) acc[rg][g][e] = fmaf(sc[g], D[rg][g][e], acc[rg][g][e]);
-      }
-      // (the sums are taken here: left to the loop's end, a stage's products fill the
-      // registers)
-#pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int e = 0; e < EL; ++e) asm volatile("" : "+v"(acc[rg][g][e]));
+            for (int e = 0; e < EL; ++e) asm volatile("" : "+v"(acc[k][rg][g][e]));
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -376,8 +417,8 @@ __global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const 
   {
     // stages n of this wave, two in flight; only the last may be cut short
     Stage A, B;
-    constexpr int stride = WK * QB;
-    int b = b_lo + QB * wk;
+    constexpr int stride = W * QB;
+    int b = b_lo + QB * wave;
     int n = (b_hi - b + stride - 1) / stride;
     if (n > 0) load(A, b, 0);
     for (; n > 2; n -= 2, b += 2 * stride) {
@@ -402,38 +443,46 @@ __global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const 
   __syncthreads();       // the stages' room is the carries' now
 
   // the waves' carries: halved until the rest fits, then side by side in LDS
-  constexpr int WF = w4_final_waves(W, NW, MR);
+  constexpr int WF = w4_final_waves(W, NT, MR);
 #pragma unroll
-  for (int half = WK / 2; half >= WF; half /= 2) {
-    if (wk >= half && wk < 2 * half) {
-      float *rw = red + (size_t)(sel * half + wk - half) * MR * 64;
+  for (int half = W / 2; half >= WF; half /= 2) {
+    float *rw = red + (size_t)(wave & (half - 1)) * NT * MR * 64;
+    if (wave >= half && wave < 2 * half) {
 #pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
+      for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-          for (int e = 0; e < EL; ++e) rw[((rg * 4 + g) * EL + e) * 64 + lane] = acc[rg][g][e];
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < EL; ++e)
+              rw[(((k * RG + rg) * 4 + g) * EL + e) * 64 + lane] = acc[k][rg][g][e];
     }
     __syncthreads();
-    if (wk < half) {
-      const float *rw = red + (size_t)(sel * half + wk) * MR * 64;
+    if (wave < half) {
 #pragma unroll
-      for (int rg = 0; rg < RG; ++rg)
+      for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-          for (int e = 0; e < EL; ++e) acc[rg][g][e] += rw[((rg * 4 + g) * EL + e) * 64 + lane];
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < EL; ++e)
+              acc[k][rg][g][e] += rw[(((k * RG + rg) * 4 + g) * EL + e) * 64 + lane];
     }
     __syncthreads();
   }
-  if (wk < WF) {
-    float *rw = red + (size_t)(sel * WF + wk) * MR * 64;
+  if (wave < WF) {
 #pragma unroll
-    for (int rg = 0; rg < RG; ++rg)
+    for (int k = 0; k < NT; ++k) {
+      float *rw = red + (size_t)(k * WF + wave) * MR * 64;
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+      for (int rg = 0; rg < RG; ++rg)
 #pragma unroll
-        for (int e = 0; e < EL; ++e) rw[(16 * rg + 4 * e + q) * 64 + 16 * g + i] = acc[rg][g][e];
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) rw[(16 * rg + 4 * e + q) * 64 + 16 * g + i] = acc[k][rg][g][e];
+    }
   }
   __syncthreads();
   // the chunk's rows of the outputs (a launch of several chunks has one split and
@@ -445,18 +494,24 @@ __global__ void __launch_bounds__(64 * W, RG == 1 ? 4 : 2) w4_tile_kernel(const 
     ep.yq_view += (size_t)r0 * 32;
     ep.view_rows = a.m;
   }
-  const TileOut out{a.y + (size_t)r0 * a.Npad, a.Npad, (size_t)t * kTile, (size_t)t * kTile, a.Npad,
-                    (unsigned)t};
-  if constexpr (PAIR)
-    finish_pair_tile<MR, 2 * WF, 64 * W>(red, out, a.partial, a.counters, mz, s, a.split_k, ep);
-  else
-    finish_tile<MR, WF, false, 64 * W>(red, out, a.partial, a.counters, mz, s, a.split_k, 0, ep);
+  const auto out = [&](int t) {
+    return TileOut{a.y + (size_t)r0 * a.Npad, a.Npad, (size_t)t * kTile, (size_t)t * kTile, a.Npad, (unsigned)t};
+  };
+  if constexpr (PAIR) {
+    finish_pair_tile<MR, 2 * WF, 64 * W>(red, out(tile[0]), a.partial, a.counters, mz, s, a.split_k, ep);
+  } else {
+    finish_tile<MR, WF, false, 64 * W>(red, out(tile[0]), a.partial, a.counters, mz, s, a.split_k, 0, ep);
+    if constexpr (NT == 2)               // (two tiles a wave are not split: finish_tile does not return early)
+      if (tile[1] < a.T)
+        finish_tile<MR, WF, false, 64 * W>(red + WF * MR * 64, out(tile[1]), a.partial, a.counters, mz, s,
+                                           a.split_k, 0, ep);
+  }
 }
 
-template <int ACT, int W, int RG, int EL, int GB, bool ZEROS, bool PAIR>
+template <int ACT, int W, int RG, int EL, int NT, int GB, bool ZEROS, bool PAIR>
 hipError_t launch_w4_k(const W4Args &a, hipStream_t stream) {
-  constexpr int MR = w4_rows(RG, EL), lds = w4_lds(ACT, W, RG, EL, PAIR ? 2 : 1);
-  const auto kern = w4_tile_kernel<ACT, W, RG, EL, GB, ZEROS, PAIR>;
+  constexpr int MR = w4_rows(RG, EL), lds = w4_lds(ACT, W, RG, EL, NT);
+  const auto kern = w4_tile_kernel<ACT, W, RG, EL, NT, GB, ZEROS, PAIR>;
   if constexpr (lds > 64 * 1024) {
     // once a device: dynamic LDS above the default 64 KiB
     static std::atomic<uint64_t> granted{0};
@@ -473,37 +528,46 @@ hipError_t launch_w4_k(const W4Args &a, hipStream_t stream) {
   }
   const unsigned chunks = (unsigned)((a.m + MR - 1) / MR);
   (void)hipGetLastError();
-  kern<<<dim3((unsigned)a.T, (unsigned)a.split_k, chunks), dim3(64 * W), lds, stream>>>(a);
+  const unsigned units = PAIR ? (unsigned)a.T : (unsigned)((a.T + NT - 1) / NT);
+  kern<<<dim3(units, (unsigned)a.split_k, chunks), dim3(64 * W), lds, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int ACT, int W, int RG, int EL, bool PAIR>
+template <int ACT, int W, int RG, int EL, int NT, bool PAIR>
 hipError_t launch_w4_g(const W4Args &a, hipStream_t stream) {
   const bool z = a.w.zeros != nullptr;
   switch (a.group) {
-    case 32: return z ? launch_w4_k<ACT, W, RG, EL, 1, true, PAIR>(a, stream)
-                      : launch_w4_k<ACT, W, RG, EL, 1, false, PAIR>(a, stream);
-    case 64: return z ? launch_w4_k<ACT, W, RG, EL, 2, true, PAIR>(a, stream)
-                      : launch_w4_k<ACT, W, RG, EL, 2, false, PAIR>(a, stream);
-    case 128: return z ? launch_w4_k<ACT, W, RG, EL, 4, true, PAIR>(a, stream)
-                       : launch_w4_k<ACT, W, RG, EL, 4, false, PAIR>(a, stream);
+    case 32: return z ? launch_w4_k<ACT, W, RG, EL, NT, 1, true, PAIR>(a, stream)
+                      : launch_w4_k<ACT, W, RG, EL, NT, 1, false, PAIR>(a, stream);
+    case 64: return z ? launch_w4_k<ACT, W, RG, EL, NT, 2, true, PAIR>(a, stream)
+                      : launch_w4_k<ACT, W, RG, EL, NT, 2, false, PAIR>(a, stream);
+    case 128: return z ? launch_w4_k<ACT, W, RG, EL, NT, 4, true, PAIR>(a, stream)
+                       : launch_w4_k<ACT, W, RG, EL, NT, 4, false, PAIR>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }
 
 template <int ACT>
-hipError_t launch_w4_tile(int rows, bool pair, const W4Args &a, hipStream_t stream) {
-  // more rows than a workgroup covers: chunks, without splits or a residual
-  if (a.m > rows && (a.split_k != 1 || a.ep.residual)) return hipErrorInvalidValue;
-  switch (rows) {
-    case 4: return pair ? launch_w4_g<ACT, 8, 1, 1, true>(a, stream)
-                        : launch_w4_g<ACT, 8, 1, 1, false>(a, stream);
-    case 16: return pair ? launch_w4_g<ACT, 8, 1, 4, true>(a, stream)
-                         : launch_w4_g<ACT, 8, 1, 4, false>(a, stream);
-    case 32: return pair ? launch_w4_g<ACT, 8, 2, 4, true>(a, stream)
-                         : launch_w4_g<ACT, 8, 2, 4, false>(a, stream);
-    case 64: return pair ? launch_w4_g<ACT, 8, 4, 4, true>(a, stream)
-                         : launch_w4_g<ACT, 8, 4, 4, false>(a, stream);
+hipError_t launch_w4_tile(const W4Plan &p, bool pair, const W4Args &a, hipStream_t stream) {
+  // more rows than a workgroup covers: chunks, without splits or a residual; two tiles
+  // of one weight: without splits
+  if (a.m > p.rows && (a.split_k != 1 || a.ep.residual)) return hipErrorInvalidValue;
+  if (!pair && p.tiles == 2 && a.split_k != 1) return hipErrorInvalidValue;
+  const int key = p.rows * 1000 + p.waves * 10 + p.tiles;
+  if (pair) switch (key) {
+    case 4162: return launch_w4_g<ACT, 16, 1, 1, 2, true>(a, stream);
+    case 16082: return launch_w4_g<ACT, 8, 1, 4, 2, true>(a, stream);
+    case 32082: return launch_w4_g<ACT, 8, 2, 4, 2, true>(a, stream);
+    default: return hipErrorInvalidValue;
+  }
+  switch (key) {
+    case 4081: return launch_w4_g<ACT, 8, 1, 1, 1, false>(a, stream);
+    case 4161: return launch_w4_g<ACT, 16, 1, 1, 1, false>(a, stream);
+    case 16081: return launch_w4_g<ACT, 8, 1, 4, 1, false>(a, stream);
+    case 16082: return launch_w4_g<ACT, 8, 1, 4, 2, false>(a, stream);
+    case 32081: return launch_w4_g<ACT, 8, 2, 4, 1, false>(a, stream);
+    case 32082: return launch_w4_g<ACT, 8, 2, 4, 2, false>(a, stream);
+    case 64081: return launch_w4_g<ACT, 8, 4, 4, 1, false>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }
