@@ -33,6 +33,31 @@ struct LogitRulesArgs {
 };
 hipError_t launch_logit_rules(const LogitRulesArgs &a, hipStream_t stream);
 
+// What the draw's launches hand on through the workspace.
+struct SliceStat {                            // of a slice of a row
+  float top;                                  // its largest logit
+  int at;                                     // the lowest index of that
+  float exp_sum;                              // of exp(l - top)
+  float sum;                                  // of the logits that can weigh anything
+  unsigned n;                                 // how many those are
+};
+struct RowCut {                               // where a row's order is cut
+  int bin;                                    // the step of M - l; kSampleBins: nowhere
+  unsigned bin_n;                             // tokens in it
+  unsigned long long before_n, before_w;      // tokens and weight before it
+  unsigned long long total_w;
+  unsigned n_cand;
+};
+struct Candidate {
+  float l;
+  int i;
+};
+
+constexpr int kSampleTile = 1024;             // tokens a wave takes at a time
+constexpr int kSampleSlice = 4096;            // tokens of a slice of the statistics
+constexpr int kSampleBins = 2048, kSampleCand = 1024;
+constexpr int kMaxVocab = 1 << 20;
+
 struct SampleArgs {
   const float *logits;
   int64_t ld;
@@ -42,9 +67,15 @@ struct SampleArgs {
   const double *u;                            // m
   int32_t *token;
   float *logprob;                             // m, or null
+  // the workspace
+  int slices, parts, row_tiles;               // of a row: statistics, workgroups a pass, tiles
+  SliceStat *stats;                           // m x slices
+  RowCut *cuts;                               // m
+  unsigned long long *tiles;                  // m x row_tiles: kept weight
+  uint32_t *counts;                           // m x parts x kSampleBins
+  unsigned long long *masses;                 // m x parts x kSampleBins
+  Candidate *cands;                           // m x kSampleCand
 };
-constexpr int kSampleTile = 1024;             // tokens a wave takes at a time
-constexpr int kMaxVocab = 1 << 20;
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream);
 
 }  // namespace q8

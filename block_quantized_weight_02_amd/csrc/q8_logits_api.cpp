@@ -2,6 +2,8 @@
 // argument validation before any launch.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "../../include/q8gemv.h"
 #include "q8_checks.h"
 #include "q8_logits.h"
@@ -20,6 +22,31 @@ int check_rows(const float *logits, int64_t ld, int64_t m, int64_t V, const char
     return report_error(Q8_ERR_SHAPE, "%s = %lld: need a multiple of 4, at least %lld", ld_name,
                         (long long)ld, (long long)V);
   return Q8_OK;
+}
+
+// The draw's workspace: its bytes, and with `ws` the places in it.  The products' and
+// attention's counters at its start are left alone, so that one workspace serves all.
+size_t sample_layout(SampleArgs &a, char *ws) {
+  const int64_t tiles = (a.V + kSampleTile - 1) / kSampleTile;
+  a.slices = (a.V + kSampleSlice - 1) / kSampleSlice;
+  a.row_tiles = (int)tiles;
+  // workgroups of a row and pass: about 1024 in all, at least 4096 tokens each, and not
+  // too many for one workgroup to sum their histograms
+  a.parts = (int)std::min<int64_t>(std::min(a.slices, 64), std::max<int64_t>(1, 1024 / a.m));
+  size_t at = kCounterBytes;
+  const auto take = [&](size_t bytes) {
+    char *p = ws + at;
+    at += (size_t)round_up((int64_t)bytes, 256);
+    return ws ? p : nullptr;
+  };
+  const size_t m = (size_t)a.m;
+  a.stats = reinterpret_cast<SliceStat *>(take(m * a.slices * sizeof(SliceStat)));
+  a.cuts = reinterpret_cast<RowCut *>(take(m * sizeof(RowCut)));
+  a.tiles = reinterpret_cast<unsigned long long *>(take(m * tiles * 8));
+  a.counts = reinterpret_cast<uint32_t *>(take(m * a.parts * kSampleBins * 4));
+  a.masses = reinterpret_cast<unsigned long long *>(take(m * a.parts * kSampleBins * 8));
+  a.cands = reinterpret_cast<Candidate *>(take(m * kSampleCand * sizeof(Candidate)));
+  return at;
 }
 
 }  // namespace
@@ -88,18 +115,20 @@ int q8_logits_rules(const float *logits, int64_t ld, int64_t m, int64_t V,
 }
 
 size_t q8_sample_workspace_bytes(int64_t m, int64_t V) {
-  (void)check_rows(nullptr, (V + 3) / 4 * 4, m, V, "ld");
-  return 0;
+  if (check_rows(nullptr, (V + 3) / 4 * 4, m, V, "ld")) return 0;
+  SampleArgs a{};
+  a.m = (int)m;
+  a.V = (int)V;
+  return sample_layout(a, nullptr);
 }
 
 int q8_sample(const float *logits, int64_t ld, int64_t m, int64_t V, const q8_sampling *sampling,
               int32_t *token, float *logprob, hipStream_t stream, void *workspace, size_t ws_bytes) {
   int st;
-  (void)ws_bytes;
   if ((st = check_rows(logits, ld, m, V, "ld"))) return st;
   if (!sampling) return report_error(Q8_ERR_NULL, "sampling is NULL");
   if ((st = check_ptr(logits, "logits")) || (st = check_ptr(token, "token")) ||
-      (st = check_opt(logprob, "logprob")) || (st = check_opt(workspace, "workspace")) ||
+      (st = check_opt(logprob, "logprob")) ||
       (st = check_ptr(sampling->u, "u")) ||
       (st = check_opt(sampling->temperature, "temperature")) ||
       (st = check_opt(sampling->top_k, "top_k")) || (st = check_opt(sampling->top_p, "top_p")) ||
@@ -117,6 +146,8 @@ int q8_sample(const float *logits, int64_t ld, int64_t m, int64_t V, const q8_sa
   a.u = sampling->u;
   a.token = token;
   a.logprob = logprob;
+  if ((st = check_workspace(workspace, ws_bytes, sample_layout(a, nullptr)))) return st;
+  sample_layout(a, static_cast<char *>(workspace));
   return done(launch_sample(a, stream), "sample launch");
 }
 

@@ -1,5 +1,4 @@
-// q8_sample.hip -- a token a row from its logits, in one launch: one workgroup of
-// 16 waves a row.
+// q8_sample.hip -- a token a row from its logits.
 //
 // With l the row's logits, M the largest, T the temperature, a token's weight is
 // w = exp((l - M) / T), and the tokens stand in the order of falling l, lower index
@@ -14,22 +13,28 @@
 // of 2^(j/64) and four terms of the series: relative error below 1e-13), about twenty
 // instructions; it is taken only where a sum needs it.
 //
-// Passes over the row (from memory once, then from the caches):
-//   1. the largest logit with its lowest index, and the mean of the finite ones;
-//   2. sum of exp(l - M) for the log-probability; with a limit on the order, counts
-//      (and for top_p weights) of 2047 even steps of M - l from 0 to 3/4 of M - mean,
-//      which few tokens reach, so that the histogram's LDS additions are few: the
-//      rest is one last bin, kept in registers.  Without such a limit, the weights'
-//      sum of each tile of 1024 tokens;
-//   3. the tokens of the limit's bin become candidates, and the tiles sum what
-//      stands before that bin.  Too many candidates: the bin's range of logits (as
-//      ordered integers) is divided again, at most three times, down to equal logits,
-//      which are counted by index.
-// The candidates are ordered by comparing each with all; then the tile that holds
-// the drawn weight is walked by one wave.
+// Five launches, the rows' vocabularies in slices so that one row too is worked on by
+// many CUs (one workgroup a row took 18 us for one row of 32000 tokens, 94 for 40 of
+// 50001 and, its slowest kind of row deciding, 268 for 256 of 131072):
+//   stats    of a slice: its largest logit with the lowest index, sum of exp(l - that),
+//            and the mean of what can weigh anything;
+//   weights  rows with a limit on the order: counts (for top_p weights too) of 2047 even
+//            steps of M - l, in LDS, a slice's histogram written out whole; rows without
+//            one: the weights' sum of each tile of 1024 tokens;
+//   cut      (a workgroup a row) the slices' histograms summed, and the step in which the
+//            order is cut;
+//   collect  the tokens of that step as candidates, and the tiles' sums of what stands
+//            before it;
+//   draw     (a workgroup a row) the candidates ordered by comparing each with all, and
+//            the tile that holds the drawn weight walked by one wave.  Where more than
+//            1024 tokens fall into one step, the step's range of logits (as ordered
+//            integers) is divided again here, down to equal logits, which are counted
+//            by index.
+// The steps reach from M to 3/4 of the way to the mean where only top_k cuts (the cut is
+// near the top, and few tokens then add to LDS), and as far below the mean as M stands
+// above it where top_p does; what lies beyond is one last step, summed in registers.
 //
-// Bound by the row's first pass at many rows; one row is bound by one CU's issue
-// (about 4 us for each 32000 tokens that need weights) and the steps between barriers.
+// The first pass is bound by the rows' bytes, the second by fp64 and by additions in LDS.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -38,11 +43,12 @@
 namespace q8 {
 namespace {
 
-constexpr int kThreads = 1024, kWaves = 16;
-constexpr int kBins = 2048;
-constexpr int kCand = 1024;
+constexpr int kThreads = 1024, kWaves = 16;   // of a workgroup a row
+constexpr int kBins = kSampleBins;
+constexpr int kCand = kSampleCand;
 constexpr int kMaxTiles = kMaxVocab / kSampleTile;
 constexpr int kVals = 16;                  // tokens of a tile a lane holds
+constexpr int kStatTiles = kSampleSlice / kSampleTile;   // one a wave
 
 typedef unsigned long long u64;
 
@@ -119,6 +125,119 @@ __device__ __forceinline__ u64 wave_scan(u64 v, int lane) {    // inclusive
   return v;
 }
 
+// What the launches hand on about a row.
+struct Params {                            // the row's limits
+  float T;
+  int k;
+  float p;
+  double min_p;
+  bool greedy, by_k, by_p;
+};
+__device__ __forceinline__ Params params_of(const SampleArgs &a, int row) {
+  Params r;
+  r.T = a.temperature ? a.temperature[row] : 1.0f;
+  r.greedy = !(r.T > 0.0f);
+  r.k = a.top_k ? a.top_k[row] : 0;
+  r.p = a.top_p ? a.top_p[row] : 1.0f;
+  const float mp = a.min_p ? a.min_p[row] : 0.0f;
+  r.min_p = mp > 0.0f ? fmin((double)mp, 1.0) : 0.0;
+  r.by_k = !r.greedy && r.k > 0 && r.k < a.V;
+  r.by_p = !r.greedy && r.p < 1.0f;
+  return r;
+}
+
+constexpr float kFar = 60.0f;              // in units of T, below the largest: no weight
+struct Total {                             // the slices' statistics together
+  float M;
+  int at;
+  float mean;
+  double exp_sum;                          // of exp(l - M)
+};
+// By each wave for itself, from the row's slices.
+__device__ __forceinline__ Total total_of(const SampleArgs &a, const Params &r, int row, int lane) {
+  const SliceStat *st = a.stats + (size_t)row * a.slices;
+  float top = -INFINITY;
+  int at = 0x7fffffff;
+  double sum = 0.0;
+  unsigned n = 0;
+  for (int i = lane; i < a.slices; i += 64) {
+    const SliceStat v = st[i];
+    if (v.top > top || (v.top == top && v.at < at)) {
+      top = v.top;
+      at = v.at;
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float t2 = __shfl_xor(top, o);
+    const int a2 = __shfl_xor(at, o);
+    if (t2 > top || (t2 == top && a2 < at)) {
+      top = t2;
+      at = a2;
+    }
+  }
+  double e = 0.0;
+  for (int i = lane; i < a.slices; i += 64) {
+    const SliceStat v = st[i];
+    // (slices of masks of the type's lowest value are no part of the mean)
+    if (v.top >= top - kFar * (r.greedy ? 1.0f : r.T)) {
+      sum += v.sum;
+      n += v.n;
+    }
+    if (v.top > -INFINITY) e += v.top == top ? (double)v.exp_sum : (double)v.exp_sum * exp((double)v.top - (double)top);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    e += __shfl_xor(e, o);
+    sum += __shfl_xor(sum, o);
+    n += __shfl_xor(n, o);
+  }
+  Total t;
+  t.M = top;
+  t.at = at;
+  t.mean = n ? (float)(sum / (double)n) : 0.0f;
+  t.exp_sum = e;
+  return t;
+}
+
+__device__ __forceinline__ Weigher weigher_of(const SampleArgs &a, const Params &r, float M, const double *pow) {
+  Weigher w;
+  w.c64 = 92.332482616893656878 / (double)(r.greedy ? 1.0f : r.T);   // 64 log2(e)
+  w.M = M;
+  w.Mf = M;
+  w.sh = min(51, 62 - (32 - __clz(a.V)));
+  w.pow = pow;
+  return w;
+}
+// A token's weight where min_p keeps it, else 0.
+struct Keep {
+  Weigher w;
+  float min_l;                             // below it: out without computing the weight
+  double min_w;
+  __device__ __forceinline__ Keep(const Weigher &wg, const Params &r) : w(wg) {
+    min_w = r.min_p * (double)(1ull << w.sh);
+    // (a margin over the roundings of the bound itself)
+    min_l = r.min_p > 0.0 ? (float)(w.M + (double)r.T * (log(r.min_p) - 1e-3) - 1e-6 * fabs(w.M)) : -INFINITY;
+  }
+  __device__ __forceinline__ u64 operator()(float l) const {
+    if (l < min_l) return 0;
+    const double d = weight_of(w, l);
+    return d < min_w ? 0 : whole(d);
+  }
+};
+// Even steps of M - l: falling l, rising step; the last takes all the rest.
+struct Steps {
+  float M, per;
+  __device__ __forceinline__ Steps(const Total &t, bool by_p) {
+    M = t.M;
+    per = (float)(kBins - 1) / ((by_p ? 2.0f : 0.75f) * (M - t.mean));
+    if (!(per > 0.0f) || !(per < INFINITY) || !(M < INFINITY)) per = 1.0f;
+  }
+  __device__ __forceinline__ int operator()(float l) const {
+    return l == M ? 0 : (int)fminf((M - l) * per, (float)(kBins - 1));
+  }
+};
+
 struct Lds {
   double pow[64];
   u64 mass[kBins];
@@ -127,10 +246,6 @@ struct Lds {
   float cand_l[kCand];
   int cand_i[kCand];
   u64 cand_w[kCand];
-  // reductions
-  float wmax[kWaves];
-  int wi[kWaves];
-  double wsum[kWaves];
   uint32_t wn[kWaves];
   u64 wmass[kWaves];
   // the state of the search
@@ -141,7 +256,6 @@ struct Lds {
   uint32_t kmin, kmax;
   uint32_t cut_key;
   int cut_index;
-  int token;
   int pick_tile;
   u64 pick_rest;
 };
@@ -150,7 +264,8 @@ struct Lds {
 // running count reaches `want_n` or running weight reaches `want_w` (in doubles:
 // compared as p * W is).  before_n, before_w: what stands before the histogram's
 // range, and on return before the bin.  Leaves s.bin = kBins where none does.
-__device__ void find_bin(Lds &s, u64 want_n, double want_w) {
+template <typename S>
+__device__ void find_bin(S &s, u64 want_n, double want_w) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // two bins a thread
   const u64 n0 = s.count[2 * tid], n1 = s.count[2 * tid + 1];
@@ -197,34 +312,25 @@ __device__ void clear_bins(Lds &s) {
   }
 }
 
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
-  __shared__ Lds s;
-  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+// ---- stats ------------------------------------------------------------------------
+__global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const SampleArgs a) {
+  __shared__ float wtop[kStatTiles], wexp[kStatTiles];
+  __shared__ int wat[kStatTiles];
+  __shared__ double wsum[kStatTiles];
+  __shared__ unsigned wn[kStatTiles];
+  const int row = blockIdx.y, slice = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float *__restrict__ x = a.logits + (size_t)row * a.ld;
-  const int V = a.V, tiles = (V + kSampleTile - 1) / kSampleTile;
-
-  // ---- pass 1
+  const int t = slice * kStatTiles + wave;
+  float v[kVals];
+  load_tile(x, a.V, t, lane, v);
   float top = -INFINITY;
   int at = 0x7fffffff;
-  float sum = 0.0f;
-  uint32_t finite = 0;
-  for (int t = wave; t < tiles; t += kWaves) {
-    float v[kVals];
-    load_tile(x, V, t, lane, v);
 #pragma unroll
-    for (int j = 0; j < kVals; ++j) {
-      if (v[j] > top) {
-        top = v[j];
-        at = index_of(t, lane, j);
-      }
-      if (fabsf(v[j]) < INFINITY) {
-        sum += v[j];
-        ++finite;
-      }
+  for (int j = 0; j < kVals; ++j)
+    if (v[j] > top) {
+      top = v[j];
+      at = index_of(t, lane, j);
     }
-  }
-  double dsum = sum;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     const float t2 = __shfl_xor(top, o);
@@ -233,30 +339,242 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
       top = t2;
       at = a2;
     }
-    dsum += __shfl_xor(dsum, o);
-    finite += __shfl_xor(finite, o);
   }
   if (lane == 0) {
-    s.wmax[wave] = top;
-    s.wi[wave] = at;
-    s.wsum[wave] = dsum;
-    s.wn[wave] = finite;
+    wtop[wave] = top;
+    wat[wave] = at;
   }
-  if (tid < 64) s.pow[tid] = exp2((double)tid / 64.0);
   __syncthreads();
-  dsum = 0.0;
-  finite = 0;
-  top = -INFINITY;
-  at = 0x7fffffff;
-  for (int i = 0; i < kWaves; ++i) {
-    if (s.wmax[i] > top || (s.wmax[i] == top && s.wi[i] < at)) {
-      top = s.wmax[i];
-      at = s.wi[i];
+  for (int i = 0; i < kStatTiles; ++i)
+    if (wtop[i] > top || (wtop[i] == top && wat[i] < at)) {
+      top = wtop[i];
+      at = wat[i];
     }
-    dsum += s.wsum[i];
-    finite += s.wn[i];
+  // the mean of what can weigh anything
+  const float T = a.temperature ? a.temperature[row] : 1.0f;
+  const float floor_l = T > 0.0f ? top - kFar * T : -INFINITY;
+  float sum = 0.0f, e = 0.0f;
+  unsigned n = 0;
+#pragma unroll
+  for (int j = 0; j < kVals; ++j) {
+    if (v[j] >= floor_l && fabsf(v[j]) < INFINITY) {
+      sum += v[j];
+      ++n;
+    }
+    e += v[j] == top ? (top > -INFINITY ? 1.0f : 0.0f)
+                     : __builtin_amdgcn_exp2f((v[j] - top) * 1.44269504088896f);
   }
-  const float M = top;
+  double ds = sum;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    ds += __shfl_xor(ds, o);
+    e += __shfl_xor(e, o);
+    n += __shfl_xor(n, o);
+  }
+  if (lane == 0) {
+    wsum[wave] = ds;
+    wexp[wave] = e;
+    wn[wave] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    SliceStat r{top, at, 0.0f, 0.0f, 0u};
+    double d = 0.0;
+    for (int i = 0; i < kStatTiles; ++i) {
+      d += wsum[i];
+      r.exp_sum += wexp[i];
+      r.n += wn[i];
+    }
+    r.sum = (float)d;
+    a.stats[(size_t)row * a.slices + slice] = r;
+  }
+}
+
+// ---- weights ------------------------------------------------------------------------
+constexpr int kPassThreads = 512, kPassWaves = kPassThreads / 64;
+
+// The tiles of a workgroup's part of the row.
+__device__ __forceinline__ void part_of_row(const SampleArgs &a, int part, int &lo, int &hi) {
+  const int tiles = (a.V + kSampleTile - 1) / kSampleTile;
+  const int each = (tiles + a.parts - 1) / a.parts;
+  lo = min(part * each, tiles);
+  hi = min(lo + each, tiles);
+}
+
+__global__ void __launch_bounds__(kPassThreads) sample_weights_kernel(const SampleArgs a) {
+  __shared__ double pow[64];
+  __shared__ u64 mass[kBins];
+  __shared__ uint32_t count[kBins];
+  const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Params r = params_of(a, row);
+  if (r.greedy) return;
+  const float *__restrict__ x = a.logits + (size_t)row * a.ld;
+  const Total tot = total_of(a, r, row, lane);
+  if (tot.M == -INFINITY) return;
+  if (tid < 64) pow[tid] = exp2((double)tid / 64.0);
+  const bool cut = r.by_k || r.by_p;
+  if (cut)
+    for (int i = tid; i < kBins; i += kPassThreads) {
+      mass[i] = 0;
+      count[i] = 0;
+    }
+  __syncthreads();
+  const Keep keep(weigher_of(a, r, tot.M, pow), r);
+  int lo, hi;
+  part_of_row(a, blockIdx.x, lo, hi);
+  if (!cut) {
+    for (int t = lo + wave; t < hi; t += kPassWaves) {
+      float v[kVals];
+      load_tile(x, a.V, t, lane, v);
+      u64 wt = 0;
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) wt += keep(v[j]);
+      wt = wave_sum(wt);
+      if (lane == 0) a.tiles[(size_t)row * a.row_tiles + t] = wt;
+    }
+    return;
+  }
+  const Steps step(tot, r.by_p);
+  u64 rest_w = 0;
+  uint32_t rest_n = 0;
+  for (int t = lo + wave; t < hi; t += kPassWaves) {
+    float v[kVals];
+    load_tile(x, a.V, t, lane, v);
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) {
+      const u64 wt = r.by_p ? whole(weight_of(keep.w, v[j])) : 0;
+      if (v[j] == -INFINITY) continue;
+      const int b = step(v[j]);
+      if (b == kBins - 1) {
+        rest_w += wt;
+        ++rest_n;
+      } else {
+        atomicAdd(&count[b], 1u);
+        if (r.by_p) atomicAdd(&mass[b], wt);
+      }
+    }
+  }
+  rest_w = wave_sum(rest_w);
+  rest_n = (uint32_t)wave_sum(rest_n);
+  if (lane == 0 && rest_n) {
+    atomicAdd(&count[kBins - 1], rest_n);
+    atomicAdd(&mass[kBins - 1], rest_w);
+  }
+  __syncthreads();
+  const size_t at = ((size_t)row * a.parts + blockIdx.x) * kBins;
+  for (int i = tid; i < kBins; i += kPassThreads) {
+    a.counts[at + i] = count[i];
+    if (r.by_p) a.masses[at + i] = mass[i];
+  }
+}
+
+// ---- cut ------------------------------------------------------------------------------
+__global__ void __launch_bounds__(kThreads) sample_cut_kernel(const SampleArgs a) {
+  __shared__ struct {
+    u64 mass[kBins];
+    uint32_t count[kBins];
+    uint32_t wn[kWaves];
+    u64 wmass[kWaves];
+    int bin;
+    u64 before_n, before_w;
+    uint32_t bin_n;
+  } s;
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Params r = params_of(a, row);
+  if (!(r.by_k || r.by_p)) return;
+  const Total tot = total_of(a, r, row, lane);
+  if (tot.M == -INFINITY) return;
+  u64 w0 = 0, w1 = 0;
+  uint32_t n0 = 0, n1 = 0;
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p) {
+    const size_t at = ((size_t)row * a.parts + p) * kBins + 2 * tid;
+    const uint2 n = *reinterpret_cast<const uint2 *>(a.counts + at);
+    n0 += n.x;
+    n1 += n.y;
+    if (r.by_p) {
+      const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(a.masses + at);
+      w0 += m.x;
+      w1 += m.y;
+    }
+  }
+  s.mass[2 * tid] = w0;
+  s.mass[2 * tid + 1] = w1;
+  s.count[2 * tid] = n0;
+  s.count[2 * tid + 1] = n1;
+  const u64 part = wave_sum(w0 + w1);
+  if (lane == 0) s.wmass[wave] = part;
+  if (tid == 0) {
+    s.before_n = 0;
+    s.before_w = 0;
+  }
+  __syncthreads();
+  u64 W = 0;
+  for (int i = 0; i < kWaves; ++i) W += s.wmass[i];
+  __syncthreads();
+  find_bin(s, r.by_k ? (u64)r.k : ~0ull, r.by_p ? (double)r.p * (double)W : INFINITY);
+  if (tid == 0) {
+    RowCut c;
+    c.bin = s.bin;
+    c.bin_n = s.bin < kBins ? s.bin_n : 0;
+    c.before_n = s.before_n;
+    c.before_w = s.before_w;
+    c.total_w = W;
+    c.n_cand = 0;
+    a.cuts[row] = c;
+  }
+}
+
+// ---- collect ----------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPassThreads) sample_collect_kernel(const SampleArgs a) {
+  __shared__ double pow[64];
+  const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Params r = params_of(a, row);
+  if (!(r.by_k || r.by_p)) return;
+  const float *__restrict__ x = a.logits + (size_t)row * a.ld;
+  const Total tot = total_of(a, r, row, lane);
+  if (tot.M == -INFINITY) return;
+  const int bin = a.cuts[row].bin;
+  if (a.cuts[row].bin_n > kCand) return;   // divided again by the draw
+  if (tid < 64) pow[tid] = exp2((double)tid / 64.0);
+  __syncthreads();
+  const Keep keep(weigher_of(a, r, tot.M, pow), r);
+  const Steps step(tot, r.by_p);
+  int lo, hi;
+  part_of_row(a, blockIdx.x, lo, hi);
+  for (int t = lo + wave; t < hi; t += kPassWaves) {
+    float v[kVals];
+    load_tile(x, a.V, t, lane, v);
+    u64 wt = 0;
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) {
+      if (v[j] == -INFINITY) continue;
+      const int b = step(v[j]);
+      if (b < bin) {
+        wt += keep(v[j]);
+      } else if (b == bin) {
+        const unsigned c = atomicAdd(&a.cuts[row].n_cand, 1u);
+        if (c < kCand) {
+          Candidate d{v[j], index_of(t, lane, j)};
+          a.cands[(size_t)row * kCand + c] = d;
+        }
+      }
+    }
+    wt = wave_sum(wt);
+    if (lane == 0) a.tiles[(size_t)row * a.row_tiles + t] = wt;
+  }
+}
+
+// ---- draw -------------------------------------------------------------------------------
+__global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs a) {
+  __shared__ Lds s;
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const float *__restrict__ x = a.logits + (size_t)row * a.ld;
+  const int V = a.V, tiles = (V + kSampleTile - 1) / kSampleTile;
+  const Params r = params_of(a, row);
+  const Total tot = total_of(a, r, row, lane);
+  const float M = tot.M;
   if (M == -INFINITY) {                    // nothing may follow
     if (tid == 0) {
       a.token[row] = -1;
@@ -264,119 +582,52 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
     return;
   }
-
-  // ---- the row's limits
-  const float T = a.temperature ? a.temperature[row] : 1.0f;
-  const bool greedy = !(T > 0.0f);
-  const int k_in = a.top_k ? a.top_k[row] : 0;
-  const float p_in = a.top_p ? a.top_p[row] : 1.0f;
-  const float mp_in = a.min_p ? a.min_p[row] : 0.0f;
-  const bool by_k = !greedy && k_in > 0 && k_in < V;
-  const bool by_p = !greedy && p_in < 1.0f;
-  const double min_p = mp_in > 0.0f ? fmin((double)mp_in, 1.0) : 0.0;
-  Weigher w;
-  w.c64 = 92.332482616893656878 / (double)(greedy ? 1.0f : T);   // 64 log2(e)
-  w.M = M;
-  w.Mf = M;
-  w.sh = min(51, 62 - (32 - __clz(V)));
-  w.pow = s.pow;
-  const double min_w = min_p * (double)(1ull << w.sh);
-  // below this a token weighs less than min_p without computing it (a margin over
-  // the roundings of the bound itself)
-  const float min_l = min_p > 0.0 ? (float)((double)M + (double)T * (log(min_p) - 1e-3) -
-                                            1e-6 * fabs((double)M)) : -INFINITY;
-  const auto kept_weight = [&](float l) -> u64 {     // 0 where min_p leaves the token out
-    if (l < min_l) return 0;
-    const double d = weight_of(w, l);
-    return d < min_w ? 0 : whole(d);
-  };
-  // 2047 steps over 3/4 of what the largest logit stands above the mean
-  const float mean = finite ? (float)(dsum / (double)finite) : 0.0f;
-  float step = 2047.0f / (0.75f * (M - mean));
-  if (!(step > 0.0f) || !(step < INFINITY) || !(M < INFINITY)) step = 1.0f;
-  const auto bin_of = [&](float l) -> int {
-    return l == M ? 0 : (int)fminf((M - l) * step, 2047.0f);   // falling l, rising bin
-  };
-
-  // ---- pass 2
-  const bool cut = by_k || by_p;
-  if (cut) clear_bins(s);
+  if (r.greedy) {
+    if (tid == 0) {
+      a.token[row] = tot.at;
+      if (a.logprob) a.logprob[row] = (float)-log(tot.exp_sum);
+    }
+    return;
+  }
+  if (tid < 64) s.pow[tid] = exp2((double)tid / 64.0);
+  const Weigher w = weigher_of(a, r, M, s.pow);
+  const Keep kept_weight(w, r);
+  const Steps bin_of(tot, r.by_p);
+  const bool cut = r.by_k || r.by_p;
+  const bool by_k = r.by_k, by_p = r.by_p;
+  RowCut rc{};
+  if (cut) rc = a.cuts[row];
+  const bool again = cut && rc.bin_n > kCand;
   if (tid == 0) {
     s.n_cand = 0;
-    s.before_n = 0;
-    s.before_w = 0;
+    s.before_n = rc.before_n;
+    s.before_w = rc.before_w;
+    s.bin_n = rc.bin_n;
     s.cut_key = 0;                         // everything
     s.cut_index = 0x7fffffff;
-    s.token = -1;
   }
+  if (!again)
+    for (int t = tid; t < tiles; t += kThreads) s.tile[t] = a.tiles[(size_t)row * a.row_tiles + t];
   __syncthreads();
-  float lse = 0.0f;
-  u64 rest_w = 0;
-  uint32_t rest_n = 0;
-  if (a.logprob || !greedy) {
-    for (int t = wave; t < tiles; t += kWaves) {
-      float v[kVals];
-      load_tile(x, V, t, lane, v);
-      if (a.logprob) {
-#pragma unroll
-        for (int j = 0; j < kVals; ++j) lse += v[j] == M ? 1.0f : expf(v[j] - M);
-      }
-      if (cut) {
-        for (int j = 0; j < kVals; ++j) {
-          if (v[j] == -INFINITY) continue;
-          const u64 wt = by_p ? whole(weight_of(w, v[j])) : 0;
-          const int b = bin_of(v[j]);
-          if (b == kBins - 1) {
-            rest_w += wt;
-            ++rest_n;
-          } else {
-            atomicAdd(&s.count[b], 1u);
-            if (by_p) atomicAdd(&s.mass[b], wt);
-          }
-        }
-      } else if (!greedy) {
-        u64 wt = 0;
-        for (int j = 0; j < kVals; ++j) wt += kept_weight(v[j]);
-        wt = wave_sum(wt);
-        if (lane == 0) s.tile[t] = wt;
-      }
-    }
-  }
-  double dl = lse;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) dl += __shfl_xor(dl, o);
-  __syncthreads();                         // (wsum's readers are done)
-  if (lane == 0) s.wsum[wave] = dl;
-  if (cut) {
-    rest_w = wave_sum(rest_w);
-    rest_n = (uint32_t)wave_sum(rest_n);
-    if (lane == 0 && rest_n) {
-      atomicAdd(&s.count[kBins - 1], rest_n);
-      atomicAdd(&s.mass[kBins - 1], rest_w);
-    }
-  }
-  __syncthreads();
-  dl = 0.0;
-  for (int i = 0; i < kWaves; ++i) dl += s.wsum[i];
 
-  if (!greedy && cut) {
-    // ---- where the order is cut
-    u64 W = 0;
-    if (by_p) {
-      u64 part = s.mass[2 * tid] + s.mass[2 * tid + 1];
-      part = wave_sum(part);
-      if (lane == 0) s.wmass[wave] = part;
-      __syncthreads();
-      for (int i = 0; i < kWaves; ++i) W += s.wmass[i];
+  if (cut) {
+    const u64 want_n = by_k ? (u64)r.k : ~0ull;
+    const double want_w = by_p ? (double)r.p * (double)rc.total_w : INFINITY;
+    int bin = rc.bin;
+    bool keyed = false, equal = false;
+    uint32_t klo = 0, khi = 0;
+    if (!again) {
+      const int n = min((int)rc.n_cand, kCand);
+      for (int c = tid; c < n; c += kThreads) {
+        const Candidate d = a.cands[(size_t)row * kCand + c];
+        s.cand_l[c] = d.l;
+        s.cand_i[c] = d.i;
+        s.cand_w[c] = whole(weight_of(w, d.l));
+      }
+      if (tid == 0) s.n_cand = n;
       __syncthreads();
     }
-    const u64 want_n = by_k ? (u64)k_in : ~0ull;
-    const double want_w = by_p ? (double)p_in * (double)W : INFINITY;
-    find_bin(s, want_n, want_w);
-    int bin = s.bin;
-    // the range of the cut: the tokens of a bin, later of an interval of keys
-    uint32_t klo = 0, khi = 0;
-    bool keyed = false, equal = false;
+    // more than kCand tokens in the step: an interval of keys, divided again
     while (bin < kBins && s.bin_n > kCand) {
       if (!keyed) {
         // the bin's smallest and largest key
@@ -389,6 +640,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         for (int t = wave; t < tiles; t += kWaves) {
           float v[kVals];
           load_tile(x, V, t, lane, v);
+#pragma unroll
           for (int j = 0; j < kVals; ++j)
             if (v[j] != -INFINITY && bin_of(v[j]) == bin) {
               const uint32_t k = key_of(v[j]);
@@ -421,6 +673,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
       for (int t = wave; t < tiles; t += kWaves) {
         float v[kVals];
         load_tile(x, V, t, lane, v);
+#pragma unroll
         for (int j = 0; j < kVals; ++j) {
           const uint32_t k = key_of(v[j]);
           if (k < klo || k > khi || v[j] == -INFINITY) continue;
@@ -439,29 +692,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
     const bool cuts = bin < kBins;
 
-    // ---- pass 3: what stands before the range, by tile; its tokens, or how many
+    // what stands before the interval, by tile; its tokens, or how many
     const uint32_t kequal = khi;
     __syncthreads();
-    for (int t = wave; t < tiles; t += kWaves) {
+    for (int t = wave; again && t < tiles; t += kWaves) {
       float v[kVals];
       load_tile(x, V, t, lane, v);
       u64 wt = 0;
       uint32_t same = 0;
+#pragma unroll
       for (int j = 0; j < kVals; ++j) {
         if (v[j] == -INFINITY) continue;
         bool first, in;
-        if (!cuts) {
-          first = true;
-          in = false;
-        } else if (keyed) {
-          const uint32_t k = key_of(v[j]);
-          first = k > khi;
-          in = k <= khi && k >= klo;
-        } else {
-          const int b = bin_of(v[j]);
-          first = b < bin;
-          in = b == bin;
-        }
+        const uint32_t k = key_of(v[j]);
+        first = k > khi;
+        in = k <= khi && k >= klo;
         if (first) wt += kept_weight(v[j]);
         if (in) {
           if (equal) {
@@ -558,6 +803,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         float v[kVals];
         load_tile(x, V, edge, lane, v);
         u64 seen = 0;
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
           u64 mine = 0;
           for (int c = 0; c < 4; ++c) mine += v[4 * j + c] != -INFINITY && key_of(v[4 * j + c]) == kequal;
@@ -572,72 +818,65 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     __syncthreads();
   }
 
-  // ---- the draw
-  if (!greedy) {
-    if (wave == 0) {
-      u64 total = 0;
-      for (int t = lane; t < tiles; t += 64) total += s.tile[t];
-      total = wave_sum(total);
-      const double u = a.u[row];
-      const double f = floor((u > 0.0 ? u : 0.0) * (double)total);
-      u64 target = f < (double)total ? (u64)f : total;
-      if (target >= total) target = total - 1;
-      // the first tile whose running sum exceeds it
-      u64 run = 0;
-      int pick = -1;
-      for (int t0 = 0; t0 < tiles && pick < 0; t0 += 64) {
-        const u64 mine = t0 + lane < tiles ? s.tile[t0 + lane] : 0;
-        const u64 upto = wave_scan(mine, lane) + run;
-        const u64 over = __ballot(upto > target);
-        if (over) {
-          const int f0 = __ffsll(over) - 1;
-          pick = t0 + f0;
-          run = __shfl(upto - mine, f0);
-        } else {
-          run = __shfl(upto, 63);
-        }
-      }
-      if (pick >= 0) {
-        float v[kVals];
-        load_tile(x, V, pick, lane, v);
-        const uint32_t ck = s.cut_key;
-        const int ci = s.cut_index;
-        int token = -1;
-        for (int j = 0; j < 4 && token < 0; ++j) {
-          u64 wt[4], mine = 0;
-          for (int c = 0; c < 4; ++c) {
-            const float l = v[4 * j + c];
-            const uint32_t k = key_of(l);
-            const bool in = l != -INFINITY && (k > ck || (k == ck && index_of(pick, lane, 4 * j + c) <= ci));
-            wt[c] = in ? kept_weight(l) : 0;
-            mine += wt[c];
-          }
-          const u64 upto = wave_scan(mine, lane) + run;
-          const u64 over = __ballot(upto > target);
-          if (over) {
-            const int f0 = __ffsll(over) - 1;
-            u64 r = upto - mine;
-            int mine_at = -1;
-            for (int c = 0; c < 4 && mine_at < 0; ++c) {
-              r += wt[c];
-              if (r > target) mine_at = index_of(pick, lane, 4 * j + c);
-            }
-            token = __shfl(mine_at, f0);
-          } else {
-            run = __shfl(upto, 63);
-          }
-        }
-        if (lane == 0) s.token = token;
-      }
-    }
-    __syncthreads();
+  // ---- the token
+  if (wave != 0) return;
+  u64 total = 0;
+  for (int t = lane; t < tiles; t += 64) total += s.tile[t];
+  total = wave_sum(total);
+  const double u = a.u[row];
+  const double f = floor((u > 0.0 ? u : 0.0) * (double)total);
+  u64 target = f < (double)total ? (u64)f : total;
+  if (target >= total) target = total - 1;
+  // the first tile whose running sum exceeds it
+  u64 run = 0;
+  int pick = -1;
+  for (int t0 = 0; t0 < tiles && pick < 0; t0 += 64) {
+    const u64 mine = t0 + lane < tiles ? s.tile[t0 + lane] : 0;
+    const u64 upto = wave_scan(mine, lane) + run;
+    const u64 over = __ballot(upto > target);
+    const int f0 = over ? __ffsll(over) - 1 : 63;
+    if (over) pick = t0 + f0;
+    run = __shfl(over ? upto - mine : upto, f0);
   }
-  if (tid == 0) {
-    const int token = greedy ? at : s.token;
+  // and in it the token
+  int token = -1;
+  if (pick >= 0) {
+    float v[kVals];
+    load_tile(x, V, pick, lane, v);
+    const uint32_t ck = s.cut_key;
+    const int ci = s.cut_index;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (token >= 0) break;
+      u64 wt[4], mine = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float l = v[4 * j + c];
+        const uint32_t k = key_of(l);
+        const bool in = l != -INFINITY && (k > ck || (k == ck && index_of(pick, lane, 4 * j + c) <= ci));
+        wt[c] = in ? kept_weight(l) : 0;
+        mine += wt[c];
+      }
+      const u64 upto = wave_scan(mine, lane) + run;
+      const u64 over = __ballot(upto > target);
+      u64 at = upto - mine;
+      int first = -1;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        at += wt[c];
+        if (first < 0 && at > target) first = index_of(pick, lane, 4 * j + c);
+      }
+      if (over)
+        token = __shfl(first, __ffsll(over) - 1);
+      else
+        run = __shfl(upto, 63);
+    }
+  }
+  if (lane == 0) {
     a.token[row] = token;
     if (a.logprob) {
       const float l = token >= 0 ? x[token] : M;
-      a.logprob[row] = (float)((l == M ? 0.0 : (double)l - (double)M) - log(dl));
+      a.logprob[row] = (float)((l == M ? 0.0 : (double)l - (double)M) - log(tot.exp_sum));
     }
   }
 }
@@ -646,7 +885,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
 
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {
   (void)hipGetLastError();
-  sample_kernel<<<dim3((unsigned)a.m), dim3(kThreads), 0, stream>>>(a);
+  const dim3 slices((unsigned)a.slices, (unsigned)a.m), parts((unsigned)a.parts, (unsigned)a.m), rows((unsigned)a.m);
+  sample_stats_kernel<<<slices, 64 * kStatTiles, 0, stream>>>(a);
+  sample_weights_kernel<<<parts, kPassThreads, 0, stream>>>(a);
+  if (a.top_k || a.top_p) {
+    sample_cut_kernel<<<rows, kThreads, 0, stream>>>(a);
+    sample_collect_kernel<<<parts, kPassThreads, 0, stream>>>(a);
+  }
+  sample_draw_kernel<<<rows, kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -26,8 +26,8 @@ def rules(logits=A, ld=128, m=2, v=100, r=None, out=A + 4096, ld_out=128, **fiel
     q8.q8_logits_rules(logits, ld, m, v, r, out, ld_out, S0)
 
 
-def sample(logits=A, ld=128, m=2, v=100, token=A, logprob=A, ws=None, **fields):
-    q8.q8_sample(logits, ld, m, v, q8.make_sampling(fields.pop("u", A), **fields), token, logprob, S0, ws, 0)
+def sample(logits=A, ld=128, m=2, v=100, token=A, logprob=A, ws=A, ws_bytes=1 << 30, **fields):
+    q8.q8_sample(logits, ld, m, v, q8.make_sampling(fields.pop("u", A), **fields), token, logprob, S0, ws, ws_bytes)
 
 
 @pytest.mark.parametrize("call", [rules, sample])
@@ -65,6 +65,15 @@ def test_sample_refuses():
     refuse(3, lambda: q8.q8_sample(A, 128, 2, 100, None, A, A, S0), part="sampling")
     for k in ("temperature", "top_k", "top_p", "min_p", "u", "token", "logprob", "ws"):
         refuse(4, lambda k=k: sample(**{k: A + 4}))
+
+
+def test_sample_workspace():
+    need = q8.q8_sample_workspace_bytes(2, 100)
+    assert need > 4 << 20 and need % 256 == 0
+    assert q8.q8_sample_workspace_bytes(256, 131072) > need
+    assert q8.q8_sample_workspace_bytes(0, 100) == 0 and q8.q8_sample_workspace_bytes(1, (1 << 20) + 1) == 0
+    refuse(5, lambda: sample(ws=None), part="needed")
+    refuse(5, lambda: sample(ws_bytes=need - 1), part="needed")
 
 
 def test_oracle_of_the_rules():
