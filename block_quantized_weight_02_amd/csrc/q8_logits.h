@@ -71,6 +71,7 @@ struct SampleArgs {
   int slices, parts, row_tiles;               // of a row: statistics, workgroups a pass, tiles
   SliceStat *stats;                           // m x slices
   RowCut *cuts;                               // m
+  float *tops;                                // m x row_tiles: a tile's largest logit
   unsigned long long *tiles;                  // m x row_tiles: kept weight
   uint32_t *counts;                           // m x parts x kSampleBins
   unsigned long long *masses;                 // m x parts x kSampleBins

@@ -42,6 +42,7 @@ size_t sample_layout(SampleArgs &a, char *ws) {
   const size_t m = (size_t)a.m;
   a.stats = reinterpret_cast<SliceStat *>(take(m * a.slices * sizeof(SliceStat)));
   a.cuts = reinterpret_cast<RowCut *>(take(m * sizeof(RowCut)));
+  a.tops = reinterpret_cast<float *>(take(m * tiles * 4));
   a.tiles = reinterpret_cast<unsigned long long *>(take(m * tiles * 8));
   a.counts = reinterpret_cast<uint32_t *>(take(m * a.parts * kSampleBins * 4));
   a.masses = reinterpret_cast<unsigned long long *>(take(m * a.parts * kSampleBins * 8));

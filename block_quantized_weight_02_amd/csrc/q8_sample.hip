@@ -61,17 +61,34 @@ __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// A row's weights.  c64: 64 log2(e) / T.
+// 2^(j/64).
+__constant__ double kPow[64] = {
+    1.0, 1.0108892860517005, 1.0218971486541166, 1.0330248790212284,
+    1.0442737824274138, 1.0556451783605572, 1.0671404006768237, 1.0787607977571199,
+    1.0905077326652577, 1.1023825833078409, 1.1143867425958924, 1.1265216186082418,
+    1.1387886347566916, 1.1511892299529827, 1.1637248587775775, 1.1763969916502812,
+    1.189207115002721, 1.2021567314527031, 1.215247359980469, 1.22848053610687,
+    1.241857812073484, 1.2553807570246911, 1.2690509571917332, 1.2828700160787783,
+    1.2968395546510096, 1.3109612115247644, 1.3252366431597413, 1.3396675240533029,
+    1.3542555469368927, 1.3690024229745905, 1.383909881963832, 1.3989796725383112,
+    1.4142135623730951, 1.42961333839197, 1.4451808069770467, 1.460917794180647,
+    1.4768261459394993, 1.4929077282912648, 1.5091644275934228, 1.5255981507445384,
+    1.5422108254079407, 1.5590044002378369, 1.5759808451078865, 1.593142151342267,
+    1.6104903319492543, 1.6280274218573478, 1.6457554781539649, 1.6636765803267364,
+    1.681792830507429, 1.7001063537185235, 1.7186192981224779, 1.7373338352737062,
+    1.7562521603732995, 1.7753764925265212, 1.7947090750031072, 1.8142521755003989,
+    1.8340080864093424, 1.8539791250833855, 1.8741676341103, 1.8945759815869656,
+    1.9152065613971474, 1.9360617934922943, 1.9571441241754002, 1.9784560263879509};
+
+// A row's weights: 2^SH exp((l - M) / T), exactly 2^SH for the largest.  c64: 64 log2(e)
+// / T; sh64: 64 SH, added to the exponent at once.
 struct Weigher {
-  double c64, M;
-  float Mf;
+  double c64, M, sh64;
   int sh;
-  const double *pow;                       // 2^(j/64), in LDS
+  const double *pow;                       // kPow, in LDS
 };
-// 2^SH exp((l - M) / T); exactly: w of the largest is 2^SH.
 __device__ __forceinline__ double weight_of(const Weigher &w, float l) {
-  if (l == w.Mf) return (double)(1ull << w.sh);
-  const double t = fmax(((double)l - w.M) * w.c64, -64.0 * 80.0);
+  const double t = fmax(fma((double)l - w.M, w.c64, w.sh64), -1024.0);   // (-infinity: 2^-16)
   const double magic = 6755399441055744.0;                     // 1.5 * 2^52
   const double k = t + magic;
   const int ki = (int)(uint32_t)__double_as_longlong(k);
@@ -79,8 +96,7 @@ __device__ __forceinline__ double weight_of(const Weigher &w, float l) {
   // exp(r ln2 / 64): r ln2 / 64 below 0.0055, the first term left out 4e-14
   const double a = 0.010830424696249145, a2 = a * a;
   const double p = fma(r, fma(r, fma(r, fma(r, a2 * a2 / 24, a2 * a / 6), a2 / 2), a), 1.0);
-  const double x = ldexp(w.pow[ki & 63] * p, (ki >> 6) + w.sh);
-  return l == -INFINITY || !(w.Mf < INFINITY) ? 0.0 : x;
+  return ldexp(w.pow[ki & 63] * p, ki >> 6);
 }
 __device__ __forceinline__ u64 whole(double x) {               // x <= 2^51, rounded
   return (u64)__double_as_longlong(x + 4503599627370496.0) & 0xfffffffffffffull;
@@ -106,6 +122,18 @@ __device__ __forceinline__ void load_tile(const float *__restrict__ x, int V, in
   }
 #pragma unroll
   for (int j = 0; j < kVals; ++j) v[j] = v[j] == v[j] ? v[j] : -INFINITY;   // NaN: no weight
+}
+// A row whose largest logit is infinite: among 0 (those) and -infinity.
+__device__ __forceinline__ void among_infinite(bool infinite, float (&v)[kVals]) {
+  if (infinite) {
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) v[j] = v[j] == INFINITY ? 0.0f : -INFINITY;
+  }
+}
+__device__ __forceinline__ void load_tile(const float *__restrict__ x, int V, int tile, int lane, bool infinite,
+                                          float (&v)[kVals]) {
+  load_tile(x, V, tile, lane, v);
+  among_infinite(infinite, v);
 }
 __device__ __forceinline__ int index_of(int tile, int lane, int j) {
   return tile * kSampleTile + (j >> 2) * 256 + lane * 4 + (j & 3);
@@ -148,25 +176,23 @@ __device__ __forceinline__ Params params_of(const SampleArgs &a, int row) {
 
 constexpr float kFar = 60.0f;              // in units of T, below the largest: no weight
 struct Total {                             // the slices' statistics together
-  float M;
+  float M;                                 // 0 where the largest is infinite (among_infinite)
   int at;
   float mean;
-  double exp_sum;                          // of exp(l - M)
+  bool infinite, none;
 };
 // By each wave for itself, from the row's slices.
 __device__ __forceinline__ Total total_of(const SampleArgs &a, const Params &r, int row, int lane) {
   const SliceStat *st = a.stats + (size_t)row * a.slices;
-  float top = -INFINITY;
-  int at = 0x7fffffff;
+  SliceStat mine{-INFINITY, 0x7fffffff, 0.0f, 0.0f, 0u};
   double sum = 0.0;
   unsigned n = 0;
   for (int i = lane; i < a.slices; i += 64) {
     const SliceStat v = st[i];
-    if (v.top > top || (v.top == top && v.at < at)) {
-      top = v.top;
-      at = v.at;
-    }
+    if (v.top > mine.top || (v.top == mine.top && v.at < mine.at)) mine = v;
   }
+  float top = mine.top;
+  int at = mine.at;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     const float t2 = __shfl_xor(top, o);
@@ -176,40 +202,70 @@ __device__ __forceinline__ Total total_of(const SampleArgs &a, const Params &r, 
       at = a2;
     }
   }
-  double e = 0.0;
-  for (int i = lane; i < a.slices; i += 64) {
-    const SliceStat v = st[i];
-    // (slices of masks of the type's lowest value are no part of the mean)
-    if (v.top >= top - kFar * (r.greedy ? 1.0f : r.T)) {
-      sum += v.sum;
-      n += v.n;
+  // (slices of masks of the type's lowest value are no part of the mean)
+  const float least = top - kFar * (r.greedy ? 1.0f : r.T);
+  if (a.slices <= 64) {
+    if (mine.top >= least) {
+      sum = mine.sum;
+      n = mine.n;
     }
-    if (v.top > -INFINITY) e += v.top == top ? (double)v.exp_sum : (double)v.exp_sum * exp((double)v.top - (double)top);
+  } else {
+    for (int i = lane; i < a.slices; i += 64) {
+      const SliceStat v = st[i];
+      if (v.top >= least) {
+        sum += v.sum;
+        n += v.n;
+      }
+    }
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
-    e += __shfl_xor(e, o);
     sum += __shfl_xor(sum, o);
     n += __shfl_xor(n, o);
   }
   Total t;
-  t.M = top;
+  t.infinite = top == INFINITY;
+  t.none = top == -INFINITY;
+  t.M = t.infinite ? 0.0f : top;
   t.at = at;
-  t.mean = n ? (float)(sum / (double)n) : 0.0f;
-  t.exp_sum = e;
+  t.mean = n && !t.infinite ? (float)(sum / (double)n) : -1.0f;
   return t;
+}
+// sum exp(l - the largest), by a wave.
+__device__ __forceinline__ double exp_sum_of(const SampleArgs &a, int row, int lane) {
+  const SliceStat *st = a.stats + (size_t)row * a.slices;
+  float top = -INFINITY;
+  for (int i = lane; i < a.slices; i += 64) top = fmaxf(top, st[i].top);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  double e = 0.0;
+  for (int i = lane; i < a.slices; i += 64) {
+    const SliceStat v = st[i];
+    if (v.top > -INFINITY)
+      e += v.top == top ? (double)v.exp_sum : (double)v.exp_sum * exp((double)v.top - (double)top);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) e += __shfl_xor(e, o);
+  return e;
+}
+
+// A tile's largest logit, as load_tile gives it.
+__device__ __forceinline__ float top_of(const SampleArgs &a, const Total &t, int row, int tile) {
+  const float l = a.tops[(size_t)row * a.row_tiles + tile];
+  return t.infinite ? (l == INFINITY ? 0.0f : -INFINITY) : l;
 }
 
 __device__ __forceinline__ Weigher weigher_of(const SampleArgs &a, const Params &r, float M, const double *pow) {
   Weigher w;
   w.c64 = 92.332482616893656878 / (double)(r.greedy ? 1.0f : r.T);   // 64 log2(e)
   w.M = M;
-  w.Mf = M;
   w.sh = min(51, 62 - (32 - __clz(a.V)));
+  w.sh64 = 64.0 * w.sh;
   w.pow = pow;
   return w;
 }
-// A token's weight where min_p keeps it, else 0.
+// A token's weight where min_p keeps it, else 0.  (MIN false: the row has no min_p; the
+// test, made for each token, would keep their chains of fp64 apart.)
 struct Keep {
   Weigher w;
   float min_l;                             // below it: out without computing the weight
@@ -219,19 +275,21 @@ struct Keep {
     // (a margin over the roundings of the bound itself)
     min_l = r.min_p > 0.0 ? (float)(w.M + (double)r.T * (log(r.min_p) - 1e-3) - 1e-6 * fabs(w.M)) : -INFINITY;
   }
-  __device__ __forceinline__ u64 operator()(float l) const {
-    if (l < min_l) return 0;
+  template <bool MIN>
+  __device__ __forceinline__ u64 of(float l) const {
     const double d = weight_of(w, l);
-    return d < min_w ? 0 : whole(d);
+    return MIN && d < min_w ? 0 : whole(d);
   }
+  __device__ __forceinline__ u64 operator()(float l) const { return of<true>(l); }   // (no min_p: min_w is 0)
 };
+
 // Even steps of M - l: falling l, rising step; the last takes all the rest.
 struct Steps {
   float M, per;
   __device__ __forceinline__ Steps(const Total &t, bool by_p) {
     M = t.M;
     per = (float)(kBins - 1) / ((by_p ? 2.0f : 0.75f) * (M - t.mean));
-    if (!(per > 0.0f) || !(per < INFINITY) || !(M < INFINITY)) per = 1.0f;
+    if (!(per > 0.0f) || !(per < INFINITY)) per = 1.0f;
   }
   __device__ __forceinline__ int operator()(float l) const {
     return l == M ? 0 : (int)fminf((M - l) * per, (float)(kBins - 1));
@@ -243,9 +301,10 @@ struct Lds {
   u64 mass[kBins];
   uint32_t count[kBins];
   u64 tile[kMaxTiles];                     // kept weight of a tile
-  float cand_l[kCand];
-  int cand_i[kCand];
-  u64 cand_w[kCand];
+  u64 cand[kCand], order[kCand];           // packed: key, then the lower index first
+  int rank[kCand];
+  double exp_sum;
+  int kept;
   uint32_t wn[kWaves];
   u64 wmass[kWaves];
   // the state of the search
@@ -257,13 +316,35 @@ struct Lds {
   uint32_t cut_key;
   int cut_index;
   int pick_tile;
-  u64 pick_rest;
 };
 
 // Finds, over the histogram, the bin in which the order's cut falls: the first whose
 // running count reaches `want_n` or running weight reaches `want_w` (in doubles:
 // compared as p * W is).  before_n, before_w: what stands before the histogram's
 // range, and on return before the bin.  Leaves s.bin = kBins where none does.
+// A candidate as one number: larger logit first, then the lower index.
+__device__ __forceinline__ u64 packed(const Candidate &c) {
+  return (u64)key_of(c.l) << 32 | (uint32_t)~c.i;
+}
+// The n candidates of s.cand in falling order, one a thread (0 past them): each is
+// compared with all, `size` (a power of two from 64, at least n) of them by 1024 / size
+// threads each.
+__device__ u64 sorted(Lds &s, int n, int size) {
+  const int tid = threadIdx.x, c = tid & (size - 1), part = tid / size, of = kThreads / size;
+  const u64 mine = c < n ? s.cand[c] : 0;
+  if (tid < size) s.rank[tid] = 0;
+  __syncthreads();
+  const int lo = n * part / of, hi = n * (part + 1) / of;
+  int above = 0;
+#pragma unroll 8
+  for (int d = lo; d < hi; ++d) above += s.cand[d] > mine;
+  if (c < n) atomicAdd(&s.rank[c], above);
+  __syncthreads();
+  if (tid < n) s.order[s.rank[tid]] = mine;
+  __syncthreads();
+  return tid < n ? s.order[tid] : 0;
+}
+
 template <typename S>
 __device__ void find_bin(S &s, u64 want_n, double want_w) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -343,6 +424,7 @@ __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const Sam
   if (lane == 0) {
     wtop[wave] = top;
     wat[wave] = at;
+    if (t < a.row_tiles) a.tops[(size_t)row * a.row_tiles + t] = top;
   }
   __syncthreads();
   for (int i = 0; i < kStatTiles; ++i)
@@ -401,18 +483,24 @@ __device__ __forceinline__ void part_of_row(const SampleArgs &a, int part, int &
   hi = min(lo + each, tiles);
 }
 
-__global__ void __launch_bounds__(kPassThreads) sample_weights_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kPassThreads, 4) sample_weights_kernel(const SampleArgs a) {
   __shared__ double pow[64];
   __shared__ u64 mass[kBins];
   __shared__ uint32_t count[kBins];
   const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const float *__restrict__ x = a.logits + (size_t)row * a.ld;
+  int lo, hi;
+  part_of_row(a, blockIdx.x, lo, hi);
   const Params r = params_of(a, row);
   if (r.greedy) return;
-  const float *__restrict__ x = a.logits + (size_t)row * a.ld;
-  const Total tot = total_of(a, r, row, lane);
-  if (tot.M == -INFINITY) return;
-  if (tid < 64) pow[tid] = exp2((double)tid / 64.0);
   const bool cut = r.by_k || r.by_p;
+  int t = lo + wave;
+  float v[kVals];
+  // (the first tile's load goes out with the row's statistics)
+  if (cut || !(r.min_p > 0.0)) load_tile(x, a.V, t, lane, v);
+  const Total tot = total_of(a, r, row, lane);
+  if (tot.none) return;
+  if (tid < 64) pow[tid] = kPow[tid];
   if (cut)
     for (int i = tid; i < kBins; i += kPassThreads) {
       mass[i] = 0;
@@ -420,15 +508,21 @@ __global__ void __launch_bounds__(kPassThreads) sample_weights_kernel(const Samp
     }
   __syncthreads();
   const Keep keep(weigher_of(a, r, tot.M, pow), r);
-  int lo, hi;
-  part_of_row(a, blockIdx.x, lo, hi);
   if (!cut) {
-    for (int t = lo + wave; t < hi; t += kPassWaves) {
-      float v[kVals];
-      load_tile(x, a.V, t, lane, v);
+    for (; t < hi; t += kPassWaves) {
       u64 wt = 0;
+      if (keep.min_w > 0.0) {              // (few tiles hold any: the others are not read)
+        if (top_of(a, tot, row, t) >= keep.min_l) {
+          load_tile(x, a.V, t, lane, tot.infinite, v);
 #pragma unroll
-      for (int j = 0; j < kVals; ++j) wt += keep(v[j]);
+          for (int j = 0; j < kVals; ++j) wt += keep.of<true>(v[j]);
+        }
+      } else {
+        if (t >= lo + kPassWaves) load_tile(x, a.V, t, lane, v);
+        among_infinite(tot.infinite, v);
+#pragma unroll
+        for (int j = 0; j < kVals; ++j) wt += keep.of<false>(v[j]);
+      }
       wt = wave_sum(wt);
       if (lane == 0) a.tiles[(size_t)row * a.row_tiles + t] = wt;
     }
@@ -437,20 +531,35 @@ __global__ void __launch_bounds__(kPassThreads) sample_weights_kernel(const Samp
   const Steps step(tot, r.by_p);
   u64 rest_w = 0;
   uint32_t rest_n = 0;
-  for (int t = lo + wave; t < hi; t += kPassWaves) {
-    float v[kVals];
-    load_tile(x, a.V, t, lane, v);
+  for (; t < hi; t += kPassWaves) {
+    if (t >= lo + kPassWaves) load_tile(x, a.V, t, lane, v);
+    among_infinite(tot.infinite, v);
+    if (r.by_p) {
 #pragma unroll
-    for (int j = 0; j < kVals; ++j) {
-      const u64 wt = r.by_p ? whole(weight_of(keep.w, v[j])) : 0;
-      if (v[j] == -INFINITY) continue;
-      const int b = step(v[j]);
-      if (b == kBins - 1) {
-        rest_w += wt;
-        ++rest_n;
-      } else {
-        atomicAdd(&count[b], 1u);
-        if (r.by_p) atomicAdd(&mass[b], wt);
+      for (int j0 = 0; j0 < kVals; j0 += 4) {
+        u64 wt[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wt[j] = whole(weight_of(keep.w, v[j0 + j]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int b = step(v[j0 + j]);
+          if (b < kBins - 1) {
+            atomicAdd(&count[b], 1u);
+            atomicAdd(&mass[b], wt[j]);
+          } else {
+            rest_w += wt[j];               // (0 of -infinity)
+            rest_n += v[j0 + j] > -INFINITY;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) {
+        const int b = step(v[j]);
+        if (b < kBins - 1)
+          atomicAdd(&count[b], 1u);
+        else
+          rest_n += v[j] > -INFINITY;
       }
     }
   }
@@ -481,9 +590,8 @@ __global__ void __launch_bounds__(kThreads) sample_cut_kernel(const SampleArgs a
   } s;
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Params r = params_of(a, row);
+  // (a row of nothing has no histogram: what is found in its place is not used)
   if (!(r.by_k || r.by_p)) return;
-  const Total tot = total_of(a, r, row, lane);
-  if (tot.M == -INFINITY) return;
   u64 w0 = 0, w1 = 0;
   uint32_t n0 = 0, n1 = 0;
 #pragma unroll 4
@@ -528,41 +636,48 @@ __global__ void __launch_bounds__(kThreads) sample_cut_kernel(const SampleArgs a
 // ---- collect ----------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPassThreads) sample_collect_kernel(const SampleArgs a) {
   __shared__ double pow[64];
+  __shared__ Candidate found[kCand];
+  __shared__ int n_found;
+  __shared__ unsigned place;
   const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const float *__restrict__ x = a.logits + (size_t)row * a.ld;
+  int lo, hi;
+  part_of_row(a, blockIdx.x, lo, hi);
   const Params r = params_of(a, row);
   if (!(r.by_k || r.by_p)) return;
-  const float *__restrict__ x = a.logits + (size_t)row * a.ld;
   const Total tot = total_of(a, r, row, lane);
-  if (tot.M == -INFINITY) return;
   const int bin = a.cuts[row].bin;
-  if (a.cuts[row].bin_n > kCand) return;   // divided again by the draw
-  if (tid < 64) pow[tid] = exp2((double)tid / 64.0);
+  const unsigned bin_n = a.cuts[row].bin_n;
+  if (tot.none || bin_n > kCand) return;   // (too many: divided again by the draw)
+  if (tid < 64) pow[tid] = kPow[tid];
+  if (tid == 0) n_found = 0;
   __syncthreads();
   const Keep keep(weigher_of(a, r, tot.M, pow), r);
   const Steps step(tot, r.by_p);
-  int lo, hi;
-  part_of_row(a, blockIdx.x, lo, hi);
   for (int t = lo + wave; t < hi; t += kPassWaves) {
-    float v[kVals];
-    load_tile(x, a.V, t, lane, v);
     u64 wt = 0;
+    if (step(top_of(a, tot, row, t)) <= bin) {   // (a tile that holds none of the first is not read)
+      float v[kVals];
+      load_tile(x, a.V, t, lane, tot.infinite, v);
 #pragma unroll
-    for (int j = 0; j < kVals; ++j) {
-      if (v[j] == -INFINITY) continue;
-      const int b = step(v[j]);
-      if (b < bin) {
-        wt += keep(v[j]);
-      } else if (b == bin) {
-        const unsigned c = atomicAdd(&a.cuts[row].n_cand, 1u);
-        if (c < kCand) {
-          Candidate d{v[j], index_of(t, lane, j)};
-          a.cands[(size_t)row * kCand + c] = d;
+      for (int j = 0; j < kVals; ++j) {
+        const int b = step(v[j]);
+        if (b < bin && v[j] > -INFINITY) wt += keep(v[j]);
+        if (b == bin && v[j] > -INFINITY) {
+          const int c = atomicAdd(&n_found, 1);
+          if (c < kCand) found[c] = Candidate{v[j], index_of(t, lane, j)};
         }
       }
+      wt = wave_sum(wt);
     }
-    wt = wave_sum(wt);
     if (lane == 0) a.tiles[(size_t)row * a.row_tiles + t] = wt;
   }
+  __syncthreads();
+  // (a row's candidates are at most kCand in all)
+  if (tid == 0) place = n_found ? atomicAdd(&a.cuts[row].n_cand, (unsigned)n_found) : 0;
+  __syncthreads();
+  for (int c = tid; c < n_found; c += kPassThreads)
+    if (place + c < kCand) a.cands[(size_t)row * kCand + place + c] = found[c];
 }
 
 // ---- draw -------------------------------------------------------------------------------
@@ -575,7 +690,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
   const Params r = params_of(a, row);
   const Total tot = total_of(a, r, row, lane);
   const float M = tot.M;
-  if (M == -INFINITY) {                    // nothing may follow
+  if (tot.none) {                          // nothing may follow
     if (tid == 0) {
       a.token[row] = -1;
       if (a.logprob) a.logprob[row] = -INFINITY;
@@ -583,13 +698,16 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
     return;
   }
   if (r.greedy) {
-    if (tid == 0) {
-      a.token[row] = tot.at;
-      if (a.logprob) a.logprob[row] = (float)-log(tot.exp_sum);
+    if (wave == 0) {
+      const double e = a.logprob ? exp_sum_of(a, row, lane) : 1.0;
+      if (lane == 0) {
+        a.token[row] = tot.at;
+        if (a.logprob) a.logprob[row] = (float)-log(e);
+      }
     }
     return;
   }
-  if (tid < 64) s.pow[tid] = exp2((double)tid / 64.0);
+  if (tid < 64) s.pow[tid] = kPow[tid];
   const Weigher w = weigher_of(a, r, M, s.pow);
   const Keep kept_weight(w, r);
   const Steps bin_of(tot, r.by_p);
@@ -600,11 +718,16 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
   const bool again = cut && rc.bin_n > kCand;
   if (tid == 0) {
     s.n_cand = 0;
+    s.kept = 0;
     s.before_n = rc.before_n;
     s.before_w = rc.before_w;
     s.bin_n = rc.bin_n;
     s.cut_key = 0;                         // everything
     s.cut_index = 0x7fffffff;
+  }
+  if (a.logprob && wave == kWaves - 1) {
+    const double e = exp_sum_of(a, row, lane);
+    if (lane == 0) s.exp_sum = e;
   }
   if (!again)
     for (int t = tid; t < tiles; t += kThreads) s.tile[t] = a.tiles[(size_t)row * a.row_tiles + t];
@@ -618,12 +741,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
     uint32_t klo = 0, khi = 0;
     if (!again) {
       const int n = min((int)rc.n_cand, kCand);
-      for (int c = tid; c < n; c += kThreads) {
-        const Candidate d = a.cands[(size_t)row * kCand + c];
-        s.cand_l[c] = d.l;
-        s.cand_i[c] = d.i;
-        s.cand_w[c] = whole(weight_of(w, d.l));
-      }
+      if (tid < n) s.cand[tid] = packed(a.cands[(size_t)row * kCand + tid]);
       if (tid == 0) s.n_cand = n;
       __syncthreads();
     }
@@ -639,7 +757,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
         uint32_t lo = 0xffffffffu, hi = 0;
         for (int t = wave; t < tiles; t += kWaves) {
           float v[kVals];
-          load_tile(x, V, t, lane, v);
+          load_tile(x, V, t, lane, tot.infinite, v);
 #pragma unroll
           for (int j = 0; j < kVals; ++j)
             if (v[j] != -INFINITY && bin_of(v[j]) == bin) {
@@ -672,7 +790,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
       __syncthreads();
       for (int t = wave; t < tiles; t += kWaves) {
         float v[kVals];
-        load_tile(x, V, t, lane, v);
+        load_tile(x, V, t, lane, tot.infinite, v);
 #pragma unroll
         for (int j = 0; j < kVals; ++j) {
           const uint32_t k = key_of(v[j]);
@@ -697,7 +815,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
     __syncthreads();
     for (int t = wave; again && t < tiles; t += kWaves) {
       float v[kVals];
-      load_tile(x, V, t, lane, v);
+      load_tile(x, V, t, lane, tot.infinite, v);
       u64 wt = 0;
       uint32_t same = 0;
 #pragma unroll
@@ -713,11 +831,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
             ++same;
           } else {
             const int c = atomicAdd(&s.n_cand, 1);
-            if (c < kCand) {
-              s.cand_l[c] = v[j];
-              s.cand_i[c] = index_of(t, lane, j);
-              s.cand_w[c] = whole(weight_of(w, v[j]));
-            }
+            if (c < kCand) s.cand[c] = packed(Candidate{v[j], index_of(t, lane, j)});
           }
         }
       }
@@ -731,38 +845,32 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
     }
     __syncthreads();
     if (cuts && !equal) {
+      // sorted, a candidate a thread; then those before each are counted and summed
       const int n = min(s.n_cand, kCand);
-      for (int c = tid; c < n; c += kThreads) {
-        const float l = s.cand_l[c];
-        const int i = s.cand_i[c];
-        u64 rank = s.before_n, mass = s.before_w;
-        for (int d = 0; d < n; ++d) {
-          const float ld = s.cand_l[d];
-          if (ld > l || (ld == l && s.cand_i[d] < i)) {
-            ++rank;
-            mass += s.cand_w[d];
-          }
-        }
-        const bool keep = rank < want_n && (rank == 0 || (double)mass < want_w);
-        const bool next = rank + 1 < want_n && (double)(mass + s.cand_w[c]) < want_w;
-        if (keep) {
-          const u64 kw = kept_weight(l);
-          if (kw) atomicAdd(&s.tile[i / kSampleTile], kw);
-          // the last one kept: its successor, if it has one here, is not
-          bool last = !next;
-          if (next) {
-            last = true;
-            for (int d = 0; d < n; ++d)
-              if (s.cand_l[d] < l || (s.cand_l[d] == l && s.cand_i[d] > i)) {
-                last = false;
-                break;
-              }
-          }
-          if (last) {
-            s.cut_key = key_of(l);
-            s.cut_index = i;
-          }
-        }
+      int size = 64;
+      while (size < n) size *= 2;
+      const u64 e = sorted(s, n, size);
+      const float l = of_key((uint32_t)(e >> 32));
+      const int i = (int)~(uint32_t)e;
+      const bool live = tid < n;
+      const u64 mine = live ? whole(weight_of(w, l)) : 0;
+      u64 mass = wave_scan(mine, lane);
+      if (lane == 63) s.wmass[wave] = mass;
+      __syncthreads();
+      mass += s.before_w - mine;
+      for (int k = 0; k < wave; ++k) mass += s.wmass[k];
+      const u64 rank = s.before_n + tid;
+      const bool keep = live && rank < want_n && (rank == 0 || (double)mass < want_w);
+      if (keep) {
+        const u64 kw = kept_weight(l);
+        if (kw) atomicAdd(&s.tile[i / kSampleTile], kw);
+        // (kept ones are a prefix)
+        atomicMax(&s.kept, tid + 1);
+      }
+      __syncthreads();
+      if (tid + 1 == s.kept) {
+        s.cut_key = (uint32_t)(e >> 32);
+        s.cut_index = i;
       }
     } else if (cuts && equal) {
       // of equal logits the first `take` by index
@@ -790,7 +898,6 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
         }
         s.cut_key = kequal;
         s.pick_tile = edge;
-        s.pick_rest = take;
         // (how many of tile `edge` are kept)
         u64 earlier = 0;
         for (int t = 0; t < edge; ++t) earlier += s.count[t];
@@ -801,7 +908,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
       const u64 keep = s.before_n;
       if (wave == 0 && edge >= 0) {
         float v[kVals];
-        load_tile(x, V, edge, lane, v);
+        load_tile(x, V, edge, lane, tot.infinite, v);
         u64 seen = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -838,45 +945,49 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
     if (over) pick = t0 + f0;
     run = __shfl(over ? upto - mine : upto, f0);
   }
-  // and in it the token
+  // and in it the token: 16 tokens in a row a lane
   int token = -1;
   if (pick >= 0) {
+    const int base = pick * kSampleTile + lane * kVals;
     float v[kVals];
-    load_tile(x, V, pick, lane, v);
+#pragma unroll
+    for (int j = 0; j < kVals; j += 4) {
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (base + j < V) f = *reinterpret_cast<const float4 *>(x + base + j);
+      v[j] = f.x;
+      v[j + 1] = f.y;
+      v[j + 2] = f.z;
+      v[j + 3] = f.w;
+    }
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) v[j] = base + j < V && v[j] == v[j] ? v[j] : -INFINITY;
+    among_infinite(tot.infinite, v);
     const uint32_t ck = s.cut_key;
     const int ci = s.cut_index;
+    u64 wt[kVals], mine = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (token >= 0) break;
-      u64 wt[4], mine = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float l = v[4 * j + c];
-        const uint32_t k = key_of(l);
-        const bool in = l != -INFINITY && (k > ck || (k == ck && index_of(pick, lane, 4 * j + c) <= ci));
-        wt[c] = in ? kept_weight(l) : 0;
-        mine += wt[c];
-      }
-      const u64 upto = wave_scan(mine, lane) + run;
-      const u64 over = __ballot(upto > target);
-      u64 at = upto - mine;
-      int first = -1;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        at += wt[c];
-        if (first < 0 && at > target) first = index_of(pick, lane, 4 * j + c);
-      }
-      if (over)
-        token = __shfl(first, __ffsll(over) - 1);
-      else
-        run = __shfl(upto, 63);
+    for (int j = 0; j < kVals; ++j) {
+      const uint32_t k = key_of(v[j]);
+      const bool in = v[j] > -INFINITY && (k > ck || (k == ck && base + j <= ci));
+      wt[j] = in ? kept_weight(v[j]) : 0;
+      mine += wt[j];
     }
+    const u64 upto = wave_scan(mine, lane) + run;
+    const u64 over = __ballot(upto > target);
+    u64 at = upto - mine;
+    int first = -1;
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) {
+      at += wt[j];
+      if (first < 0 && at > target) first = base + j;
+    }
+    if (over) token = __shfl(first, __ffsll(over) - 1);
   }
   if (lane == 0) {
     a.token[row] = token;
     if (a.logprob) {
       const float l = token >= 0 ? x[token] : M;
-      a.logprob[row] = (float)((l == M ? 0.0 : (double)l - (double)M) - log(tot.exp_sum));
+      a.logprob[row] = (float)((tot.infinite ? 0.0 : (double)l - (double)M) - log(s.exp_sum));
     }
   }
 }
