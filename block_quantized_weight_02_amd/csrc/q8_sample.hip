@@ -13,28 +13,30 @@
 // of 2^(j/64) and four terms of the series: relative error below 1e-13), about twenty
 // instructions; it is taken only where a sum needs it.
 //
-// Five launches, the rows' vocabularies in slices so that one row too is worked on by
-// many CUs (one workgroup a row took 18 us for one row of 32000 tokens, 94 for 40 of
-// 50001 and, its slowest kind of row deciding, 268 for 256 of 131072):
+// Five passes:
 //   stats    of a slice: its largest logit with the lowest index, sum of exp(l - that),
-//            and the mean of what can weigh anything;
+//            the mean of what can weigh anything, and each tile's largest;
 //   weights  rows with a limit on the order: counts (for top_p weights too) of 2047 even
 //            steps of M - l, in LDS, a slice's histogram written out whole; rows without
 //            one: the weights' sum of each tile of 1024 tokens;
-//   cut      (a workgroup a row) the slices' histograms summed, and the step in which the
-//            order is cut;
+//   cut      the slices' histograms summed, and the step in which the order is cut;
 //   collect  the tokens of that step as candidates, and the tiles' sums of what stands
 //            before it;
-//   draw     (a workgroup a row) the candidates ordered by comparing each with all, and
-//            the tile that holds the drawn weight walked by one wave.  Where more than
-//            1024 tokens fall into one step, the step's range of logits (as ordered
-//            integers) is divided again here, down to equal logits, which are counted
-//            by index.
+//   draw     the candidates ordered by comparing each with all, and the tile that holds
+//            the drawn weight walked by one wave.  Where more than 1024 tokens fall into
+//            one step, the step's range of logits (as ordered integers) is divided again
+//            here, down to equal logits, which are counted by index.
 // The steps reach from M to 3/4 of the way to the mean where only top_k cuts (the cut is
 // near the top, and few tokens then add to LDS), and as far below the mean as M stands
 // above it where top_p does; what lies beyond is one last step, summed in registers.
 //
-// The first pass is bound by the rows' bytes, the second by fp64 and by additions in LDS.
+// They are five launches with the rows' vocabularies in slices, so that few long rows too
+// are worked on by many CUs, or one launch with a workgroup a row, where a row is short
+// enough for its registers (launch_sample has both sides' figures).  Mixed kinds of rows:
+// 1 x 32000 24 us, 40 x 50001 45, 256 x 131072 121 (greedy alone 38, top_k 100, top_p
+// 150).  The first pass of those 256 rows, 25 us, is bound by their 134 MB; the second,
+// 41, by fp64 and by additions in LDS; the collecting one, 29, by fp64; the two with a
+// workgroup a row (8 and 17), and all of them with few rows, by latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -47,7 +49,9 @@ constexpr int kThreads = 1024, kWaves = 16;   // of a workgroup a row
 constexpr int kBins = kSampleBins;
 constexpr int kCand = kSampleCand;
 constexpr int kMaxTiles = kMaxVocab / kSampleTile;
+static_assert(kMaxTiles <= kThreads && kCand <= kThreads, "a thread takes a tile's sum and a candidate");
 constexpr int kVals = 16;                  // tokens of a tile a lane holds
+constexpr int kHeldTokens = 2 * kWaves * kSampleTile;   // of a row in a workgroup's registers
 constexpr int kStatTiles = kSampleSlice / kSampleTile;   // one a wave
 
 typedef unsigned long long u64;
@@ -153,6 +157,19 @@ __device__ __forceinline__ u64 wave_scan(u64 v, int lane) {    // inclusive
   return v;
 }
 
+// The wave's largest logit, with the lowest index.
+__device__ __forceinline__ void largest(float &top, int &at) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float t2 = __shfl_xor(top, o);
+    const int a2 = __shfl_xor(at, o);
+    if (t2 > top || (t2 == top && a2 < at)) {
+      top = t2;
+      at = a2;
+    }
+  }
+}
+
 // What the launches hand on about a row.
 struct Params {                            // the row's limits
   float T;
@@ -193,15 +210,7 @@ __device__ __forceinline__ Total total_of(const SampleArgs &a, const Params &r, 
   }
   float top = mine.top;
   int at = mine.at;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float t2 = __shfl_xor(top, o);
-    const int a2 = __shfl_xor(at, o);
-    if (t2 > top || (t2 == top && a2 < at)) {
-      top = t2;
-      at = a2;
-    }
-  }
+  largest(top, at);
   // (slices of masks of the type's lowest value are no part of the mean)
   const float least = top - kFar * (r.greedy ? 1.0f : r.T);
   if (a.slices <= 64) {
@@ -283,6 +292,24 @@ struct Keep {
   __device__ __forceinline__ u64 operator()(float l) const { return of<true>(l); }   // (no min_p: min_w is 0)
 };
 
+// (four at a time: more of their chains at once take registers that no kernel here has)
+template <bool MIN>
+__device__ __forceinline__ u64 weight_of_tile(const Keep &keep, const float (&v)[kVals]) {
+  u64 wt = 0;
+  if constexpr (MIN) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) any |= v[j] >= keep.min_l;
+    if (!__any(any)) return 0;
+  }
+#pragma unroll
+  for (int j = 0; j < kVals; j += 4) {
+    wt += keep.of<MIN>(v[j]) + keep.of<MIN>(v[j + 1]) + keep.of<MIN>(v[j + 2]) + keep.of<MIN>(v[j + 3]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  return wave_sum(wt);
+}
+
 // Even steps of M - l: falling l, rising step; the last takes all the rest.
 struct Steps {
   float M, per;
@@ -307,6 +334,9 @@ struct Lds {
   int kept;
   uint32_t wn[kWaves];
   u64 wmass[kWaves];
+  float wtop[kWaves];
+  int wat[kWaves];
+  double wexp[kWaves], wsum[kWaves];
   // the state of the search
   int n_cand;
   int bin;
@@ -393,6 +423,53 @@ __device__ void clear_bins(Lds &s) {
   }
 }
 
+// A tile's tokens into the steps; those of the last step into rest_n and rest_w.
+__device__ __forceinline__ void add_to_steps(const float (&v)[kVals], const Weigher &w, const Steps &step, bool by_p,
+                                             uint32_t *count, u64 *mass, uint32_t &rest_n, u64 &rest_w) {
+  if (by_p) {
+#pragma unroll
+    for (int j0 = 0; j0 < kVals; j0 += 4) {
+      u64 wt[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wt[j] = whole(weight_of(w, v[j0 + j]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int b = step(v[j0 + j]);
+        if (b < kBins - 1) {
+          atomicAdd(&count[b], 1u);
+          atomicAdd(&mass[b], wt[j]);
+        } else {
+          rest_w += wt[j];                 // (0 of -infinity)
+          rest_n += v[j0 + j] > -INFINITY;
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) {
+      const int b = step(v[j]);
+      if (b < kBins - 1)
+        atomicAdd(&count[b], 1u);
+      else
+        rest_n += v[j] > -INFINITY;
+    }
+  }
+}
+
+// The histogram's weight in all.
+template <typename S>
+__device__ u64 total_mass(S &s) {
+  const int tid = threadIdx.x;
+  const u64 part = wave_sum(s.mass[2 * tid] + s.mass[2 * tid + 1]);
+  if ((tid & 63) == 0) s.wmass[tid >> 6] = part;
+  __syncthreads();
+  u64 W = 0;
+  for (int i = 0; i < kWaves; ++i) W += s.wmass[i];
+  __syncthreads();
+  return W;
+}
+
 // ---- stats ------------------------------------------------------------------------
 __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const SampleArgs a) {
   __shared__ float wtop[kStatTiles], wexp[kStatTiles];
@@ -412,15 +489,7 @@ __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const Sam
       top = v[j];
       at = index_of(t, lane, j);
     }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float t2 = __shfl_xor(top, o);
-    const int a2 = __shfl_xor(at, o);
-    if (t2 > top || (t2 == top && a2 < at)) {
-      top = t2;
-      at = a2;
-    }
-  }
+  largest(top, at);
   if (lane == 0) {
     wtop[wave] = top;
     wat[wave] = at;
@@ -514,16 +583,13 @@ __global__ void __launch_bounds__(kPassThreads, 4) sample_weights_kernel(const S
       if (keep.min_w > 0.0) {              // (few tiles hold any: the others are not read)
         if (top_of(a, tot, row, t) >= keep.min_l) {
           load_tile(x, a.V, t, lane, tot.infinite, v);
-#pragma unroll
-          for (int j = 0; j < kVals; ++j) wt += keep.of<true>(v[j]);
+          wt = weight_of_tile<true>(keep, v);
         }
       } else {
         if (t >= lo + kPassWaves) load_tile(x, a.V, t, lane, v);
         among_infinite(tot.infinite, v);
-#pragma unroll
-        for (int j = 0; j < kVals; ++j) wt += keep.of<false>(v[j]);
+        wt = weight_of_tile<false>(keep, v);
       }
-      wt = wave_sum(wt);
       if (lane == 0) a.tiles[(size_t)row * a.row_tiles + t] = wt;
     }
     return;
@@ -534,34 +600,7 @@ __global__ void __launch_bounds__(kPassThreads, 4) sample_weights_kernel(const S
   for (; t < hi; t += kPassWaves) {
     if (t >= lo + kPassWaves) load_tile(x, a.V, t, lane, v);
     among_infinite(tot.infinite, v);
-    if (r.by_p) {
-#pragma unroll
-      for (int j0 = 0; j0 < kVals; j0 += 4) {
-        u64 wt[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) wt[j] = whole(weight_of(keep.w, v[j0 + j]));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int b = step(v[j0 + j]);
-          if (b < kBins - 1) {
-            atomicAdd(&count[b], 1u);
-            atomicAdd(&mass[b], wt[j]);
-          } else {
-            rest_w += wt[j];               // (0 of -infinity)
-            rest_n += v[j0 + j] > -INFINITY;
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVals; ++j) {
-        const int b = step(v[j]);
-        if (b < kBins - 1)
-          atomicAdd(&count[b], 1u);
-        else
-          rest_n += v[j] > -INFINITY;
-      }
-    }
+    add_to_steps(v, keep.w, step, r.by_p, count, mass, rest_n, rest_w);
   }
   rest_w = wave_sum(rest_w);
   rest_n = (uint32_t)wave_sum(rest_n);
@@ -588,13 +627,13 @@ __global__ void __launch_bounds__(kThreads) sample_cut_kernel(const SampleArgs a
     u64 before_n, before_w;
     uint32_t bin_n;
   } s;
-  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row = blockIdx.x, tid = threadIdx.x;
   const Params r = params_of(a, row);
   // (a row of nothing has no histogram: what is found in its place is not used)
   if (!(r.by_k || r.by_p)) return;
   u64 w0 = 0, w1 = 0;
   uint32_t n0 = 0, n1 = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int p = 0; p < a.parts; ++p) {
     const size_t at = ((size_t)row * a.parts + p) * kBins + 2 * tid;
     const uint2 n = *reinterpret_cast<const uint2 *>(a.counts + at);
@@ -610,16 +649,11 @@ __global__ void __launch_bounds__(kThreads) sample_cut_kernel(const SampleArgs a
   s.mass[2 * tid + 1] = w1;
   s.count[2 * tid] = n0;
   s.count[2 * tid + 1] = n1;
-  const u64 part = wave_sum(w0 + w1);
-  if (lane == 0) s.wmass[wave] = part;
   if (tid == 0) {
     s.before_n = 0;
     s.before_w = 0;
   }
-  __syncthreads();
-  u64 W = 0;
-  for (int i = 0; i < kWaves; ++i) W += s.wmass[i];
-  __syncthreads();
+  const u64 W = total_mass(s);             // (a thread's own two steps first)
   find_bin(s, r.by_k ? (u64)r.k : ~0ull, r.by_p ? (double)r.p * (double)W : INFINITY);
   if (tid == 0) {
     RowCut c;
@@ -645,9 +679,9 @@ __global__ void __launch_bounds__(kPassThreads) sample_collect_kernel(const Samp
   part_of_row(a, blockIdx.x, lo, hi);
   const Params r = params_of(a, row);
   if (!(r.by_k || r.by_p)) return;
-  const Total tot = total_of(a, r, row, lane);
   const int bin = a.cuts[row].bin;
   const unsigned bin_n = a.cuts[row].bin_n;
+  const Total tot = total_of(a, r, row, lane);
   if (tot.none || bin_n > kCand) return;   // (too many: divided again by the draw)
   if (tid < 64) pow[tid] = kPow[tid];
   if (tid == 0) n_found = 0;
@@ -681,70 +715,39 @@ __global__ void __launch_bounds__(kPassThreads) sample_collect_kernel(const Samp
 }
 
 // ---- draw -------------------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs a) {
-  __shared__ Lds s;
+// The draw of one row.  `again`: step `bin` holds more tokens than s.cand, and neither
+// they nor the tiles' sums have been collected; else both are in LDS.  total_w: the
+// row's weight in all, for top_p.
+__device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Params &r, const Total &tot,
+                                         u64 total_w, int bin, bool again) {
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const float *__restrict__ x = a.logits + (size_t)row * a.ld;
   const int V = a.V, tiles = (V + kSampleTile - 1) / kSampleTile;
-  const Params r = params_of(a, row);
-  const Total tot = total_of(a, r, row, lane);
-  const float M = tot.M;
-  if (tot.none) {                          // nothing may follow
-    if (tid == 0) {
-      a.token[row] = -1;
-      if (a.logprob) a.logprob[row] = -INFINITY;
-    }
-    return;
-  }
-  if (r.greedy) {
-    if (wave == 0) {
-      const double e = a.logprob ? exp_sum_of(a, row, lane) : 1.0;
-      if (lane == 0) {
-        a.token[row] = tot.at;
-        if (a.logprob) a.logprob[row] = (float)-log(e);
-      }
-    }
-    return;
-  }
-  if (tid < 64) s.pow[tid] = kPow[tid];
-  const Weigher w = weigher_of(a, r, M, s.pow);
+  const Weigher w = weigher_of(a, r, tot.M, s.pow);
   const Keep kept_weight(w, r);
   const Steps bin_of(tot, r.by_p);
-  const bool cut = r.by_k || r.by_p;
   const bool by_k = r.by_k, by_p = r.by_p;
-  RowCut rc{};
-  if (cut) rc = a.cuts[row];
-  const bool again = cut && rc.bin_n > kCand;
+  const double u = a.u[row];
+  const auto each_tile = [&](auto f) {
+    for (int t = wave; t < tiles; t += kWaves) {
+      float v[kVals];
+      load_tile(x, V, t, lane, tot.infinite, v);
+      f(t, v);
+    }
+  };
   if (tid == 0) {
-    s.n_cand = 0;
     s.kept = 0;
-    s.before_n = rc.before_n;
-    s.before_w = rc.before_w;
-    s.bin_n = rc.bin_n;
     s.cut_key = 0;                         // everything
     s.cut_index = 0x7fffffff;
   }
-  if (a.logprob && wave == kWaves - 1) {
-    const double e = exp_sum_of(a, row, lane);
-    if (lane == 0) s.exp_sum = e;
-  }
-  if (!again)
-    for (int t = tid; t < tiles; t += kThreads) s.tile[t] = a.tiles[(size_t)row * a.row_tiles + t];
   __syncthreads();
 
-  if (cut) {
+  if (by_k || by_p) {
     const u64 want_n = by_k ? (u64)r.k : ~0ull;
-    const double want_w = by_p ? (double)r.p * (double)rc.total_w : INFINITY;
-    int bin = rc.bin;
+    const double want_w = by_p ? (double)r.p * (double)total_w : INFINITY;
     bool keyed = false, equal = false;
     uint32_t klo = 0, khi = 0;
-    if (!again) {
-      const int n = min((int)rc.n_cand, kCand);
-      if (tid < n) s.cand[tid] = packed(a.cands[(size_t)row * kCand + tid]);
-      if (tid == 0) s.n_cand = n;
-      __syncthreads();
-    }
     // more than kCand tokens in the step: an interval of keys, divided again
     while (bin < kBins && s.bin_n > kCand) {
       if (!keyed) {
@@ -755,9 +758,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
         }
         __syncthreads();
         uint32_t lo = 0xffffffffu, hi = 0;
-        for (int t = wave; t < tiles; t += kWaves) {
-          float v[kVals];
-          load_tile(x, V, t, lane, tot.infinite, v);
+        each_tile([&](int, const float (&v)[kVals]) {
 #pragma unroll
           for (int j = 0; j < kVals; ++j)
             if (v[j] != -INFINITY && bin_of(v[j]) == bin) {
@@ -765,7 +766,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
               lo = min(lo, k);
               hi = max(hi, k);
             }
-        }
+        });
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) {
           lo = min(lo, (uint32_t)__shfl_xor((int)lo, o));
@@ -788,9 +789,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
       while ((khi - klo) >> shift >= (uint32_t)kBins) ++shift;
       clear_bins(s);
       __syncthreads();
-      for (int t = wave; t < tiles; t += kWaves) {
-        float v[kVals];
-        load_tile(x, V, t, lane, tot.infinite, v);
+      each_tile([&](int, const float (&v)[kVals]) {
 #pragma unroll
         for (int j = 0; j < kVals; ++j) {
           const uint32_t k = key_of(v[j]);
@@ -799,7 +798,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
           atomicAdd(&s.count[b], 1u);
           if (by_p) atomicAdd(&s.mass[b], whole(weight_of(w, v[j])));
         }
-      }
+      });
       __syncthreads();
       find_bin(s, want_n, want_w);
       bin = s.bin;
@@ -813,36 +812,33 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
     // what stands before the interval, by tile; its tokens, or how many
     const uint32_t kequal = khi;
     __syncthreads();
-    for (int t = wave; again && t < tiles; t += kWaves) {
-      float v[kVals];
-      load_tile(x, V, t, lane, tot.infinite, v);
-      u64 wt = 0;
-      uint32_t same = 0;
+    if (again)
+      each_tile([&](int t, const float (&v)[kVals]) {
+        u64 wt = 0;
+        uint32_t same = 0;
 #pragma unroll
-      for (int j = 0; j < kVals; ++j) {
-        if (v[j] == -INFINITY) continue;
-        bool first, in;
-        const uint32_t k = key_of(v[j]);
-        first = k > khi;
-        in = k <= khi && k >= klo;
-        if (first) wt += kept_weight(v[j]);
-        if (in) {
-          if (equal) {
-            ++same;
-          } else {
-            const int c = atomicAdd(&s.n_cand, 1);
-            if (c < kCand) s.cand[c] = packed(Candidate{v[j], index_of(t, lane, j)});
+        for (int j = 0; j < kVals; ++j) {
+          if (v[j] == -INFINITY) continue;
+          const uint32_t k = key_of(v[j]);
+          if (k > khi) {
+            wt += kept_weight(v[j]);
+          } else if (k >= klo) {
+            if (equal) {
+              ++same;
+            } else {
+              const int c = atomicAdd(&s.n_cand, 1);
+              if (c < kCand) s.cand[c] = packed(Candidate{v[j], index_of(t, lane, j)});
+            }
           }
         }
-      }
-      wt = wave_sum(wt);
-      if (equal) same = (uint32_t)wave_sum(same);
-      if (lane == 0) {
-        s.tile[t] = wt;
-        // (equal logits: the histogram's room holds the tiles' counts)
-        if (equal) s.count[t] = same;
-      }
-    }
+        wt = wave_sum(wt);
+        if (equal) same = (uint32_t)wave_sum(same);
+        if (lane == 0) {
+          s.tile[t] = wt;
+          // (equal logits: the histogram's room holds the tiles' counts)
+          if (equal) s.count[t] = same;
+        }
+      });
     __syncthreads();
     if (cuts && !equal) {
       // sorted, a candidate a thread; then those before each are counted and summed
@@ -930,7 +926,6 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
   u64 total = 0;
   for (int t = lane; t < tiles; t += 64) total += s.tile[t];
   total = wave_sum(total);
-  const double u = a.u[row];
   const double f = floor((u > 0.0 ? u : 0.0) * (double)total);
   u64 target = f < (double)total ? (u64)f : total;
   if (target >= total) target = total - 1;
@@ -947,6 +942,7 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
   }
   // and in it the token: 16 tokens in a row a lane
   int token = -1;
+  float l = tot.M;
   if (pick >= 0) {
     const int base = pick * kSampleTile + lane * kVals;
     float v[kVals];
@@ -976,26 +972,260 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
     const u64 over = __ballot(upto > target);
     u64 at = upto - mine;
     int first = -1;
+    float of = 0.0f;
 #pragma unroll
     for (int j = 0; j < kVals; ++j) {
       at += wt[j];
-      if (first < 0 && at > target) first = base + j;
+      if (first < 0 && at > target) {
+        first = base + j;
+        of = v[j];
+      }
     }
-    if (over) token = __shfl(first, __ffsll(over) - 1);
+    if (over) {
+      token = __shfl(first, __ffsll(over) - 1);
+      l = __shfl(of, __ffsll(over) - 1);
+    }
   }
   if (lane == 0) {
     a.token[row] = token;
-    if (a.logprob) {
-      const float l = token >= 0 ? x[token] : M;
-      a.logprob[row] = (float)((tot.infinite ? 0.0 : (double)l - (double)M) - log(s.exp_sum));
-    }
+    // (infinite logits stand at 0 here, and M does)
+    if (a.logprob) a.logprob[row] = (float)((double)l - (double)tot.M - log(s.exp_sum));
   }
 }
 
-}  // namespace
+// What is not drawn: a row of nothing, and a greedy one.  exp_sum: of exp(l - M).
+__device__ __forceinline__ void store_nothing(const SampleArgs &a, int row) {
+  a.token[row] = -1;
+  if (a.logprob) a.logprob[row] = -INFINITY;
+}
+__device__ __forceinline__ void store_largest(const SampleArgs &a, int row, const Total &tot, double exp_sum) {
+  a.token[row] = tot.at;
+  if (a.logprob) a.logprob[row] = (float)-log(exp_sum);
+}
 
-hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {
-  (void)hipGetLastError();
+__global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs a) {
+  __shared__ Lds s;
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // (loads of what the passes before have left go out together, also what this kind of
+  // row does not use)
+  const Params r = params_of(a, row);
+  const RowCut rc = a.cuts[row];
+  const Candidate c = a.cands[(size_t)row * kCand + tid];
+  const u64 tile = tid < a.row_tiles ? a.tiles[(size_t)row * a.row_tiles + tid] : 0;
+  const Total tot = total_of(a, r, row, lane);
+  if (tot.none) {                          // nothing may follow
+    if (tid == 0) store_nothing(a, row);
+    return;
+  }
+  if (r.greedy) {
+    if (wave == 0) {
+      const double e = a.logprob ? exp_sum_of(a, row, lane) : 1.0;
+      if (lane == 0) store_largest(a, row, tot, e);
+    }
+    return;
+  }
+  if (tid < 64) s.pow[tid] = kPow[tid];
+  const bool cut = r.by_k || r.by_p;
+  const bool again = cut && rc.bin_n > kCand;
+  const int n = again || !cut ? 0 : min((int)rc.n_cand, kCand);
+  if (tid == 0) {
+    s.n_cand = n;
+    s.before_n = rc.before_n;
+    s.before_w = rc.before_w;
+    s.bin_n = rc.bin_n;
+  }
+  if (a.logprob && wave == kWaves - 1) {
+    const double e = exp_sum_of(a, row, lane);
+    if (lane == 0) s.exp_sum = e;
+  }
+  if (tid < n) s.cand[tid] = packed(c);
+  if (tid < a.row_tiles) s.tile[tid] = tile;
+  draw_row(s, a, r, tot, rc.total_w, rc.bin, again);
+}
+
+// ---- a row's five passes in one workgroup ------------------------------------------------
+// A wave's tiles: held in registers, or (TW 0) read by each pass.
+template <int TW>
+struct RowTiles {
+  int tiles, wave;
+  float v[TW][kVals];
+  __device__ __forceinline__ RowTiles(const float *x, int V, int wave_, int lane)
+      : tiles((V + kSampleTile - 1) / kSampleTile), wave(wave_) {
+#pragma unroll
+    for (int i = 0; i < TW; ++i) load_tile(x, V, wave + i * kWaves, lane, v[i]);
+  }
+  __device__ __forceinline__ void settle(bool infinite) {
+#pragma unroll
+    for (int i = 0; i < TW; ++i) among_infinite(infinite, v[i]);
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
+#pragma unroll
+    for (int i = 0; i < TW; ++i)
+      if (wave + i * kWaves < tiles) f(wave + i * kWaves, v[i]);
+  }
+};
+template <>
+struct RowTiles<0> {
+  const float *x;
+  int V, tiles, wave, lane;
+  bool infinite;
+  __device__ __forceinline__ RowTiles(const float *x_, int V_, int wave_, int lane_)
+      : x(x_), V(V_), tiles((V_ + kSampleTile - 1) / kSampleTile), wave(wave_), lane(lane_), infinite(false) {}
+  __device__ __forceinline__ void settle(bool inf) { infinite = inf; }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
+    float v[kVals], next[kVals];
+    load_tile(x, V, wave, lane, v);
+    for (int t = wave; t < tiles; t += kWaves) {
+      if (t + kWaves < tiles) load_tile(x, V, t + kWaves, lane, next);
+      among_infinite(infinite, v);
+      f(t, v);
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) v[j] = next[j];
+    }
+  }
+};
+
+template <int TW>
+__global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a) {
+  __shared__ Lds s;
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  RowTiles<TW> held(a.logits + (size_t)row * a.ld, a.V, wave, lane);
+  const Params r = params_of(a, row);
+  const bool cut = r.by_k || r.by_p;
+  if (tid < 64) s.pow[tid] = kPow[tid];
+  if (cut) clear_bins(s);
+  if (tid == 0) {
+    s.n_cand = 0;
+    s.before_n = 0;
+    s.before_w = 0;
+    s.bin_n = 0;
+  }
+
+  // the statistics
+  float top = -INFINITY;
+  int at = 0x7fffffff;
+  held.each([&](int t, const float (&v)[kVals]) {
+#pragma unroll
+    for (int j = 0; j < kVals; ++j)
+      if (v[j] > top) {
+        top = v[j];
+        at = index_of(t, lane, j);
+      }
+  });
+  largest(top, at);
+  if (lane == 0) {
+    s.wtop[wave] = top;
+    s.wat[wave] = at;
+  }
+  __syncthreads();
+  top = s.wtop[lane & (kWaves - 1)];
+  at = s.wat[lane & (kWaves - 1)];
+  largest(top, at);
+  Total tot;
+  tot.infinite = top == INFINITY;
+  tot.none = top == -INFINITY;
+  tot.M = tot.infinite ? 0.0f : top;
+  tot.at = at;
+  tot.mean = -1.0f;
+  if (tot.none) {
+    if (tid == 0) store_nothing(a, row);
+    return;
+  }
+  if (cut || a.logprob) {
+    const float least = top - kFar * (r.greedy ? 1.0f : r.T);
+    float e = 0.0f, sum = 0.0f;
+    uint32_t n = 0;
+    held.each([&](int, const float (&v)[kVals]) {
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) {
+        if (v[j] >= least && v[j] < INFINITY) {
+          sum += v[j];
+          ++n;
+        }
+        e += v[j] == top ? 1.0f : __builtin_amdgcn_exp2f((v[j] - top) * 1.44269504088896f);
+      }
+    });
+    double de = e, ds = sum;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      de += __shfl_xor(de, o);
+      ds += __shfl_xor(ds, o);
+      n += __shfl_xor(n, o);
+    }
+    if (lane == 0) {
+      s.wexp[wave] = de;
+      s.wsum[wave] = ds;
+      s.wn[wave] = n;
+    }
+    __syncthreads();
+    de = ds = 0.0;
+    n = 0;
+    for (int i = 0; i < kWaves; ++i) {
+      de += s.wexp[i];
+      ds += s.wsum[i];
+      n += s.wn[i];
+    }
+    if (tid == 0) s.exp_sum = de;
+    if (n && !tot.infinite) tot.mean = (float)(ds / (double)n);
+  }
+  if (r.greedy) {
+    if (tid == 0) store_largest(a, row, tot, a.logprob ? s.exp_sum : 1.0);
+    return;
+  }
+  held.settle(tot.infinite);
+
+  const Keep keep(weigher_of(a, r, tot.M, s.pow), r);
+  const Steps step(tot, r.by_p);
+  u64 total_w = 0;
+  int bin = kBins;
+  bool again = false;
+  if (!cut) {
+    held.each([&](int t, const float (&v)[kVals]) {
+      const u64 wt = keep.min_w > 0.0 ? weight_of_tile<true>(keep, v) : weight_of_tile<false>(keep, v);
+      if (lane == 0) s.tile[t] = wt;
+    });
+  } else {
+    uint32_t rest_n = 0;
+    u64 rest_w = 0;
+    held.each([&](int, const float (&v)[kVals]) {
+      add_to_steps(v, keep.w, step, r.by_p, s.count, s.mass, rest_n, rest_w);
+    });
+    rest_w = wave_sum(rest_w);
+    rest_n = (uint32_t)wave_sum(rest_n);
+    if (lane == 0 && rest_n) {
+      atomicAdd(&s.count[kBins - 1], rest_n);
+      atomicAdd(&s.mass[kBins - 1], rest_w);
+    }
+    __syncthreads();
+    total_w = total_mass(s);
+    find_bin(s, r.by_k ? (u64)r.k : ~0ull, r.by_p ? (double)r.p * (double)total_w : INFINITY);
+    bin = s.bin;
+    again = bin < kBins && s.bin_n > kCand;
+    if (!again)
+      held.each([&](int t, const float (&v)[kVals]) {
+        u64 wt = 0;
+#pragma unroll
+        for (int j = 0; j < kVals; ++j) {
+          const int b = v[j] > -INFINITY ? step(v[j]) : kBins;
+          if (b < bin) wt += keep(v[j]);
+          if (b == bin && bin < kBins) {
+            const int c = atomicAdd(&s.n_cand, 1);
+            if (c < kCand) s.cand[c] = packed(Candidate{v[j], index_of(t, lane, j)});
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        wt = wave_sum(wt);
+        if (lane == 0) s.tile[t] = wt;
+      });
+  }
+  draw_row(s, a, r, tot, total_w, bin, again);
+}
+
+hipError_t launch_slices(const SampleArgs &a, hipStream_t stream) {
   const dim3 slices((unsigned)a.slices, (unsigned)a.m), parts((unsigned)a.parts, (unsigned)a.m), rows((unsigned)a.m);
   sample_stats_kernel<<<slices, 64 * kStatTiles, 0, stream>>>(a);
   sample_weights_kernel<<<parts, kPassThreads, 0, stream>>>(a);
@@ -1004,6 +1234,25 @@ hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {
     sample_collect_kernel<<<parts, kPassThreads, 0, stream>>>(a);
   }
   sample_draw_kernel<<<rows, kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {
+  (void)hipGetLastError();
+  // One launch, a workgroup a row, where a row's tiles fit a workgroup's registers, and
+  // with rows for a third of the CUs up to twice that; else slices (us, mixed kinds of
+  // rows: 1 x 32000 26 against 34; 256 x 50001 58 against 76; 40 x 50001 51 against 45;
+  // 128 x 80000 83 against 72; 256 x 131072 137 against 121)
+  if (a.V <= kHeldTokens / 2)
+    sample_row_kernel<1><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
+  else if (a.V <= kHeldTokens)
+    sample_row_kernel<2><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
+  else if (a.V <= 2 * kHeldTokens && a.m >= 96)
+    sample_row_kernel<0><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
+  else
+    return launch_slices(a, stream);
   return hipGetLastError();
 }
 
