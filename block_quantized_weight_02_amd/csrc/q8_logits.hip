@@ -20,14 +20,16 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxSlice = 4096;
+constexpr int kQuads = kMaxSlice / (4 * kThreads);   // of a thread
+constexpr int kAhead = 8;                            // history loads in flight of a thread
 constexpr uint32_t kPrompt = 0x80000000u;   // the token stands in the prompt
 
 // HELD: rows may have a history; BIASED: biases.  Without either no LDS is used.
 template <bool HELD, bool BIASED>
 __global__ void __launch_bounds__(kThreads)
 logit_rules_kernel(const LogitRulesArgs a, int slice) {
-  __shared__ uint32_t count[HELD ? kMaxSlice : 1];
-  __shared__ int last[BIASED ? kMaxSlice : 1];
+  __shared__ uint4 count[HELD ? kMaxSlice / 4 : 1];
+  __shared__ int4 last[BIASED ? kMaxSlice / 4 : 1];
   const int r = blockIdx.y, tid = threadIdx.x;
   const int base = blockIdx.x * slice;
   const int n = min(slice, a.V - base);
@@ -40,28 +42,60 @@ logit_rules_kernel(const LogitRulesArgs a, int slice) {
     bias_hi = (int)min((int64_t)u.bias_start[r + 1], u.n_bias);
   }
   const bool any = (HELD && held > 0) || (BIASED && bias_hi > bias_lo);
+  const uint32_t *mask = nullptr;
+  if (u.mask) {
+    const int mr = u.mask_row ? u.mask_row[r] : r;
+    if (mr >= 0 && mr < u.mask_rows) mask = u.mask + (size_t)mr * u.ld_mask;
+  }
+  const float rep = HELD && u.repetition ? u.repetition[r] : 1.0f;
+  const float pres = HELD && u.presence ? u.presence[r] : 0.0f;
+  const float freq = HELD && u.frequency ? u.frequency[r] : 0.0f;
+  const float *in = a.logits + (size_t)r * a.ld + base;
+  float *out = a.out + (size_t)r * a.ld_out + base;
+  const bool in_place = in == out;
+
+  // What the masks leave of the slice, and its logits: on their way while the history
+  // is walked.  In place, only the quads that change are read, below.
+  uint32_t allowed[kQuads];
+  float4 v[kQuads];
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    const int i = 4 * (tid + q * kThreads);
+    allowed[q] = 15u;
+    if (mask && i < n) allowed[q] = mask[(base + i) >> 5] >> ((base + i) & 31) & 15u;
+  }
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    const int i = 4 * (tid + q * kThreads);
+    v[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!in_place && i < n && allowed[q]) v[q] = *reinterpret_cast<const float4 *>(in + i);   // (a row's stride is whole fours)
+  }
+
   if (any) {
-    for (int i = tid; i < n; i += kThreads) {
-      if constexpr (HELD) count[i] = 0;
-      if constexpr (BIASED) last[i] = -1;
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+      const int i = tid + q * kThreads;
+      if constexpr (HELD) count[i] = make_uint4(0, 0, 0, 0);
+      if constexpr (BIASED) last[i] = make_int4(-1, -1, -1, -1);
     }
     __syncthreads();
     if constexpr (HELD) {
+      uint32_t *cnt = reinterpret_cast<uint32_t *>(count);
       const int prompt = u.prompt_lens ? u.prompt_lens[r] : 0;
       const int32_t *tok = u.tokens + (size_t)r * u.ld_tokens;
-      for (int j0 = tid; j0 < held; j0 += 4 * kThreads) {
-        int t[4];
+      for (int j0 = tid; j0 < held; j0 += kAhead * kThreads) {
+        int t[kAhead];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) t[c] = tok[min(j0 + c * kThreads, held - 1)];
+        for (int c = 0; c < kAhead; ++c) t[c] = tok[min(j0 + c * kThreads, held - 1)];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kAhead; ++c) {
           const int j = j0 + c * kThreads;
           const int64_t at = (int64_t)t[c] - base;
           if (j < held && at >= 0 && at < n) {
             if (j >= prompt)
-              atomicAdd(&count[at], 1u);
+              atomicAdd(&cnt[at], 1u);
             else
-              atomicOr(&count[at], kPrompt);
+              atomicOr(&cnt[at], kPrompt);
           }
         }
       }
@@ -69,44 +103,33 @@ logit_rules_kernel(const LogitRulesArgs a, int slice) {
     if constexpr (BIASED) {
       for (int j = bias_lo + tid; j < bias_hi; j += kThreads) {
         const int64_t at = (int64_t)u.bias_token[j] - base;
-        if (at >= 0 && at < n) atomicMax(&last[at], j);
+        if (at >= 0 && at < n) atomicMax(reinterpret_cast<int *>(last) + at, j);
       }
     }
     __syncthreads();
   }
 
-  const float rep = HELD && u.repetition ? u.repetition[r] : 1.0f;
-  const float pres = HELD && u.presence ? u.presence[r] : 0.0f;
-  const float freq = HELD && u.frequency ? u.frequency[r] : 0.0f;
-  const uint32_t *mask = nullptr;
-  if (u.mask) {
-    const int mr = u.mask_row ? u.mask_row[r] : r;
-    if (mr >= 0 && mr < u.mask_rows) mask = u.mask + (size_t)mr * u.ld_mask;
-  }
-  const float *in = a.logits + (size_t)r * a.ld + base;
-  float *out = a.out + (size_t)r * a.ld_out + base;
-  const bool in_place = in == out;
-  for (int i = 4 * tid; i < n; i += 4 * kThreads) {
-    const int live = min(4, n - i);
-    uint32_t allowed = 15u;
-    if (mask) allowed = mask[(base + i) >> 5] >> ((base + i) & 31) & 15u;
-    uint32_t cnt[4] = {0, 0, 0, 0};
-    int bias[4] = {-1, -1, -1, -1};
-    bool touched = allowed != 15u;
-    if (any) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < live) {
-          if constexpr (HELD) cnt[c] = count[i + c];
-          if constexpr (BIASED) bias[c] = last[i + c];
-          touched |= cnt[c] != 0 || bias[c] >= 0;
-        }
+  for (int q = 0; q < kQuads; ++q) {
+    const int i = 4 * (tid + q * kThreads);
+    if (i >= n) break;
+    uint4 c4 = make_uint4(0, 0, 0, 0);
+    int4 b4 = make_int4(-1, -1, -1, -1);
+    if (any) {
+      if constexpr (HELD) c4 = count[i / 4];
+      if constexpr (BIASED) b4 = last[i / 4];
     }
-    if (in_place && !touched) continue;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (allowed) v = *reinterpret_cast<const float4 *>(in + i);   // (a row's stride is whole fours)
-    float x[4] = {v.x, v.y, v.z, v.w};
+    // (past the row's end nothing is counted)
+    const bool touched = allowed[q] != 15u || (c4.x | c4.y | c4.z | c4.w) != 0 ||
+                         (b4.x & b4.y & b4.z & b4.w) >= 0;
+    if (in_place) {
+      if (!touched) continue;
+      if (allowed[q]) v[q] = *reinterpret_cast<const float4 *>(in + i);
+    }
+    float x[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
     if (touched) {
+      const uint32_t cnt[4] = {c4.x, c4.y, c4.z, c4.w};
+      const int bias[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if constexpr (HELD) {
@@ -118,9 +141,10 @@ logit_rules_kernel(const LogitRulesArgs a, int slice) {
         }
         if constexpr (BIASED)
           if (bias[c] >= 0) x[c] += u.bias_value[bias[c]];
-        if (!(allowed >> c & 1u)) x[c] = -INFINITY;
+        if (!(allowed[q] >> c & 1u)) x[c] = -INFINITY;
       }
     }
+    const int live = min(4, n - i);
     if (live == 4) {
       *reinterpret_cast<float4 *>(out + i) = make_float4(x[0], x[1], x[2], x[3]);
     } else {
