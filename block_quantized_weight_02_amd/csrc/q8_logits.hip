@@ -1,13 +1,18 @@
 // q8_logits.hip -- the rules on a step's logits: penalties of the tokens that a
 // request holds, biases and grammar masks, in one pass over the rows.
 //
-// A workgroup takes a slice of one row's vocabulary.  It walks the whole of the
-// row's history (from the caches: every slice's workgroup reads it) and counts, in
-// LDS, the tokens that fall into its slice, and notes the last bias entry of each;
-// then it reads, changes and writes the slice.  So no counts are kept between calls
-// and none leave the chip, and integer counts do not depend on the order of the
-// additions.  Bound by the rows' bytes, read once and written once; four tokens a
-// thread and load.
+// A workgroup takes a slice of one row's vocabulary.  It sends for the slice's logits
+// and masks, walks the whole of the row's history (from the caches: every slice's
+// workgroup reads it) and counts, in LDS, the tokens that fall into its slice, and notes
+// the last bias entry of each; then it changes and writes the slice.  So no counts are
+// kept between calls and none leave the chip, and integer counts do not depend on the
+// order of the additions.
+//
+// Bound by the rows' bytes, read once and written once: 192 rows of 130001 take 39 us
+// without rules (the 200 MB at 5.1 TB/s) and 49 with histories of up to 4096 tokens,
+// biases and masks.  With the logits sent for after the walk it was 84; slices of 4096
+// tokens in workgroups of 256 threads 64, of 1024 61; slices of 2048 54, of 8192 (1024
+// threads) 48.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -18,7 +23,7 @@
 namespace q8 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kMaxSlice = 4096;
 constexpr int kQuads = kMaxSlice / (4 * kThreads);   // of a thread
 constexpr int kAhead = 8;                            // history loads in flight of a thread
