@@ -71,7 +71,7 @@ hipError_t launch_w4_unpack(const char *values, const char *scales, const char *
                             int64_t N, int group, uint8_t *u, uint16_t *s, uint8_t *z,
                             hipStream_t stream);
 
-// The tile kernel: rows 4, 16, 32 or 64 a workgroup (more rows in chunks), its waves (8
+// The tile kernel: rows 4, 16, 32 or 64 (Q8_0: 8 and 24 too) a workgroup (more in chunks), its waves (8
 // or 16) splitting K, each over `tiles` column tiles (the pair: both weights' tile).
 struct W4Plan {
   int rows, waves, tiles;

@@ -20,7 +20,10 @@
 //     -z sum x, all exact; the activation's bytes take the nibbles' order.
 //   * a group's blocks chain in one accumulator and are scaled once.
 //   * activation row 4 e + q sits in operand row 4 q + e, so that with up to 4 rows
-//     only the first of a lane's four results counts, and is scaled.
+//     only the first of a lane's four results counts, and is scaled; with Q8_0
+//     activations, whose results are each converted and scaled twice a block, of 8 or 24
+//     rows the first two of the last row group's (m = 24, K 5120, N 32001: 30.3 -> 27.6
+//     us, a pair of 8 rows, K 4096, N 14336, 17.3 -> 15.3; bf16 gains 2 %).
 // A wave has two stages in flight, taking turns: the weight's in two register sets, the
 // activation's rows (and Q8_0 scales) loaded straight into two places in LDS of the
 // wave's own, so that the registers hold weight alone and no wave waits for another.
@@ -95,10 +98,12 @@ constexpr int w4_waves_per_simd(int ACT, int RG, int EL, int NT, int GB) {
 
 // NT: column tiles a wave covers, sharing its activation stage: the pair's two weights'
 // (PAIR), or two of one weight side by side.
-template <int ACT, int W, int RG, int EL, int NT, int GB, bool ZEROS, bool PAIR>
+template <int ACT, int W, int RG, int EL, int LE, int NT, int GB, bool ZEROS, bool PAIR>
 __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)) w4_tile_kernel(const W4Args a) {
   constexpr bool kQ8 = ACT == kActQ8;
   constexpr int MR = w4_rows(RG, EL);
+  // results of a lane that count: of the last row group LE
+  const auto el = [](int rg) Q8_INLINE { return rg == RG - 1 ? LE : EL; };
   static_assert(!PAIR || NT == 2, "the pair's tiles of both weights");
   constexpr int QB = w4_stage_blocks(RG, NT);
   constexpr int CH = GB < QB ? GB : QB;      // of them, blocks that share a scale
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
               dx[0] = v.x; dx[1] = v.y; dx[2] = v.z; dx[3] = v.w;
             } else {
 #pragma unroll
-              for (int e = 0; e < EL; ++e) dx[e] = dp[e];
+              for (int e = 0; e < el(rg); ++e) dx[e] = dp[e];
             }
             // -8 sum x, or -sum x where zero points multiply it
             const long cst = ZEROS ? -1l : (long)0xf8f8f8f8f8f8f8f8ul;
@@ -317,11 +322,11 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
                 if constexpr (ZEROS) {
                   const int z = (int)((st.w[k].z[n] >> (8 * g)) & 0xffu);
 #pragma unroll
-                  for (int e = 0; e < EL; ++e) C[e] = __mul24(X[e], z);
+                  for (int e = 0; e < el(rg); ++e) C[e] = __mul24(X[e], z);
                 }
                 const i32x4_t D = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, w4_i8(wd[g]), C, 0, 0, 0);
 #pragma unroll
-                for (int e = 0; e < EL; ++e) {
+                for (int e = 0; e < el(rg); ++e) {
                   const float d = (float)D[e];
                   if constexpr (CH == 1)
                     acc[k][rg][g][e] = fmaf(dx[e] * sc[k][g], d, acc[k][rg][g][e]);
@@ -340,7 +345,7 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
 #pragma unroll
               for (int g = 0; g < 4; ++g)
 #pragma unroll
-                for (int e = 0; e < EL; ++e)
+                for (int e = 0; e < el(rg); ++e)
                   acc[k][rg][g][e] = fmaf(sc[k][g], tt[k][rg][g][e], acc[k][rg][g][e]);
         }
       } else {
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
               if constexpr (ZEROS) {
                 const float z = -16.0f - (float)((st.w[k].z[n] >> (8 * g)) & 0xffu);
 #pragma unroll
-                for (int e = 0; e < EL; ++e) D[rg][g][e] = z * X[rg][e];
+                for (int e = 0; e < el(rg); ++e) D[rg][g][e] = z * X[rg][e];
               }
             }
 #pragma unroll
@@ -396,7 +401,7 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
 #pragma unroll
-              for (int e = 0; e < EL; ++e)
+              for (int e = 0; e < el(rg); ++e)
                 acc[k][rg][g][e] = fmaf(sc[k][g], D[rg][g][e], acc[k][rg][g][e]);
         }
       }
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int e = 0; e < EL; ++e) asm volatile("" : "+v"(acc[k][rg][g][e]));
+            for (int e = 0; e < el(rg); ++e) asm volatile("" : "+v"(acc[k][rg][g][e]));
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int e = 0; e < EL; ++e)
+            for (int e = 0; e < el(rg); ++e)
               rw[(((k * RG + rg) * 4 + g) * EL + e) * 64 + lane] = acc[k][rg][g][e];
     }
     __syncthreads();
@@ -467,7 +472,7 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int e = 0; e < EL; ++e)
+            for (int e = 0; e < el(rg); ++e)
               acc[k][rg][g][e] += rw[(((k * RG + rg) * 4 + g) * EL + e) * 64 + lane];
     }
     __syncthreads();
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
-          for (int e = 0; e < EL; ++e) rw[(16 * rg + 4 * e + q) * 64 + 16 * g + i] = acc[k][rg][g][e];
+          for (int e = 0; e < el(rg); ++e) rw[(16 * rg + 4 * e + q) * 64 + 16 * g + i] = acc[k][rg][g][e];
     }
   }
   __syncthreads();
@@ -508,10 +513,10 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
   }
 }
 
-template <int ACT, int W, int RG, int EL, int NT, int GB, bool ZEROS, bool PAIR>
+template <int ACT, int W, int RG, int EL, int LE, int NT, int GB, bool ZEROS, bool PAIR>
 hipError_t launch_w4_k(const W4Args &a, hipStream_t stream) {
   constexpr int MR = w4_rows(RG, EL), lds = w4_lds(ACT, W, RG, EL, NT);
-  const auto kern = w4_tile_kernel<ACT, W, RG, EL, NT, GB, ZEROS, PAIR>;
+  const auto kern = w4_tile_kernel<ACT, W, RG, EL, LE, NT, GB, ZEROS, PAIR>;
   if constexpr (lds > 64 * 1024) {
     // once a device: dynamic LDS above the default 64 KiB
     static std::atomic<uint64_t> granted{0};
@@ -533,16 +538,16 @@ hipError_t launch_w4_k(const W4Args &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int ACT, int W, int RG, int EL, int NT, bool PAIR>
+template <int ACT, int W, int RG, int EL, int LE, int NT, bool PAIR>
 hipError_t launch_w4_g(const W4Args &a, hipStream_t stream) {
   const bool z = a.w.zeros != nullptr;
   switch (a.group) {
-    case 32: return z ? launch_w4_k<ACT, W, RG, EL, NT, 1, true, PAIR>(a, stream)
-                      : launch_w4_k<ACT, W, RG, EL, NT, 1, false, PAIR>(a, stream);
-    case 64: return z ? launch_w4_k<ACT, W, RG, EL, NT, 2, true, PAIR>(a, stream)
-                      : launch_w4_k<ACT, W, RG, EL, NT, 2, false, PAIR>(a, stream);
-    case 128: return z ? launch_w4_k<ACT, W, RG, EL, NT, 4, true, PAIR>(a, stream)
-                       : launch_w4_k<ACT, W, RG, EL, NT, 4, false, PAIR>(a, stream);
+    case 32: return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 1, true, PAIR>(a, stream)
+                      : launch_w4_k<ACT, W, RG, EL, LE, NT, 1, false, PAIR>(a, stream);
+    case 64: return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 2, true, PAIR>(a, stream)
+                      : launch_w4_k<ACT, W, RG, EL, LE, NT, 2, false, PAIR>(a, stream);
+    case 128: return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 4, true, PAIR>(a, stream)
+                       : launch_w4_k<ACT, W, RG, EL, LE, NT, 4, false, PAIR>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -554,20 +559,25 @@ hipError_t launch_w4_tile(const W4Plan &p, bool pair, const W4Args &a, hipStream
   if (a.m > p.rows && (a.split_k != 1 || a.ep.residual)) return hipErrorInvalidValue;
   if (!pair && p.tiles == 2 && a.split_k != 1) return hipErrorInvalidValue;
   const int key = p.rows * 1000 + p.waves * 10 + p.tiles;
-  if (pair) switch (key) {
-    case 4162: return launch_w4_g<ACT, 16, 1, 1, 2, true>(a, stream);
-    case 16082: return launch_w4_g<ACT, 8, 1, 4, 2, true>(a, stream);
-    case 32082: return launch_w4_g<ACT, 8, 2, 4, 2, true>(a, stream);
-    default: return hipErrorInvalidValue;
+  if constexpr (ACT == kActQ8) {
+    switch (pair ? -key : key) {
+      case 8081: return launch_w4_g<ACT, 8, 1, 4, 2, 1, false>(a, stream);
+      case 24081: return launch_w4_g<ACT, 8, 2, 4, 2, 1, false>(a, stream);
+      case 24082: return launch_w4_g<ACT, 8, 2, 4, 2, 2, false>(a, stream);
+      case -8082: return launch_w4_g<ACT, 8, 1, 4, 2, 2, true>(a, stream);
+      case -24082: return launch_w4_g<ACT, 8, 2, 4, 2, 2, true>(a, stream);
+    }
   }
-  switch (key) {
-    case 4081: return launch_w4_g<ACT, 8, 1, 1, 1, false>(a, stream);
-    case 4161: return launch_w4_g<ACT, 16, 1, 1, 1, false>(a, stream);
-    case 16081: return launch_w4_g<ACT, 8, 1, 4, 1, false>(a, stream);
-    case 16082: return launch_w4_g<ACT, 8, 1, 4, 2, false>(a, stream);
-    case 32081: return launch_w4_g<ACT, 8, 2, 4, 1, false>(a, stream);
-    case 32082: return launch_w4_g<ACT, 8, 2, 4, 2, false>(a, stream);
-    case 64081: return launch_w4_g<ACT, 8, 4, 4, 1, false>(a, stream);
+  switch (pair ? -key : key) {
+    case 4081: return launch_w4_g<ACT, 8, 1, 1, 1, 1, false>(a, stream);
+    case 4161: return launch_w4_g<ACT, 16, 1, 1, 1, 1, false>(a, stream);
+    case 16081: return launch_w4_g<ACT, 8, 1, 4, 4, 1, false>(a, stream);
+    case 32081: return launch_w4_g<ACT, 8, 2, 4, 4, 1, false>(a, stream);
+    case 32082: return launch_w4_g<ACT, 8, 2, 4, 4, 2, false>(a, stream);
+    case 64081: return launch_w4_g<ACT, 8, 4, 4, 4, 1, false>(a, stream);
+    case -4162: return launch_w4_g<ACT, 16, 1, 1, 1, 2, true>(a, stream);
+    case -16082: return launch_w4_g<ACT, 8, 1, 4, 4, 2, true>(a, stream);
+    case -32082: return launch_w4_g<ACT, 8, 2, 4, 4, 2, true>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -78,6 +78,16 @@ def test_exact_many_rows(m, group, zeros, fmt, act):
 
 
 @pytest.mark.parametrize("act", [BF16, Q8])
+@pytest.mark.parametrize("group,zeros,fmt", FORMS)
+@pytest.mark.parametrize("m", [6, 8, 9, 18, 23, 24, 25])
+def test_exact_part_filled_row_groups(m, group, zeros, fmt, act):
+    for K, N in ((160, 65), (1120, 130), (64, 24600)):
+        w = Weight(K, N, group, zeros, fmt, 5, exact=True).pack()
+        a = Act(m, K, act, 7, exact=True)
+        np.testing.assert_array_equal(u.real(u.gemv(a, w), N), a.times(w)[0], err_msg=f"{m}x{K}x{N}")
+
+
+@pytest.mark.parametrize("act", [BF16, Q8])
 @pytest.mark.parametrize("m,K,N,group,zeros,fmt", [
     (1, 4096, 1024, 128, False, 0), (1, 4096, 40, 32, True, 0), (2, 1024, 9000, 64, False, 1),
     (8, 14336, 512, 64, True, 1), (16, 4096, 320, 128, True, 0), (27, 2080, 1000, 32, False, 0),
@@ -173,7 +183,8 @@ def pair_tolerance(gate, up, bg, bu):
 
 PAIRS = [(1, 32, 1, 32, False, 0), (1, 4096, 1000, 64, False, 0), (4, 1056, 130, 128, True, 1),
          (16, 2048, 9000, 32, True, 0), (29, 1024, 200, 64, True, 1), (32, 512, 64, 128, False, 0),
-         (40, 512, 300, 32, False, 1), (128, 1024, 200, 128, True, 0), (257, 288, 520, 64, False, 0)]
+         (7, 1024, 300, 32, True, 1), (8, 512, 5000, 128, False, 0), (23, 2048, 130, 32, False, 0),
+         (24, 544, 9000, 64, True, 0), (40, 512, 300, 32, False, 1), (128, 1024, 200, 128, True, 0), (257, 288, 520, 64, False, 0)]
 
 
 @pytest.mark.parametrize("act", [BF16, Q8])
