@@ -49,7 +49,8 @@ constexpr int kThreads = 1024, kWaves = 16;   // of a workgroup a row
 constexpr int kBins = kSampleBins;
 constexpr int kCand = kSampleCand;
 constexpr int kMaxTiles = kMaxVocab / kSampleTile;
-static_assert(kMaxTiles <= kThreads && kCand <= kThreads, "a thread takes a tile's sum and a candidate");
+static_assert(kMaxTiles <= kThreads && kCand <= kThreads && kSampleTile == kThreads,
+              "a thread takes a tile's sum, a candidate and a token of the drawn tile");
 constexpr int kVals = 16;                  // tokens of a tile a lane holds
 constexpr int kHeldTokens = 2 * kWaves * kSampleTile;   // of a row in a workgroup's registers
 constexpr int kStatTiles = kSampleSlice / kSampleTile;   // one a wave
@@ -143,31 +144,58 @@ __device__ __forceinline__ int index_of(int tile, int lane, int j) {
   return tile * kSampleTile + (j >> 2) * 256 + lane * 4 + (j & 3);
 }
 
-__device__ __forceinline__ u64 wave_sum(u64 v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+// Reductions over the wave by lane moves within the vector unit (a step of a shuffle
+// through LDS takes ten times as long, and few rows are bound by latency): rows of 16
+// lanes first, then each row's last lane into the rows behind it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 moved(u64 v) {                  // 0 where nothing comes
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+  return (u64)(uint32_t)hi << 32 | (uint32_t)lo;
 }
-__device__ __forceinline__ u64 wave_scan(u64 v, int lane) {    // inclusive
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const u64 w = __shfl_up(v, o);
-    if (lane >= o) v += w;
-  }
-  return v;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+  return __longlong_as_double((long long)moved<CTRL, ROWS>((u64)__double_as_longlong(v)));
+}
+template <typename T, typename F>
+__device__ __forceinline__ T row_scan(T v, F f) {              // of 16 lanes, inclusive
+  v = f(v, moved<0x111, 0xf>(v));
+  v = f(v, moved<0x112, 0xf>(v));
+  v = f(v, moved<0x114, 0xf>(v));
+  return f(v, moved<0x118, 0xf>(v));
+}
+template <typename T, typename F>
+__device__ __forceinline__ T wave_scan(T v, F f) {             // inclusive
+  v = row_scan(v, f);
+  v = f(v, moved<0x142, 0xa>(v));
+  return f(v, moved<0x143, 0xc>(v));
+}
+__device__ __forceinline__ uint32_t of_lane(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ u64 of_lane(u64 v, int lane) {
+  return (u64)of_lane((uint32_t)(v >> 32), lane) << 32 | of_lane((uint32_t)v, lane);
+}
+__device__ __forceinline__ double of_lane(double v, int lane) {
+  return __longlong_as_double((long long)of_lane((u64)__double_as_longlong(v), lane));
+}
+struct Add {
+  template <typename T>
+  __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) { return wave_scan(v, Add{}); }
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) { return of_lane(wave_scan(v, Add{}), 63); }
 
-// The wave's largest logit, with the lowest index.
-__device__ __forceinline__ void largest(float &top, int &at) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float t2 = __shfl_xor(top, o);
-    const int a2 = __shfl_xor(at, o);
-    if (t2 > top || (t2 == top && a2 < at)) {
-      top = t2;
-      at = a2;
-    }
-  }
+// A logit and its index as one number: larger logit first, then the lower index.
+__device__ __forceinline__ u64 packed(float l, int i) { return (u64)key_of(l) << 32 | (uint32_t)~i; }
+__device__ __forceinline__ u64 wave_largest(u64 v) {
+  return of_lane(wave_scan(v, [](u64 a, u64 b) { return a > b ? a : b; }), 63);
 }
 
 // What the launches hand on about a row.
@@ -201,61 +229,52 @@ struct Total {                             // the slices' statistics together
 // By each wave for itself, from the row's slices.
 __device__ __forceinline__ Total total_of(const SampleArgs &a, const Params &r, int row, int lane) {
   const SliceStat *st = a.stats + (size_t)row * a.slices;
-  SliceStat mine{-INFINITY, 0x7fffffff, 0.0f, 0.0f, 0u};
-  double sum = 0.0;
-  unsigned n = 0;
+  u64 best = 0;
+  SliceStat mine{};
   for (int i = lane; i < a.slices; i += 64) {
-    const SliceStat v = st[i];
-    if (v.top > mine.top || (v.top == mine.top && v.at < mine.at)) mine = v;
+    mine = st[i];
+    const u64 v = packed(mine.top, mine.at);
+    best = v > best ? v : best;
   }
-  float top = mine.top;
-  int at = mine.at;
-  largest(top, at);
+  best = wave_largest(best);
+  const float top = of_key((uint32_t)(best >> 32));
   // (slices of masks of the type's lowest value are no part of the mean)
   const float least = top - kFar * (r.greedy ? 1.0f : r.T);
-  if (a.slices <= 64) {
+  double sum = 0.0;
+  uint32_t n = 0;
+  for (int i = lane; i < a.slices; i += 64) {
+    if (a.slices > 64) mine = st[i];
     if (mine.top >= least) {
-      sum = mine.sum;
-      n = mine.n;
-    }
-  } else {
-    for (int i = lane; i < a.slices; i += 64) {
-      const SliceStat v = st[i];
-      if (v.top >= least) {
-        sum += v.sum;
-        n += v.n;
-      }
+      sum += mine.sum;
+      n += mine.n;
     }
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    sum += __shfl_xor(sum, o);
-    n += __shfl_xor(n, o);
-  }
+  sum = wave_sum(sum);
+  n = wave_sum(n);
   Total t;
   t.infinite = top == INFINITY;
   t.none = top == -INFINITY;
   t.M = t.infinite ? 0.0f : top;
-  t.at = at;
+  t.at = (int)~(uint32_t)best;
   t.mean = n && !t.infinite ? (float)(sum / (double)n) : -1.0f;
   return t;
 }
 // sum exp(l - the largest), by a wave.
 __device__ __forceinline__ double exp_sum_of(const SampleArgs &a, int row, int lane) {
   const SliceStat *st = a.stats + (size_t)row * a.slices;
-  float top = -INFINITY;
-  for (int i = lane; i < a.slices; i += 64) top = fmaxf(top, st[i].top);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  u64 best = 0;
+  for (int i = lane; i < a.slices; i += 64) {
+    const u64 v = packed(st[i].top, 0);
+    best = v > best ? v : best;
+  }
+  const float top = of_key((uint32_t)(wave_largest(best) >> 32));
   double e = 0.0;
   for (int i = lane; i < a.slices; i += 64) {
     const SliceStat v = st[i];
     if (v.top > -INFINITY)
       e += v.top == top ? (double)v.exp_sum : (double)v.exp_sum * exp((double)v.top - (double)top);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) e += __shfl_xor(e, o);
-  return e;
+  return wave_sum(e);
 }
 
 // A tile's largest logit, as load_tile gives it.
@@ -330,12 +349,10 @@ struct Lds {
   u64 tile[kMaxTiles];                     // kept weight of a tile
   u64 cand[kCand], order[kCand];           // packed: key, then the lower index first
   int rank[kCand];
-  double exp_sum;
+  double log_sum;                          // of exp(l - M)
   int kept;
   uint32_t wn[kWaves];
   u64 wmass[kWaves];
-  float wtop[kWaves];
-  int wat[kWaves];
   double wexp[kWaves], wsum[kWaves];
   // the state of the search
   int n_cand;
@@ -348,14 +365,6 @@ struct Lds {
   int pick_tile;
 };
 
-// Finds, over the histogram, the bin in which the order's cut falls: the first whose
-// running count reaches `want_n` or running weight reaches `want_w` (in doubles:
-// compared as p * W is).  before_n, before_w: what stands before the histogram's
-// range, and on return before the bin.  Leaves s.bin = kBins where none does.
-// A candidate as one number: larger logit first, then the lower index.
-__device__ __forceinline__ u64 packed(const Candidate &c) {
-  return (u64)key_of(c.l) << 32 | (uint32_t)~c.i;
-}
 // The n candidates of s.cand in falling order, one a thread (0 past them): each is
 // compared with all, `size` (a power of two from 64, at least n) of them by 1024 / size
 // threads each.
@@ -375,27 +384,43 @@ __device__ u64 sorted(Lds &s, int n, int size) {
   return tid < n ? s.order[tid] : 0;
 }
 
-template <typename S>
-__device__ void find_bin(S &s, u64 want_n, double want_w) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// Of a number each wave has put into LDS: the sum over the waves before this one, and
+// over all.
+template <typename T>
+__device__ __forceinline__ void across_waves(const T *of, int wave, T &before, T &all) {
+  const T upto = row_scan(of[threadIdx.x & (kWaves - 1)], Add{});
+  all = of_lane(upto, kWaves - 1);
+  before = wave ? of_lane(upto, wave - 1) : T(0);
+}
+static_assert(kWaves == 16, "a row of lanes takes a value of each wave");
+
+// Finds, over the histogram, the bin in which the order's cut falls: the first whose
+// running count reaches `want_n` or running weight reaches want_w(the histogram's weight)
+// (in doubles: compared as p * W is).  before_n, before_w: what stands before the
+// histogram's range, and on return before the bin.  Leaves s.bin = kBins where none does.
+// Returns the histogram's weight.
+template <typename S, typename F>
+__device__ u64 find_bin(S &s, u64 want_n, F want_of) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // two bins a thread
-  const u64 n0 = s.count[2 * tid], n1 = s.count[2 * tid + 1];
+  const uint32_t n0 = s.count[2 * tid], n1 = s.count[2 * tid + 1];
   const u64 w0 = s.mass[2 * tid], w1 = s.mass[2 * tid + 1];
-  u64 n = wave_scan(n0 + n1, lane), w = wave_scan(w0 + w1, lane);
+  const uint32_t ns = wave_scan(n0 + n1);
+  const u64 ws = wave_scan(w0 + w1);
   if (lane == 63) {
-    s.wn[wave] = (uint32_t)n;
-    s.wmass[wave] = w;
+    s.wn[wave] = ns;
+    s.wmass[wave] = ws;
   }
   if (tid == 0) s.bin = kBins;
-  __syncthreads();
-  for (int i = 0; i < wave; ++i) {
-    n += s.wn[i];
-    w += s.wmass[i];
-  }
   const u64 bn = s.before_n, bw = s.before_w;
-  n += bn;
-  w += bw;
   __syncthreads();
+  uint32_t n_before, n_all;
+  u64 w_before, w_all;
+  across_waves(s.wn, wave, n_before, n_all);
+  across_waves(s.wmass, wave, w_before, w_all);
+  const double want_w = want_of(w_all);
+  const u64 n = bn + n_before + ns, w = bw + w_before + ws;
   const u64 na = n - n1, wa = w - w1;      // through the thread's first bin
   const u64 np = na - n0, wp = wa - w0;    // before it
   const auto reached = [&](u64 c, u64 m) { return c >= want_n || (double)m >= want_w; };
@@ -404,16 +429,17 @@ __device__ void find_bin(S &s, u64 want_n, double want_w) {
   const bool before = tid == 0 ? false : reached(np, wp);
   if (!before && reached(na, wa)) {
     s.bin = 2 * tid;
-    s.bin_n = (uint32_t)n0;
+    s.bin_n = n0;
     s.before_n = np;
     s.before_w = wp;
   } else if (!before && reached(n, w)) {
     s.bin = 2 * tid + 1;
-    s.bin_n = (uint32_t)n1;
+    s.bin_n = n1;
     s.before_n = na;
     s.before_w = wa;
   }
   __syncthreads();
+  return w_all;
 }
 
 __device__ void clear_bins(Lds &s) {
@@ -457,19 +483,6 @@ __device__ __forceinline__ void add_to_steps(const float (&v)[kVals], const Weig
   }
 }
 
-// The histogram's weight in all.
-template <typename S>
-__device__ u64 total_mass(S &s) {
-  const int tid = threadIdx.x;
-  const u64 part = wave_sum(s.mass[2 * tid] + s.mass[2 * tid + 1]);
-  if ((tid & 63) == 0) s.wmass[tid >> 6] = part;
-  __syncthreads();
-  u64 W = 0;
-  for (int i = 0; i < kWaves; ++i) W += s.wmass[i];
-  __syncthreads();
-  return W;
-}
-
 // ---- stats ------------------------------------------------------------------------
 __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const SampleArgs a) {
   __shared__ float wtop[kStatTiles], wexp[kStatTiles];
@@ -481,15 +494,17 @@ __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const Sam
   const int t = slice * kStatTiles + wave;
   float v[kVals];
   load_tile(x, a.V, t, lane, v);
-  float top = -INFINITY;
-  int at = 0x7fffffff;
+  float top = v[0];
+  int at = index_of(t, lane, 0);
 #pragma unroll
-  for (int j = 0; j < kVals; ++j)
+  for (int j = 1; j < kVals; ++j)
     if (v[j] > top) {
       top = v[j];
       at = index_of(t, lane, j);
     }
-  largest(top, at);
+  const u64 best = wave_largest(packed(top, at));
+  top = of_key((uint32_t)(best >> 32));
+  at = (int)~(uint32_t)best;
   if (lane == 0) {
     wtop[wave] = top;
     wat[wave] = at;
@@ -515,16 +530,11 @@ __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const Sam
     e += v[j] == top ? (top > -INFINITY ? 1.0f : 0.0f)
                      : __builtin_amdgcn_exp2f((v[j] - top) * 1.44269504088896f);
   }
-  double ds = sum;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    ds += __shfl_xor(ds, o);
-    e += __shfl_xor(e, o);
-    n += __shfl_xor(n, o);
-  }
+  const double ds = wave_sum((double)sum), de = wave_sum((double)e);
+  n = wave_sum(n);
   if (lane == 0) {
     wsum[wave] = ds;
-    wexp[wave] = e;
+    wexp[wave] = (float)de;
     wn[wave] = n;
   }
   __syncthreads();
@@ -603,7 +613,7 @@ __global__ void __launch_bounds__(kPassThreads, 4) sample_weights_kernel(const S
     add_to_steps(v, keep.w, step, r.by_p, count, mass, rest_n, rest_w);
   }
   rest_w = wave_sum(rest_w);
-  rest_n = (uint32_t)wave_sum(rest_n);
+  rest_n = wave_sum(rest_n);
   if (lane == 0 && rest_n) {
     atomicAdd(&count[kBins - 1], rest_n);
     atomicAdd(&mass[kBins - 1], rest_w);
@@ -653,8 +663,8 @@ __global__ void __launch_bounds__(kThreads) sample_cut_kernel(const SampleArgs a
     s.before_n = 0;
     s.before_w = 0;
   }
-  const u64 W = total_mass(s);             // (a thread's own two steps first)
-  find_bin(s, r.by_k ? (u64)r.k : ~0ull, r.by_p ? (double)r.p * (double)W : INFINITY);
+  __syncthreads();
+  const u64 W = find_bin(s, r.by_k ? (u64)r.k : ~0ull, [&](u64 all) { return r.by_p ? (double)r.p * (double)all : INFINITY; });
   if (tid == 0) {
     RowCut c;
     c.bin = s.bin;
@@ -800,7 +810,7 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
         }
       });
       __syncthreads();
-      find_bin(s, want_n, want_w);
+      find_bin(s, want_n, [&](u64) { return want_w; });
       bin = s.bin;
       if (bin >= kBins) break;             // (the range held the cut: it does not happen)
       khi = khi - ((uint32_t)bin << shift);
@@ -827,12 +837,12 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
               ++same;
             } else {
               const int c = atomicAdd(&s.n_cand, 1);
-              if (c < kCand) s.cand[c] = packed(Candidate{v[j], index_of(t, lane, j)});
+              if (c < kCand) s.cand[c] = packed(v[j], index_of(t, lane, j));
             }
           }
         }
         wt = wave_sum(wt);
-        if (equal) same = (uint32_t)wave_sum(same);
+        if (equal) same = wave_sum(same);
         if (lane == 0) {
           s.tile[t] = wt;
           // (equal logits: the histogram's room holds the tiles' counts)
@@ -850,11 +860,12 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
       const int i = (int)~(uint32_t)e;
       const bool live = tid < n;
       const u64 mine = live ? whole(weight_of(w, l)) : 0;
-      u64 mass = wave_scan(mine, lane);
+      u64 mass = wave_scan(mine);
       if (lane == 63) s.wmass[wave] = mass;
       __syncthreads();
-      mass += s.before_w - mine;
-      for (int k = 0; k < wave; ++k) mass += s.wmass[k];
+      u64 earlier, all;
+      across_waves(s.wmass, wave, earlier, all);
+      mass += s.before_w - mine + earlier;
       const u64 rank = s.before_n + tid;
       const bool keep = live && rank < want_n && (rank == 0 || (double)mass < want_w);
       if (keep) {
@@ -910,7 +921,7 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
         for (int j = 0; j < 4; ++j) {
           u64 mine = 0;
           for (int c = 0; c < 4; ++c) mine += v[4 * j + c] != -INFINITY && key_of(v[4 * j + c]) == kequal;
-          u64 n = wave_scan(mine, lane) - mine + seen;
+          u64 n = wave_scan(mine) - mine + seen;
           for (int c = 0; c < 4; ++c)
             if (v[4 * j + c] != -INFINITY && key_of(v[4 * j + c]) == kequal && ++n == keep)
               s.cut_index = index_of(edge, lane, 4 * j + c);
@@ -921,8 +932,7 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
     __syncthreads();
   }
 
-  // ---- the token
-  if (wave != 0) return;
+  // ---- the token: each wave finds the tile for itself
   u64 total = 0;
   for (int t = lane; t < tiles; t += 64) total += s.tile[t];
   total = wave_sum(total);
@@ -934,62 +944,34 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
   int pick = -1;
   for (int t0 = 0; t0 < tiles && pick < 0; t0 += 64) {
     const u64 mine = t0 + lane < tiles ? s.tile[t0 + lane] : 0;
-    const u64 upto = wave_scan(mine, lane) + run;
+    const u64 upto = wave_scan(mine) + run;
     const u64 over = __ballot(upto > target);
-    const int f0 = over ? __ffsll(over) - 1 : 63;
+    const int f0 = __builtin_amdgcn_readfirstlane(over ? __ffsll(over) - 1 : 63);
     if (over) pick = t0 + f0;
-    run = __shfl(over ? upto - mine : upto, f0);
+    run = of_lane(over ? upto - mine : upto, f0);
   }
-  // and in it the token: 16 tokens in a row a lane
-  int token = -1;
-  float l = tot.M;
-  if (pick >= 0) {
-    const int base = pick * kSampleTile + lane * kVals;
-    float v[kVals];
-#pragma unroll
-    for (int j = 0; j < kVals; j += 4) {
-      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (base + j < V) f = *reinterpret_cast<const float4 *>(x + base + j);
-      v[j] = f.x;
-      v[j + 1] = f.y;
-      v[j + 2] = f.z;
-      v[j + 3] = f.w;
-    }
-#pragma unroll
-    for (int j = 0; j < kVals; ++j) v[j] = base + j < V && v[j] == v[j] ? v[j] : -INFINITY;
-    among_infinite(tot.infinite, v);
-    const uint32_t ck = s.cut_key;
-    const int ci = s.cut_index;
-    u64 wt[kVals], mine = 0;
-#pragma unroll
-    for (int j = 0; j < kVals; ++j) {
-      const uint32_t k = key_of(v[j]);
-      const bool in = v[j] > -INFINITY && (k > ck || (k == ck && base + j <= ci));
-      wt[j] = in ? kept_weight(v[j]) : 0;
-      mine += wt[j];
-    }
-    const u64 upto = wave_scan(mine, lane) + run;
-    const u64 over = __ballot(upto > target);
-    u64 at = upto - mine;
-    int first = -1;
-    float of = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kVals; ++j) {
-      at += wt[j];
-      if (first < 0 && at > target) {
-        first = base + j;
-        of = v[j];
-      }
-    }
-    if (over) {
-      token = __shfl(first, __ffsll(over) - 1);
-      l = __shfl(of, __ffsll(over) - 1);
-    }
+  if (pick < 0) {                          // (the largest logit is always kept: it does not happen)
+    if (tid == 0) a.token[row] = -1;
+    return;
   }
-  if (lane == 0) {
-    a.token[row] = token;
+  // and in it the token: one a thread
+  const int i = pick * kSampleTile + tid;
+  float l = i < V ? x[i] : -INFINITY;
+  l = l == l ? l : -INFINITY;
+  if (tot.infinite) l = l == INFINITY ? 0.0f : -INFINITY;
+  const uint32_t key = key_of(l), ck = s.cut_key;
+  const bool in = l > -INFINITY && (key > ck || (key == ck && i <= s.cut_index));
+  const u64 mine = in ? kept_weight(l) : 0;
+  const u64 upto = wave_scan(mine);
+  if (lane == 63) s.wmass[wave] = upto;
+  __syncthreads();
+  u64 earlier, all;
+  across_waves(s.wmass, wave, earlier, all);
+  const u64 end = run + earlier + upto;
+  if (end > target && end - mine <= target) {
+    a.token[row] = i;
     // (infinite logits stand at 0 here, and M does)
-    if (a.logprob) a.logprob[row] = (float)((double)l - (double)tot.M - log(s.exp_sum));
+    if (a.logprob) a.logprob[row] = (float)((double)l - (double)tot.M - s.log_sum);
   }
 }
 
@@ -1036,10 +1018,10 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
     s.bin_n = rc.bin_n;
   }
   if (a.logprob && wave == kWaves - 1) {
-    const double e = exp_sum_of(a, row, lane);
-    if (lane == 0) s.exp_sum = e;
+    const double e = log(exp_sum_of(a, row, lane));
+    if (lane == 0) s.log_sum = e;
   }
-  if (tid < n) s.cand[tid] = packed(c);
+  if (tid < n) s.cand[tid] = packed(c.l, c.i);
   if (tid < a.row_tiles) s.tile[tid] = tile;
   draw_row(s, a, r, tot, rc.total_w, rc.bin, again);
 }
@@ -1106,35 +1088,36 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
   }
 
   // the statistics
-  float top = -INFINITY;
-  int at = 0x7fffffff;
+  u64 best = 0;
   held.each([&](int t, const float (&v)[kVals]) {
+    float top = v[0];
+    int at = index_of(t, lane, 0);
 #pragma unroll
-    for (int j = 0; j < kVals; ++j)
+    for (int j = 1; j < kVals; ++j)
       if (v[j] > top) {
         top = v[j];
         at = index_of(t, lane, j);
       }
+    const u64 b = packed(top, at);
+    best = b > best ? b : best;
   });
-  largest(top, at);
-  if (lane == 0) {
-    s.wtop[wave] = top;
-    s.wat[wave] = at;
-  }
+  best = wave_largest(best);
+  if (lane == 0) s.wmass[wave] = best;
   __syncthreads();
-  top = s.wtop[lane & (kWaves - 1)];
-  at = s.wat[lane & (kWaves - 1)];
-  largest(top, at);
+  best = s.wmass[lane & (kWaves - 1)];
+  best = wave_largest(best);
+  const float top = of_key((uint32_t)(best >> 32));
   Total tot;
   tot.infinite = top == INFINITY;
   tot.none = top == -INFINITY;
   tot.M = tot.infinite ? 0.0f : top;
-  tot.at = at;
+  tot.at = (int)~(uint32_t)best;
   tot.mean = -1.0f;
   if (tot.none) {
     if (tid == 0) store_nothing(a, row);
     return;
   }
+  double exp_sum = 1.0;
   if (cut || a.logprob) {
     const float least = top - kFar * (r.greedy ? 1.0f : r.T);
     float e = 0.0f, sum = 0.0f;
@@ -1149,31 +1132,28 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
         e += v[j] == top ? 1.0f : __builtin_amdgcn_exp2f((v[j] - top) * 1.44269504088896f);
       }
     });
-    double de = e, ds = sum;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      de += __shfl_xor(de, o);
-      ds += __shfl_xor(ds, o);
-      n += __shfl_xor(n, o);
-    }
+    const double de = wave_sum((double)e), ds = wave_sum((double)sum);
+    n = wave_sum(n);
     if (lane == 0) {
       s.wexp[wave] = de;
       s.wsum[wave] = ds;
       s.wn[wave] = n;
     }
     __syncthreads();
-    de = ds = 0.0;
-    n = 0;
-    for (int i = 0; i < kWaves; ++i) {
-      de += s.wexp[i];
-      ds += s.wsum[i];
-      n += s.wn[i];
+    double before, e_all, sum_all;
+    uint32_t n_before;
+    across_waves(s.wexp, wave, before, e_all);
+    across_waves(s.wsum, wave, before, sum_all);
+    across_waves(s.wn, wave, n_before, n);
+    exp_sum = e_all;
+    if (a.logprob && !r.greedy && wave == kWaves - 1) {
+      const double l = log(e_all);
+      if (lane == 0) s.log_sum = l;
     }
-    if (tid == 0) s.exp_sum = de;
-    if (n && !tot.infinite) tot.mean = (float)(ds / (double)n);
+    if (n && !tot.infinite) tot.mean = (float)(sum_all / (double)n);
   }
   if (r.greedy) {
-    if (tid == 0) store_largest(a, row, tot, a.logprob ? s.exp_sum : 1.0);
+    if (tid == 0) store_largest(a, row, tot, exp_sum);
     return;
   }
   held.settle(tot.infinite);
@@ -1195,14 +1175,13 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
       add_to_steps(v, keep.w, step, r.by_p, s.count, s.mass, rest_n, rest_w);
     });
     rest_w = wave_sum(rest_w);
-    rest_n = (uint32_t)wave_sum(rest_n);
+    rest_n = wave_sum(rest_n);
     if (lane == 0 && rest_n) {
       atomicAdd(&s.count[kBins - 1], rest_n);
       atomicAdd(&s.mass[kBins - 1], rest_w);
     }
     __syncthreads();
-    total_w = total_mass(s);
-    find_bin(s, r.by_k ? (u64)r.k : ~0ull, r.by_p ? (double)r.p * (double)total_w : INFINITY);
+    total_w = find_bin(s, r.by_k ? (u64)r.k : ~0ull, [&](u64 all) { return r.by_p ? (double)r.p * (double)all : INFINITY; });
     bin = s.bin;
     again = bin < kBins && s.bin_n > kCand;
     if (!again)
@@ -1214,7 +1193,7 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
           if (b < bin) wt += keep(v[j]);
           if (b == bin && bin < kBins) {
             const int c = atomicAdd(&s.n_cand, 1);
-            if (c < kCand) s.cand[c] = packed(Candidate{v[j], index_of(t, lane, j)});
+            if (c < kCand) s.cand[c] = packed(v[j], index_of(t, lane, j));
           }
           __builtin_amdgcn_sched_barrier(0);
         }
