@@ -52,7 +52,7 @@ constexpr int kMaxTiles = kMaxVocab / kSampleTile;
 static_assert(kMaxTiles <= kThreads && kCand <= kThreads && kSampleTile == kThreads,
               "a thread takes a tile's sum, a candidate and a token of the drawn tile");
 constexpr int kVals = 16;                  // tokens of a tile a lane holds
-constexpr int kHeldTokens = 2 * kWaves * kSampleTile;   // of a row in a workgroup's registers
+constexpr int kHeldTokens = 4 * kWaves * kSampleTile;   // of a row in a workgroup's registers
 constexpr int kStatTiles = kSampleSlice / kSampleTile;   // one a wave
 
 typedef unsigned long long u64;
@@ -92,7 +92,10 @@ struct Weigher {
   int sh;
   const double *pow;                       // kPow, in LDS
 };
-__device__ __forceinline__ double weight_of(const Weigher &w, float l) {
+struct Scaled {                            // a weight is power * p
+  double power, p;
+};
+__device__ __forceinline__ Scaled scaled_weight(const Weigher &w, float l) {
   const double t = fmax(fma((double)l - w.M, w.c64, w.sh64), -1024.0);   // (-infinity: 2^-16)
   const double magic = 6755399441055744.0;                     // 1.5 * 2^52
   const double k = t + magic;
@@ -101,10 +104,15 @@ __device__ __forceinline__ double weight_of(const Weigher &w, float l) {
   // exp(r ln2 / 64): r ln2 / 64 below 0.0055, the first term left out 4e-14
   const double a = 0.010830424696249145, a2 = a * a;
   const double p = fma(r, fma(r, fma(r, fma(r, a2 * a2 / 24, a2 * a / 6), a2 / 2), a), 1.0);
-  return ldexp(w.pow[ki & 63] * p, ki >> 6);
+  return Scaled{ldexp(w.pow[ki & 63], ki >> 6), p};
 }
-__device__ __forceinline__ u64 whole(double x) {               // x <= 2^51, rounded
-  return (u64)__double_as_longlong(x + 4503599627370496.0) & 0xfffffffffffffull;
+// As a whole number (it is at most 2^51): the sum with 2^52, whose own bits stand above.
+__device__ __forceinline__ u64 weight_over(const Scaled &w) {
+  return (u64)__double_as_longlong(fma(w.power, w.p, 4503599627370496.0));
+}
+constexpr u64 kOver = 0x433ull << 52;      // the bits of 2^52
+__device__ __forceinline__ u64 weight_of(const Weigher &w, float l) {
+  return weight_over(scaled_weight(w, l)) - kOver;
 }
 
 __device__ __forceinline__ void load_tile(const float *__restrict__ x, int V, int tile, int lane,
@@ -292,8 +300,7 @@ __device__ __forceinline__ Weigher weigher_of(const SampleArgs &a, const Params 
   w.pow = pow;
   return w;
 }
-// A token's weight where min_p keeps it, else 0.  (MIN false: the row has no min_p; the
-// test, made for each token, would keep their chains of fp64 apart.)
+// A token's weight where min_p keeps it, else 0.
 struct Keep {
   Weigher w;
   float min_l;                             // below it: out without computing the weight
@@ -303,28 +310,32 @@ struct Keep {
     // (a margin over the roundings of the bound itself)
     min_l = r.min_p > 0.0 ? (float)(w.M + (double)r.T * (log(r.min_p) - 1e-3) - 1e-6 * fabs(w.M)) : -INFINITY;
   }
-  template <bool MIN>
-  __device__ __forceinline__ u64 of(float l) const {
-    const double d = weight_of(w, l);
-    return MIN && d < min_w ? 0 : whole(d);
+  __device__ __forceinline__ u64 operator()(float l) const {    // (no min_p: min_w is 0)
+    const Scaled d = scaled_weight(w, l);
+    return d.power * d.p < min_w ? 0 : weight_over(d) - kOver;
   }
-  __device__ __forceinline__ u64 operator()(float l) const { return of<true>(l); }   // (no min_p: min_w is 0)
 };
-
 // (four at a time: more of their chains at once take registers that no kernel here has)
-template <bool MIN>
 __device__ __forceinline__ u64 weight_of_tile(const Keep &keep, const float (&v)[kVals]) {
   u64 wt = 0;
-  if constexpr (MIN) {
+  if (keep.min_w > 0.0) {
     bool any = false;
 #pragma unroll
     for (int j = 0; j < kVals; ++j) any |= v[j] >= keep.min_l;
     if (!__any(any)) return 0;
-  }
 #pragma unroll
-  for (int j = 0; j < kVals; j += 4) {
-    wt += keep.of<MIN>(v[j]) + keep.of<MIN>(v[j + 1]) + keep.of<MIN>(v[j + 2]) + keep.of<MIN>(v[j + 3]);
-    __builtin_amdgcn_sched_barrier(0);
+    for (int j = 0; j < kVals; j += 4) {
+      wt += keep(v[j]) + keep(v[j + 1]) + keep(v[j + 2]) + keep(v[j + 3]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVals; j += 4) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) wt += weight_over(scaled_weight(keep.w, v[j + c]));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wt -= kVals * kOver;                   // (modulo 2^64)
   }
   return wave_sum(wt);
 }
@@ -382,6 +393,31 @@ __device__ u64 sorted(Lds &s, int n, int size) {
   if (tid < n) s.order[s.rank[tid]] = mine;
   __syncthreads();
   return tid < n ? s.order[tid] : 0;
+}
+
+// Of a tile the weight that stands before step `bin`; found(j) of its tokens in it.
+template <typename F>
+__device__ __forceinline__ u64 collect_tile(const Keep &keep, const Steps &step, int bin, const float (&v)[kVals],
+                                            F found) {
+  u64 wt = 0;
+#pragma unroll
+  for (int j = 0; j < kVals; j += 4) {
+    int b[4], least = kBins + 1;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      b[c] = v[j + c] > -INFINITY ? step(v[j + c]) : kBins + 1;
+      least = min(least, b[c]);
+    }
+    if (__any(least <= bin)) {             // (not a branch a token: their chains run side by side)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const u64 w = keep(v[j + c]);
+        wt += b[c] < bin ? w : 0;
+        if (b[c] == bin) found(j + c);
+      }
+    }
+  }
+  return wave_sum(wt);
 }
 
 // Of a number each wave has put into LDS: the sum over the waves before this one, and
@@ -449,38 +485,40 @@ __device__ void clear_bins(Lds &s) {
   }
 }
 
-// A tile's tokens into the steps; those of the last step into rest_n and rest_w.
-__device__ __forceinline__ void add_to_steps(const float (&v)[kVals], const Weigher &w, const Steps &step, bool by_p,
-                                             uint32_t *count, u64 *mass, uint32_t &rest_n, u64 &rest_w) {
-  if (by_p) {
+// A tile's tokens into the steps; those of the last step into rest_n and rest_w.  Counts
+// where top_k cuts, weights where top_p does.
+template <bool K, bool P>
+__device__ __forceinline__ void add_kind(const float (&v)[kVals], const Weigher &w, const Steps &step, uint32_t *count,
+                                         u64 *mass, uint32_t &rest_n, u64 &rest_w) {
 #pragma unroll
-    for (int j0 = 0; j0 < kVals; j0 += 4) {
-      u64 wt[4];
+  for (int j = 0; j < kVals; j += 4) {
+    u64 wt[4];
+    if constexpr (P) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wt[j] = whole(weight_of(w, v[j0 + j]));
+      for (int c = 0; c < 4; ++c) wt[c] = weight_of(w, v[j + c]);
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int b = step(v[j0 + j]);
-        if (b < kBins - 1) {
-          atomicAdd(&count[b], 1u);
-          atomicAdd(&mass[b], wt[j]);
-        } else {
-          rest_w += wt[j];                 // (0 of -infinity)
-          rest_n += v[j0 + j] > -INFINITY;
-        }
+    for (int c = 0; c < 4; ++c) {
+      const int b = step(v[j + c]);
+      if (b < kBins - 1) {
+        if constexpr (K) atomicAdd(&count[b], 1u);
+        if constexpr (P) atomicAdd(&mass[b], wt[c]);
+      } else {
+        if constexpr (K) rest_n += v[j + c] > -INFINITY;
+        if constexpr (P) rest_w += wt[c];  // (0 of -infinity)
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < kVals; ++j) {
-      const int b = step(v[j]);
-      if (b < kBins - 1)
-        atomicAdd(&count[b], 1u);
-      else
-        rest_n += v[j] > -INFINITY;
-    }
+    if constexpr (P) __builtin_amdgcn_sched_barrier(0);
   }
+}
+__device__ __forceinline__ void add_to_steps(const float (&v)[kVals], const Weigher &w, const Steps &step, bool by_k,
+                                             bool by_p, uint32_t *count, u64 *mass, uint32_t &rest_n, u64 &rest_w) {
+  if (!by_p)
+    add_kind<true, false>(v, w, step, count, mass, rest_n, rest_w);
+  else if (by_k)
+    add_kind<true, true>(v, w, step, count, mass, rest_n, rest_w);
+  else
+    add_kind<false, true>(v, w, step, count, mass, rest_n, rest_w);
 }
 
 // ---- stats ------------------------------------------------------------------------
@@ -593,12 +631,12 @@ __global__ void __launch_bounds__(kPassThreads, 4) sample_weights_kernel(const S
       if (keep.min_w > 0.0) {              // (few tiles hold any: the others are not read)
         if (top_of(a, tot, row, t) >= keep.min_l) {
           load_tile(x, a.V, t, lane, tot.infinite, v);
-          wt = weight_of_tile<true>(keep, v);
+          wt = weight_of_tile(keep, v);
         }
       } else {
         if (t >= lo + kPassWaves) load_tile(x, a.V, t, lane, v);
         among_infinite(tot.infinite, v);
-        wt = weight_of_tile<false>(keep, v);
+        wt = weight_of_tile(keep, v);
       }
       if (lane == 0) a.tiles[(size_t)row * a.row_tiles + t] = wt;
     }
@@ -610,18 +648,18 @@ __global__ void __launch_bounds__(kPassThreads, 4) sample_weights_kernel(const S
   for (; t < hi; t += kPassWaves) {
     if (t >= lo + kPassWaves) load_tile(x, a.V, t, lane, v);
     among_infinite(tot.infinite, v);
-    add_to_steps(v, keep.w, step, r.by_p, count, mass, rest_n, rest_w);
+    add_to_steps(v, keep.w, step, r.by_k, r.by_p, count, mass, rest_n, rest_w);
   }
   rest_w = wave_sum(rest_w);
   rest_n = wave_sum(rest_n);
-  if (lane == 0 && rest_n) {
+  if (lane == 0) {
     atomicAdd(&count[kBins - 1], rest_n);
     atomicAdd(&mass[kBins - 1], rest_w);
   }
   __syncthreads();
   const size_t at = ((size_t)row * a.parts + blockIdx.x) * kBins;
   for (int i = tid; i < kBins; i += kPassThreads) {
-    a.counts[at + i] = count[i];
+    if (r.by_k) a.counts[at + i] = count[i];
     if (r.by_p) a.masses[at + i] = mass[i];
   }
 }
@@ -643,14 +681,19 @@ __global__ void __launch_bounds__(kThreads) sample_cut_kernel(const SampleArgs a
   if (!(r.by_k || r.by_p)) return;
   u64 w0 = 0, w1 = 0;
   uint32_t n0 = 0, n1 = 0;
+  const size_t at = (size_t)row * a.parts * kBins + 2 * tid;
+  if (r.by_k) {                            // (two loops: a branch within one would part its loads)
 #pragma unroll 8
-  for (int p = 0; p < a.parts; ++p) {
-    const size_t at = ((size_t)row * a.parts + p) * kBins + 2 * tid;
-    const uint2 n = *reinterpret_cast<const uint2 *>(a.counts + at);
-    n0 += n.x;
-    n1 += n.y;
-    if (r.by_p) {
-      const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(a.masses + at);
+    for (int p = 0; p < a.parts; ++p) {
+      const uint2 n = *reinterpret_cast<const uint2 *>(a.counts + at + (size_t)p * kBins);
+      n0 += n.x;
+      n1 += n.y;
+    }
+  }
+  if (r.by_p) {
+#pragma unroll 8
+    for (int p = 0; p < a.parts; ++p) {
+      const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(a.masses + at + (size_t)p * kBins);
       w0 += m.x;
       w1 += m.y;
     }
@@ -703,24 +746,18 @@ __global__ void __launch_bounds__(kPassThreads) sample_collect_kernel(const Samp
     if (step(top_of(a, tot, row, t)) <= bin) {   // (a tile that holds none of the first is not read)
       float v[kVals];
       load_tile(x, a.V, t, lane, tot.infinite, v);
-#pragma unroll
-      for (int j = 0; j < kVals; ++j) {
-        const int b = step(v[j]);
-        if (b < bin && v[j] > -INFINITY) wt += keep(v[j]);
-        if (b == bin && v[j] > -INFINITY) {
-          const int c = atomicAdd(&n_found, 1);
-          if (c < kCand) found[c] = Candidate{v[j], index_of(t, lane, j)};
-        }
-      }
-      wt = wave_sum(wt);
+      wt = collect_tile(keep, step, bin, v, [&](int j) {
+        const int c = atomicAdd(&n_found, 1);
+        if (c < kCand) found[c] = Candidate{v[j], index_of(t, lane, j)};
+      });
     }
     if (lane == 0) a.tiles[(size_t)row * a.row_tiles + t] = wt;
   }
   __syncthreads();
-  // (a row's candidates are at most kCand in all)
+  // (past kCand in all, which only a row without top_k can hold, the draw finds them itself)
   if (tid == 0) place = n_found ? atomicAdd(&a.cuts[row].n_cand, (unsigned)n_found) : 0;
   __syncthreads();
-  for (int c = tid; c < n_found; c += kPassThreads)
+  for (int c = tid; c < min(n_found, kCand); c += kPassThreads)
     if (place + c < kCand) a.cands[(size_t)row * kCand + place + c] = found[c];
 }
 
@@ -806,7 +843,7 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
           if (k < klo || k > khi || v[j] == -INFINITY) continue;
           const uint32_t b = (khi - k) >> shift;
           atomicAdd(&s.count[b], 1u);
-          if (by_p) atomicAdd(&s.mass[b], whole(weight_of(w, v[j])));
+          if (by_p) atomicAdd(&s.mass[b], weight_of(w, v[j]));
         }
       });
       __syncthreads();
@@ -859,7 +896,7 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
       const float l = of_key((uint32_t)(e >> 32));
       const int i = (int)~(uint32_t)e;
       const bool live = tid < n;
-      const u64 mine = live ? whole(weight_of(w, l)) : 0;
+      const u64 mine = live ? weight_of(w, l) : 0;
       u64 mass = wave_scan(mine);
       if (lane == 63) s.wmass[wave] = mass;
       __syncthreads();
@@ -867,7 +904,7 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
       across_waves(s.wmass, wave, earlier, all);
       mass += s.before_w - mine + earlier;
       const u64 rank = s.before_n + tid;
-      const bool keep = live && rank < want_n && (rank == 0 || (double)mass < want_w);
+      const bool keep = live && rank < want_n && (mass == 0 || (double)mass < want_w);
       if (keep) {
         const u64 kw = kept_weight(l);
         if (kw) atomicAdd(&s.tile[i / kSampleTile], kw);
@@ -882,7 +919,7 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
     } else if (cuts && equal) {
       // of equal logits the first `take` by index
       if (tid == 0) {
-        const u64 each = whole(weight_of(w, of_key(kequal)));
+        const u64 each = weight_of(w, of_key(kequal));
         u64 take = 0;
         if (by_k) take = want_n - s.before_n;
         if (by_p) {
@@ -893,7 +930,7 @@ __device__ __forceinline__ void draw_row(Lds &s, const SampleArgs &a, const Para
           while (each && tp < (u64)V && (double)(s.before_w + tp * each) < want_w) ++tp;
           take = by_k ? (take < tp ? take : tp) : tp;
         }
-        if (take == 0 && s.before_n == 0) take = 1;
+        if (take == 0 && s.before_w == 0) take = 1;
         const u64 kw = kept_weight(of_key(kequal));
         u64 left = take;
         int edge = -1;
@@ -1009,13 +1046,14 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
   }
   if (tid < 64) s.pow[tid] = kPow[tid];
   const bool cut = r.by_k || r.by_p;
-  const bool again = cut && rc.bin_n > kCand;
-  const int n = again || !cut ? 0 : min((int)rc.n_cand, kCand);
+  const unsigned bin_n = max(rc.bin_n, rc.n_cand);   // (without top_k only the latter is counted)
+  const bool again = cut && bin_n > kCand;
+  const int n = again || !cut ? 0 : (int)rc.n_cand;
   if (tid == 0) {
     s.n_cand = n;
     s.before_n = rc.before_n;
     s.before_w = rc.before_w;
-    s.bin_n = rc.bin_n;
+    s.bin_n = bin_n;
   }
   if (a.logprob && wave == kWaves - 1) {
     const double e = log(exp_sum_of(a, row, lane));
@@ -1027,9 +1065,8 @@ __global__ void __launch_bounds__(kThreads) sample_draw_kernel(const SampleArgs 
 }
 
 // ---- a row's five passes in one workgroup ------------------------------------------------
-// A wave's tiles: held in registers, or (TW 0) read by each pass.
 template <int TW>
-struct RowTiles {
+struct RowTiles {                          // a wave's tiles, in registers
   int tiles, wave;
   float v[TW][kVals];
   __device__ __forceinline__ RowTiles(const float *x, int V, int wave_, int lane)
@@ -1046,27 +1083,6 @@ struct RowTiles {
 #pragma unroll
     for (int i = 0; i < TW; ++i)
       if (wave + i * kWaves < tiles) f(wave + i * kWaves, v[i]);
-  }
-};
-template <>
-struct RowTiles<0> {
-  const float *x;
-  int V, tiles, wave, lane;
-  bool infinite;
-  __device__ __forceinline__ RowTiles(const float *x_, int V_, int wave_, int lane_)
-      : x(x_), V(V_), tiles((V_ + kSampleTile - 1) / kSampleTile), wave(wave_), lane(lane_), infinite(false) {}
-  __device__ __forceinline__ void settle(bool inf) { infinite = inf; }
-  template <typename F>
-  __device__ __forceinline__ void each(F f) {
-    float v[kVals], next[kVals];
-    load_tile(x, V, wave, lane, v);
-    for (int t = wave; t < tiles; t += kWaves) {
-      if (t + kWaves < tiles) load_tile(x, V, t + kWaves, lane, next);
-      among_infinite(infinite, v);
-      f(t, v);
-#pragma unroll
-      for (int j = 0; j < kVals; ++j) v[j] = next[j];
-    }
   }
 };
 
@@ -1165,18 +1181,18 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
   bool again = false;
   if (!cut) {
     held.each([&](int t, const float (&v)[kVals]) {
-      const u64 wt = keep.min_w > 0.0 ? weight_of_tile<true>(keep, v) : weight_of_tile<false>(keep, v);
+      const u64 wt = weight_of_tile(keep, v);
       if (lane == 0) s.tile[t] = wt;
     });
   } else {
     uint32_t rest_n = 0;
     u64 rest_w = 0;
     held.each([&](int, const float (&v)[kVals]) {
-      add_to_steps(v, keep.w, step, r.by_p, s.count, s.mass, rest_n, rest_w);
+      add_to_steps(v, keep.w, step, r.by_k, r.by_p, s.count, s.mass, rest_n, rest_w);
     });
     rest_w = wave_sum(rest_w);
     rest_n = wave_sum(rest_n);
-    if (lane == 0 && rest_n) {
+    if (lane == 0) {
       atomicAdd(&s.count[kBins - 1], rest_n);
       atomicAdd(&s.mass[kBins - 1], rest_w);
     }
@@ -1184,22 +1200,24 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
     total_w = find_bin(s, r.by_k ? (u64)r.k : ~0ull, [&](u64 all) { return r.by_p ? (double)r.p * (double)all : INFINITY; });
     bin = s.bin;
     again = bin < kBins && s.bin_n > kCand;
-    if (!again)
+    if (!again) {
       held.each([&](int t, const float (&v)[kVals]) {
-        u64 wt = 0;
-#pragma unroll
-        for (int j = 0; j < kVals; ++j) {
-          const int b = v[j] > -INFINITY ? step(v[j]) : kBins;
-          if (b < bin) wt += keep(v[j]);
-          if (b == bin && bin < kBins) {
-            const int c = atomicAdd(&s.n_cand, 1);
-            if (c < kCand) s.cand[c] = packed(v[j], index_of(t, lane, j));
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        wt = wave_sum(wt);
+        const u64 wt = collect_tile(keep, step, bin, v, [&](int j) {
+          const int c = atomicAdd(&s.n_cand, 1);
+          if (c < kCand) s.cand[c] = packed(v[j], index_of(t, lane, j));
+        });
         if (lane == 0) s.tile[t] = wt;
       });
+      if (!r.by_k) {                       // (their counts are not in the histogram)
+        __syncthreads();
+        again = s.n_cand > kCand;
+        __syncthreads();
+        if (again && tid == 0) {
+          s.bin_n = s.n_cand;
+          s.n_cand = 0;
+        }
+      }
+    }
   }
   draw_row(s, a, r, tot, total_w, bin, again);
 }
@@ -1220,16 +1238,14 @@ hipError_t launch_slices(const SampleArgs &a, hipStream_t stream) {
 
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {
   (void)hipGetLastError();
-  // One launch, a workgroup a row, where a row's tiles fit a workgroup's registers, and
-  // with rows for a third of the CUs up to twice that; else slices (us, mixed kinds of
-  // rows: 1 x 32000 26 against 34; 256 x 50001 58 against 76; 40 x 50001 51 against 45;
-  // 128 x 80000 83 against 72; 256 x 131072 137 against 121)
-  if (a.V <= kHeldTokens / 2)
+  // One launch, a workgroup a row, where a row's tiles fit a workgroup's registers; from
+  // half of them on only with rows for a third of the CUs
+  if (a.V <= kHeldTokens / 4)
     sample_row_kernel<1><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
-  else if (a.V <= kHeldTokens)
+  else if (a.V <= kHeldTokens / 2)
     sample_row_kernel<2><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
-  else if (a.V <= 2 * kHeldTokens && a.m >= 96)
-    sample_row_kernel<0><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
+  else if (a.V <= kHeldTokens && a.m >= 96)
+    sample_row_kernel<4><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
   else
     return launch_slices(a, stream);
   return hipGetLastError();
