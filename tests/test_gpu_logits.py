@@ -232,6 +232,73 @@ def test_draw_over_masked_rows(limits):
     assert token[5] in (17, 2999)
 
 
+# rows of two tiles a wave in one workgroup, rows in slices, and four tiles a wave (from 96 rows)
+LONG = [(6, 20001), (6, 40001), (97, 33333), (3, 131073)]
+
+
+@pytest.mark.parametrize("limits", LIMITS)
+@pytest.mark.parametrize("m,v", LONG)
+def test_draw_of_long_rows(m, v, limits):
+    r = np.random.default_rng([41, v])
+    x = (r.standard_normal((m, v)) * r.choice([0.3, 1, 3, 10], (m, 1))).astype(np.float32)
+    check_draw(x, r.random(m), **limits)
+
+
+@pytest.mark.parametrize("kind", ["equal", "two", "narrow", "steps", "wide", "outlier", "ties"])
+@pytest.mark.parametrize("limits", LIMITS[4:6] + LIMITS[8:11] + [dict(top_k=3000), dict(top_k=15000, top_p=0.7)])
+@pytest.mark.parametrize("m,v", LONG[:3])
+def test_draw_of_crowded_long_rows(m, v, kind, limits):
+    """More tokens in the step of the cut than are ordered at once, counted (top_k) or not (top_p)."""
+    r = np.random.default_rng([43, v])
+    m = min(m, 4) if m < 96 else m
+    n = r.standard_normal((4, v))
+    x = {"equal": np.full((4, v), 1.5), "two": np.where(n > 1.0, 2.0, 1.0), "narrow": 7 + n * 1e-6,
+         "steps": np.round(n * 2), "wide": n * 1000, "outlier": np.where(np.arange(v) == 77, 1e30, n),
+         "ties": np.round(n * 40) / 40}[kind].astype(np.float32)
+    # (of 97 rows the oracle looks at these four, and the last)
+    rows, u = x[np.arange(m) % 4], r.random(m)
+    token, lp = draw(rows, u, **limits)
+    for i in (0, 1, 2, 3, m - 1):
+        one = {k: (int(a) if k == "top_k" else float(a)) for k, a in limits.items()}
+        assert int(token[i]) in ol.sample(rows[i], float(u[i]), **one), (i, limits, float(u[i]), int(token[i]))
+    again, lp2 = draw(rows, u, **limits)
+    np.testing.assert_array_equal(token, again)
+    np.testing.assert_array_equal(lp, lp2)
+
+
+@pytest.mark.parametrize("limits", [LIMITS[i] for i in (0, 1, 4, 5, 8)])
+@pytest.mark.parametrize("m,v", LONG[:3])
+def test_draw_over_masked_long_rows(m, v, limits):
+    r = np.random.default_rng([47, v])
+    m = max(m, 9)
+    x = (r.standard_normal((m, v)) * 3).astype(np.float32)
+    x[0] = -INF
+    x[1] = np.nan
+    x[2] = -INF
+    x[2, 2048] = -3e38
+    x[3, r.random(v) < 0.999] = -INF
+    x[4, r.random(v) < 0.5] = np.nan
+    x[5, 17] = x[5, v - 2] = INF
+    x[6] = np.finfo(np.float32).min
+    x[7] = INF
+    x[8, :] = -INF
+    x[8, -1] = 4.0
+    token = check_draw(x, r.random(m), **limits)
+    assert token[0] == token[1] == -1 and token[2] == 2048 and token[8] == v - 1
+    assert token[5] in (17, v - 2)
+
+
+@pytest.mark.parametrize("v", [20001, 40001])
+def test_a_row_is_drawn_alike_alone_and_in_a_batch(v):
+    r = np.random.default_rng([53, v])
+    x = (r.standard_normal((100, v)) * 3).astype(np.float32)
+    u = r.random(100)
+    for limits in ({}, dict(top_p=0.9), dict(top_k=40, top_p=0.95, min_p=0.01)):
+        token, _ = draw(x, u, **limits)
+        for i in (0, 57, 99):
+            assert draw(x[i:i + 1], u[i:i + 1], **limits)[0][0] == token[i]
+
+
 def test_draw_at_the_ends_of_u():
     x = np.zeros((6, 40), np.float32)
     x[:, :8] = -INF
