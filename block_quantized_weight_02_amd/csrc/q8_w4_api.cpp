@@ -158,22 +158,23 @@ int run_tile(W4Args &a, int act_fmt, bool pair, int splits, int64_t m, hipStream
 }
 
 // Many rows: the GEMM, whose workgroups own 128 rows by 256 columns (the pair 128), or
-// the tile kernel in chunks of 64 rows, one workgroup a tile and chunk.  The tile kernel
-// takes one step of its time for each 256 workgroups, the GEMM one of its (three to four
-// times longer) for each 256.  Measured on MI355X (us, tile kernel against GEMM), bf16,
-// K = 4096: 224 workgroups of the tile kernel (m = 64, N = 14336) 25 against 72, 448
-// (m = 128) 46 against 74, 672 (m = 192) 66 against 75, 896 (m = 256) 87 against 75; m =
-// 512, N = 4096 (512) 46 against 74; K = 5120, N = 32000, m = 128 (1000) 105 against 93.
-// Q8_0, groups of 32: m = 512, N = 4096 (512) 66 against 137, m = 256, N = 14336 (896) 126
-// against 138.  The pair: bf16 m = 64, 128, N = 14336 (224, 448) 40, 77 against 81, 83;
-// Q8_0 m = 128, N = 4096 (128) 60 against 145, m = 200, N = 14336 (896) 231 against 147.
-bool gemm_route(int64_t m, int64_t N, int act_fmt, bool pair) {
-  const int64_t workgroups = (m + 63) / 64 * (round_up(N, Q8_TILE_COLS) / Q8_TILE_COLS);
-  return m > 64 && workgroups > (pair ? 512 : act_fmt == Q8_ACT_BF16 ? 768 : 1024);
+// the tile kernel in chunks of 64 rows (the pair 32), one workgroup a tile and chunk.  The
+// tile kernel takes one step of its time for each 256 workgroups, the GEMM one of its
+// (four to five times longer) for each 256.  Measured on MI355X (us, tile kernel against
+// GEMM, by workgroups of the former), K = 4096, groups of 128: bf16 224 19 against 65, 448
+// 34 against 67, 896 65 against 68, 1024 65 against 69, 1120 81 against 69; the pair 448
+// 36 against 73, 896 70 against 76, 1024 66 against 76, 1120 87 against 76.  With Q8_0 or
+// groups of 32, whose GEMM scales more: 1120 bf16, groups of 32, 87 against 103; Q8_0 105
+// against 109, groups of 32 118 against 127 (the pair 114 against 136); 1344 Q8_0 125
+// against 109, the pair 137 against 136.
+bool gemm_route(const W4Args &a, int act_fmt, bool pair) {
+  const int chunk = pair ? 32 : 64;
+  const int64_t workgroups = (int64_t)((a.m + chunk - 1) / chunk) * a.T;
+  return a.m > 64 && workgroups > (act_fmt == Q8_ACT_Q8_0 || a.group == 32 ? 1280 : 1024);
 }
 
 int run_many(W4Args &a, int act_fmt, bool pair, hipStream_t stream) {
-  if (!gemm_route(a.m, a.ep.N, act_fmt, pair)) return run_tile(a, act_fmt, pair, 1, a.m, stream, nullptr, 0);
+  if (!gemm_route(a, act_fmt, pair)) return run_tile(a, act_fmt, pair, 1, a.m, stream, nullptr, 0);
   return done(launch_w4_gemm(act_fmt, pair, a, stream), "4-bit product launch");
 }
 

@@ -113,6 +113,42 @@ def test_random_many_rows(m, K, N, group, zeros, fmt, act):
     assert torch.equal(first, u.gemm(a, w)), "two calls differ"
 
 
+# Sizes with more than 1280 tiles of 64 x 64 (the pair's of 32 x 64): the blocks of 128 rows.
+@pytest.mark.parametrize("act", [BF16, Q8])
+@pytest.mark.parametrize("group,zeros,fmt", FORMS)
+@pytest.mark.parametrize("m,K,N", [(1025, 32, 5129), (1087, 416, 5000), (4100, 96, 1300)])
+def test_exact_blocks(m, K, N, group, zeros, fmt, act):
+    w = Weight(K, N, group, zeros, fmt, 5, exact=True).pack()
+    a = Act(m, K, act, 9, exact=True)
+    np.testing.assert_array_equal(u.real(u.gemm(a, w), N), a.times(w)[0])
+
+
+@pytest.mark.parametrize("act", [BF16, Q8])
+@pytest.mark.parametrize("m,K,N,group,zeros,fmt", [
+    (1100, 1056, 4993, 64, True, 0), (1030, 2048, 5100, 128, False, 1), (1281, 544, 4100, 32, True, 1),
+    (2000, 1184, 2700, 32, False, 0)])
+def test_random_blocks(m, K, N, group, zeros, fmt, act):
+    w = Weight(K, N, group, zeros, fmt, 17).pack()
+    a = Act(m, K, act, 19)
+    first = u.gemm(a, w)
+    u.compare(u.real(first, N), a.times(w), (m, K, N, group, zeros))
+    assert torch.equal(first, u.gemm(a, w)), "two calls differ"
+
+
+def test_a_row_of_infinities_stays_in_its_row_of_a_block():
+    m, K, N = 1025, 96, 5129
+    w = Weight(K, N, 128, False, 0, 31, exact=True).pack()
+    a = Act(m, K, BF16, 37, exact=True)
+    want = a.times(w)[0]
+    bad = [1, 127, 512, m - 1]
+    for r in bad:
+        a.dev[r] = 0x7F80                          # infinity
+    got = u.gemm(a, w).cpu().numpy()[:, :N]
+    assert not np.isfinite(got[bad]).any()
+    good = np.setdiff1d(np.arange(m), bad)
+    np.testing.assert_array_equal(got[good].astype(np.float64), want[good])
+
+
 @pytest.mark.parametrize("act", [BF16, Q8])
 @pytest.mark.parametrize("m", [2, 16, 40])
 def test_zero_points_of_a_whole_byte(m, act):
@@ -184,7 +220,9 @@ def pair_tolerance(gate, up, bg, bu):
 PAIRS = [(1, 32, 1, 32, False, 0), (1, 4096, 1000, 64, False, 0), (4, 1056, 130, 128, True, 1),
          (16, 2048, 9000, 32, True, 0), (29, 1024, 200, 64, True, 1), (32, 512, 64, 128, False, 0),
          (7, 1024, 300, 32, True, 1), (8, 512, 5000, 128, False, 0), (23, 2048, 130, 32, False, 0),
-         (24, 544, 9000, 64, True, 0), (40, 512, 300, 32, False, 1), (128, 1024, 200, 128, True, 0), (257, 288, 520, 64, False, 0)]
+         (24, 544, 9000, 64, True, 0), (40, 512, 300, 32, False, 1), (128, 1024, 200, 128, True, 0),
+         (257, 288, 520, 64, False, 0), (600, 544, 4470, 128, True, 0), (1030, 160, 2600, 64, False, 1),
+         (641, 288, 4200, 32, True, 1)]
 
 
 @pytest.mark.parametrize("act", [BF16, Q8])
