@@ -33,10 +33,10 @@
 // They are five launches with the rows' vocabularies in slices, so that few long rows too
 // are worked on by many CUs, or one launch with a workgroup a row, where a row is short
 // enough for its registers (launch_sample has both sides' figures).  Mixed kinds of rows:
-// 1 x 32000 24 us, 40 x 50001 45, 256 x 131072 121 (greedy alone 38, top_k 100, top_p
-// 150).  The first pass of those 256 rows, 25 us, is bound by their 134 MB; the second,
-// 41, by fp64 and by additions in LDS; the collecting one, 29, by fp64; the two with a
-// workgroup a row (8 and 17), and all of them with few rows, by latency.
+// 1 x 32000 17 us, 40 x 50001 36, 256 x 131072 105.  The first pass of those 256 rows, 24
+// us, is bound by their 134 MB; the second, 40, by fp64, by additions in LDS and by the
+// rows' unlike work; the collecting one, 28, by fp64 and the same; the two with a
+// workgroup a row (6 and 13), and all of them with few rows, by latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -1241,7 +1241,10 @@ hipError_t launch_slices(const SampleArgs &a, hipStream_t stream) {
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {
   (void)hipGetLastError();
   // One launch, a workgroup a row, where a row's tiles fit a workgroup's registers; from
-  // half of them on only with rows for a third of the CUs
+  // half of them on only with rows for a third of the CUs (us, mean of the kinds of rows,
+  // one launch against slices: 1 x 1000 11 against 23, 1 x 32000 20 against 25, 256 x 32000
+  // 25 against 46, 128 x 65000 38 against 46, 256 x 65000 43 against 61; but 1 x 50001 28
+  // against 27, 8 x 50001 mixed 42 against 33, 64 x 65000 mixed 57 against 49)
   if (a.V <= kHeldTokens / 4)
     sample_row_kernel<1><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
   else if (a.V <= kHeldTokens / 2)
