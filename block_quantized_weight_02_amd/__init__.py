@@ -1,6 +1,8 @@
 """MI355X (gfx950) Q8_0 weight product: y = x . W over int8 values with one
 fp32 scale per 32 rows of each column, for 1..32 activation rows (bf16 or
-their per-32-block int8 form), the weight streamed once for all rows.
+their per-32-block int8 form), the weight streamed once for all rows; the same
+over 4-bit weights with group scales; what a layer runs between its products;
+and the way from logits to tokens.
 
 The compute is the HIP library ``libq8gemv.so`` (C ABI: include/q8gemv.h);
 ``binding`` exposes it to Python under the same names.  ``inputs`` draws the

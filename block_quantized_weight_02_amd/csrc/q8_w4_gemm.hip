@@ -17,6 +17,12 @@
 //   * workgroups are numbered so that each XCD walks a contiguous range of (column
 //     block, row block) with the row block fastest: the row blocks that read one
 //     weight tile run together, and its L2 serves the tile to all of them.
+//
+// Measured: 2048 rows, K = 4096, N = 14336, groups of 128, 215..225 us (1070..1120
+// TFLOP/s; the large bf16 library product reaches 1325, 181 us); 8192 rows 854 (1127).  The
+// matrix unit is busy 47 % of the time, the vector unit 65 %, and the LDS reads of the
+// activation's operands (128 rows for 64 columns a wave) hold both up: without them 159 us.
+// More columns a wave would halve them, but their sums do not fit the registers.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

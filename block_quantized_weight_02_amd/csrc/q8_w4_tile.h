@@ -28,6 +28,13 @@
 // activation's rows (and Q8_0 scales) loaded straight into two places in LDS of the
 // wave's own, so that the registers hold weight alone and no wave waits for another.
 // The waves' carries meet in LDS, the splits' through finish_tile.
+//
+// Measured, calls back to back: m = 1, K = 4096, N = 14336 8.1 us, N = 32000 13.5 (68 MB,
+// 5.0 TB/s); m = 16, N = 14336, zero points 9.5 (31 MB; a plain read 4.9): the launch, the
+// first loads' latency and the join stand beside the stream.  Q8_0, groups of 32, m = 32, K
+// = 5120, N = 32001 31 (92 MB; a plain read 14): the vector unit, busy 60 % (three
+// instructions a result and block, conversion and two scales; with zero points four), the
+// matrix unit 15 %, beside the activation's loads through L2.
 #pragma once
 
 #include <hip/hip_runtime.h>
