@@ -88,16 +88,18 @@ logit_rules_kernel(const LogitRulesArgs a, int slice) {
       uint32_t *cnt = reinterpret_cast<uint32_t *>(count);
       const int prompt = u.prompt_lens ? u.prompt_lens[r] : 0;
       const int32_t *tok = u.tokens + (size_t)r * u.ld_tokens;
-      for (int j0 = tid; j0 < held; j0 += kAhead * kThreads) {
+      // (unsigned: a row may hold up to 2^31 - 1 tokens)
+      const unsigned end = (unsigned)held;
+      for (unsigned j0 = tid; j0 < end; j0 += kAhead * kThreads) {
         int t[kAhead];
 #pragma unroll
-        for (int c = 0; c < kAhead; ++c) t[c] = tok[min(j0 + c * kThreads, held - 1)];
+        for (int c = 0; c < kAhead; ++c) t[c] = tok[min(j0 + c * kThreads, end - 1)];
 #pragma unroll
         for (int c = 0; c < kAhead; ++c) {
-          const int j = j0 + c * kThreads;
+          const unsigned j = j0 + c * kThreads;
           const int64_t at = (int64_t)t[c] - base;
-          if (j < held && at >= 0 && at < n) {
-            if (j >= prompt)
+          if (j < end && at >= 0 && at < n) {
+            if ((int)j >= prompt)
               atomicAdd(&cnt[at], 1u);
             else
               atomicOr(&cnt[at], kPrompt);
@@ -106,9 +108,9 @@ logit_rules_kernel(const LogitRulesArgs a, int slice) {
       }
     }
     if constexpr (BIASED) {
-      for (int j = bias_lo + tid; j < bias_hi; j += kThreads) {
+      for (unsigned j = (unsigned)bias_lo + tid; j < (unsigned)bias_hi; j += kThreads) {
         const int64_t at = (int64_t)u.bias_token[j] - base;
-        if (at >= 0 && at < n) atomicMax(reinterpret_cast<int *>(last) + at, j);
+        if (at >= 0 && at < n) atomicMax(reinterpret_cast<int *>(last) + at, (int)j);
       }
     }
     __syncthreads();

@@ -117,6 +117,18 @@ def test_rules_of_a_long_history():
     check_rules(s, x, s.device())
 
 
+def test_rules_of_the_longest_history():
+    """2^31 - 1 tokens, of which the first and the last few count."""
+    n, v = 2 ** 31 - 1, 8
+    tokens = torch.full((1, n), -1, dtype=torch.int32, device=g.DEV)
+    tokens[0, 0], tokens[0, n - 3:] = 2, torch.tensor([5, 5, 7], dtype=torch.int32, device=g.DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=g.DEV)
+    freq = torch.ones(1, device=g.DEV)
+    x = torch.zeros((1, 64), device=g.DEV)
+    q8.q8_logits_rules(x, 64, 1, v, q8.make_logit_rules(tokens=tokens, ld_tokens=n, lens=lens, frequency=freq), x, 64)
+    assert x[0, :v].tolist() == [0, 0, -1, 0, 0, -2, 0, -1]
+
+
 def test_rules_bounds():
     """Lengths outside the row, tokens outside the vocabulary, biases past the entries, prompt lengths
     past the history, and a width of no multiple of four."""
@@ -349,6 +361,41 @@ def test_draw_without_logprob():
     u = r.random(3)
     for limits in ({}, dict(temperature=0.0), dict(top_k=5)):
         np.testing.assert_array_equal(draw(x, u, logprob=False, **limits)[0], draw(x, u, **limits)[0])
+
+
+@pytest.mark.parametrize("m,v", [(5, 20001), (5, 40001), (97, 33333)])
+def test_draws_captured_and_on_two_streams(m, v):
+    """Replays over new logits and numbers, and two calls at once, each with a workspace of its own."""
+    r = np.random.default_rng([59, v])
+    ld = ld_of(v)
+    x = [torch.zeros((m, ld), device=g.DEV) for _ in range(2)]
+    u = [torch.zeros(m, dtype=torch.float64, device=g.DEV) for _ in range(2)]
+    top_p, top_k = torch.full((m,), 0.9, device=g.DEV), torch.full((m,), 40, dtype=torch.int32, device=g.DEV)
+    top_k[::2] = 0
+    need = q8.q8_sample_workspace_bytes(m, v)
+    ws = [torch.empty(need, dtype=torch.uint8, device=g.DEV).fill_(0xA5) for _ in range(2)]
+    out = [(torch.zeros(m, dtype=torch.int32, device=g.DEV), torch.zeros(m, device=g.DEV)) for _ in range(2)]
+    sampling = [q8.make_sampling(n, top_p=top_p, top_k=top_k) for n in u]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side[0]):
+        q8.q8_sample(x[0], ld, m, v, sampling[0], *out[0], None, ws[0], need)
+    for _ in range(4):
+        rows = [(r.standard_normal((m, v)) * 3).astype(np.float32) for _ in range(2)]
+        nums = [r.random(m) for _ in range(2)]
+        for k in range(2):
+            x[k][:, :v].copy_(torch.from_numpy(rows[k]))
+            u[k].copy_(torch.from_numpy(nums[k]))
+        want = [draw(rows[k], nums[k], top_p=0.9, top_k=top_k.cpu().numpy()) for k in range(2)]
+        with torch.cuda.stream(side[0]):
+            graph.replay()
+        with torch.cuda.stream(side[1]):
+            q8.q8_sample(x[1], ld, m, v, sampling[1], *out[1], None, ws[1], need)
+        torch.cuda.synchronize()
+        for k in range(2):
+            np.testing.assert_array_equal(out[k][0].cpu().numpy(), want[k][0])
+            np.testing.assert_array_equal(out[k][1].cpu().numpy(), want[k][1])
 
 
 # ---- together ------------------------------------------------------------------------
