@@ -513,7 +513,8 @@ int q8_w4_unpack(const q8_w4_weight *W /* host pointer */, uint8_t *u_kn, uint16
  * The sums are fp32: bf16 activations are multiplied exactly and added in fp32, a
  * group's sum is scaled once; Q8_0 activations' dots are exact int32 per 32 rows.
  * An infinity or NaN in a row of a bf16 activation makes that row's outputs NaN or
- * infinite, no other row's.
+ * infinite, no other row's; so may a value above 2^112 in size, since a group's sum may
+ * be taken of (16 + u) x and (16 + z) x.
  *
  * The workspace is the caller's, as in q8_gemv_ws: q8_w4_gemv_workspace_bytes(...)
  * bytes, 16-byte aligned, NULL when that is 0; its first 4 MiB are counters, zero at
@@ -831,11 +832,12 @@ int q8_attn_rows(const uint16_t *q, int64_t m, int64_t q_heads,
  *     whose token is t;
  *   - mask: -infinity where bit t % 32 of word t / 32 of mask row mask_row[r] is 0
  *     (a row of -1, or any outside 0 .. mask_rows - 1: no mask).
- * In fp32 (a value past its range becomes infinite).  A row's tokens are tokens[r * ld_tokens + 0 .. lens[r] - 1]; lengths below
- * 0 count as 0, above ld_tokens as that; tokens outside 0 .. V - 1 (of a history or a
- * bias) are ignored.  Entries past bias_entries are not read.  Columns V .. ld_out - 1
- * stay as they were.  out may be logits (then ld_out = ld; only what a rule changes is
- * read and written), else it must not overlap it.
+ * In fp32 (a value past its range becomes infinite).  A row's tokens are
+ * tokens[r * ld_tokens + 0 .. lens[r] - 1]; lengths below 0 count as 0, above ld_tokens
+ * as that; tokens outside 0 .. V - 1 (of a history or a bias) are ignored.  Entries past
+ * bias_entries are not read.  Columns V .. ld_out - 1 stay as they were.  out may be
+ * logits (then ld_out = ld; only what a rule changes is read and written), else it must
+ * not overlap it.
  */
 typedef struct q8_logit_rules {
   const int32_t *tokens;      /* m x ld_tokens, or NULL: no penalties            */

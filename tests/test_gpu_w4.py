@@ -259,6 +259,37 @@ def test_pair(m, K, N, group, zeros, fmt, many, act):
     assert torch.isnan(untouched).all()
 
 
+@pytest.mark.parametrize("m", [2, 20, 70, 1025])
+def test_large_activations(m):
+    """Rows at the header's bound on a bf16 activation, 2^112 (the exact case's largest value is 127)."""
+    for zeros in (False, True):
+        K, N = 160, 5129 if m > 1000 else 130
+        w = Weight(K, N, 128, zeros, 1, 97, exact=True, points=(0, 256)).pack()
+        a = Act(m, K, BF16, 101, exact=True)
+        want = a.times(w)[0]
+        a.dev.copy_(torch.where(a.dev == 0, a.dev, a.dev + (105 << 7)))       # times 2^105
+        got = (u.gemv(a, w) if m <= 32 else u.gemm(a, w)).cpu().numpy()[:, :N].astype(np.float64)
+        np.testing.assert_array_equal(got * 2.0 ** -105, want)
+
+
+@pytest.mark.parametrize("act", [BF16, Q8])
+@pytest.mark.parametrize("m", [3, 24, 100, 1025])
+def test_smallest_scales(m, act):
+    """fp16 scales below its normal range (2^-24 .. 2^-21) are exact."""
+    K, N = 96, 5129 if m > 1000 else 70
+    w = Weight(K, N, 32, False, 0, 103, exact=True)
+    w.s = scale_bits_of(w.s, 2.0 ** -21)
+    w.canonical = (w.u, w.s, w.z, w.fmt, w.group)
+    w.pack()
+    a = Act(m, K, act, 107, exact=True)
+    got = u.real(u.gemv(a, w) if m <= 32 else u.gemm(a, w), N)
+    np.testing.assert_array_equal(got, a.times(w)[0])
+
+
+def scale_bits_of(bits, factor):
+    return (bits.view(np.float16) * np.float16(factor)).view(np.uint16)
+
+
 def test_one_workspace_serves_every_shape():
     """Splits over one zeroed workspace, products and pairs in turn: its counters end at zero."""
     cases = [(1, 4096, 40), (32, 2048, 300), (7, 1024, 900), (16, 4096, 130)]
