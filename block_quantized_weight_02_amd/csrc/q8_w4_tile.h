@@ -30,7 +30,7 @@
 // The waves' carries meet in LDS, the splits' through finish_tile.
 //
 // Measured, calls back to back: m = 1, K = 4096, N = 14336 8.1 us, N = 32000 13.5 (68 MB,
-// 5.0 TB/s); m = 16, N = 14336, zero points 9.5 (31 MB; a plain read 4.9): the launch, the
+// 5.0 TB/s); m = 16, N = 14336, zero points 9.1 (31 MB; a plain read 4.9): the launch, the
 // first loads' latency and the join stand beside the stream.  Q8_0, groups of 32, m = 32, K
 // = 5120, N = 32001 31 (92 MB; a plain read 14): the vector unit, busy 60 % (three
 // instructions a result and block, conversion and two scales; with zero points four), the
@@ -553,8 +553,11 @@ hipError_t launch_w4_g(const W4Args &a, hipStream_t stream) {
                       : launch_w4_k<ACT, W, RG, EL, LE, NT, 1, false, PAIR>(a, stream);
     case 64: return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 2, true, PAIR>(a, stream)
                       : launch_w4_k<ACT, W, RG, EL, LE, NT, 2, false, PAIR>(a, stream);
-    case 128: return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 4, true, PAIR>(a, stream)
-                       : launch_w4_k<ACT, W, RG, EL, LE, NT, 4, false, PAIR>(a, stream);
+    case 128:
+      // (16 waves leave it 128 registers, fewer than it has in use)
+      if constexpr (ACT == kActQ8 && W == 16 && EL == 4) return hipErrorInvalidValue;
+      else return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 4, true, PAIR>(a, stream)
+                    : launch_w4_k<ACT, W, RG, EL, LE, NT, 4, false, PAIR>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -579,6 +582,7 @@ hipError_t launch_w4_tile(const W4Plan &p, bool pair, const W4Args &a, hipStream
     case 4081: return launch_w4_g<ACT, 8, 1, 1, 1, 1, false>(a, stream);
     case 4161: return launch_w4_g<ACT, 16, 1, 1, 1, 1, false>(a, stream);
     case 16081: return launch_w4_g<ACT, 8, 1, 4, 4, 1, false>(a, stream);
+    case 16161: return launch_w4_g<ACT, 16, 1, 4, 4, 1, false>(a, stream);
     case 32081: return launch_w4_g<ACT, 8, 2, 4, 4, 1, false>(a, stream);
     case 32082: return launch_w4_g<ACT, 8, 2, 4, 4, 2, false>(a, stream);
     case 64081: return launch_w4_g<ACT, 8, 4, 4, 4, 1, false>(a, stream);
