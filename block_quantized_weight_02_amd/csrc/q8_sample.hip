@@ -349,7 +349,7 @@ struct Steps {
     if (!(per > 0.0f) || !(per < INFINITY)) per = 1.0f;
   }
   __device__ __forceinline__ int operator()(float l) const {
-    return l == M ? 0 : (int)fminf((M - l) * per, (float)(kBins - 1));
+    return (int)fminf((M - l) * per, (float)(kBins - 1));
   }
 };
 
@@ -396,8 +396,10 @@ __device__ u64 sorted(Lds &s, int n, int size) {
 }
 
 // Of a tile the weight that stands before step `bin`; found(j) of its tokens in it.
-template <typename F>
-__device__ __forceinline__ u64 collect_tile(const Keep &keep, const Steps &step, int bin, const float (&v)[kVals],
+// MIN: the row may have min_p; else its test is left out (256 rows of 131072, mixed: 105 ->
+// 102 us; a workgroup a row has no registers for both).
+template <bool MIN, typename F>
+__device__ __forceinline__ u64 collect_kind(const Keep &keep, const Steps &step, int bin, const float (&v)[kVals],
                                             F found) {
   u64 wt = 0;
 #pragma unroll
@@ -411,13 +413,19 @@ __device__ __forceinline__ u64 collect_tile(const Keep &keep, const Steps &step,
     if (__any(least <= bin)) {             // (not a branch a token: their chains run side by side)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const u64 w = keep(v[j + c]);
+        const u64 w = MIN ? keep(v[j + c]) : weight_of(keep.w, v[j + c]);
         wt += b[c] < bin ? w : 0;
         if (b[c] == bin) found(j + c);
       }
     }
   }
   return wave_sum(wt);
+}
+template <typename F>
+__device__ __forceinline__ u64 collect_tile(const Keep &keep, const Steps &step, int bin, const float (&v)[kVals],
+                                            F found) {
+  return keep.min_w > 0.0 ? collect_kind<true>(keep, step, bin, v, found)
+                          : collect_kind<false>(keep, step, bin, v, found);
 }
 
 // Of a number each wave has put into LDS: the sum over the waves before this one, and
@@ -1204,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
     again = bin < kBins && s.bin_n > kCand;
     if (!again) {
       held.each([&](int t, const float (&v)[kVals]) {
-        const u64 wt = collect_tile(keep, step, bin, v, [&](int j) {
+        const u64 wt = collect_kind<true>(keep, step, bin, v, [&](int j) {
           const int c = atomicAdd(&s.n_cand, 1);
           if (c < kCand) s.cand[c] = packed(v[j], index_of(t, lane, j));
         });
