@@ -37,7 +37,7 @@ hipError_t launch_logit_rules(const LogitRulesArgs &a, hipStream_t stream);
 struct SliceStat {                            // of a slice of a row
   float top;                                  // its largest logit
   int at;                                     // the lowest index of that
-  float exp_sum;                              // of exp(l - top)
+  double exp_sum;                             // of exp(l - top)
   float sum;                                  // of the logits that can weigh anything
   unsigned n;                                 // how many those are
 };

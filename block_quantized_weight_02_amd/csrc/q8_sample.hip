@@ -280,7 +280,7 @@ __device__ __forceinline__ double exp_sum_of(const SampleArgs &a, int row, int l
   for (int i = lane; i < a.slices; i += 64) {
     const SliceStat v = st[i];
     if (v.top > -INFINITY)
-      e += v.top == top ? (double)v.exp_sum : (double)v.exp_sum * exp((double)v.top - (double)top);
+      e += v.top == top ? v.exp_sum : v.exp_sum * exp((double)v.top - (double)top);
   }
   return wave_sum(e);
 }
@@ -546,14 +546,16 @@ __device__ __forceinline__ int index_in(const float (&v)[kVals], float top, int 
   return at;
 }
 // exp(l - top), summed; top finite, or infinite (then of those alone), or -infinity (0).
-__device__ __forceinline__ float exp_sum_in(const float (&v)[kVals], float top) {
-  float e = 0.0f;
+// (The terms in fp32, their sum in fp64: beside the largest one's 1 the small ones would
+// be rounded to 2^-24, and a log-probability near 0 is their sum.)
+__device__ __forceinline__ double exp_sum_in(const float (&v)[kVals], float top) {
+  double e = 0.0;
   if (fabsf(top) < INFINITY) {
 #pragma unroll
-    for (int j = 0; j < kVals; ++j) e += __builtin_amdgcn_exp2f((v[j] - top) * 1.44269504088896f);
+    for (int j = 0; j < kVals; ++j) e += (double)__builtin_amdgcn_exp2f((v[j] - top) * 1.44269504088896f);
   } else if (top > 0.0f) {
 #pragma unroll
-    for (int j = 0; j < kVals; ++j) e += v[j] == INFINITY;
+    for (int j = 0; j < kVals; ++j) e += v[j] == INFINITY ? 1.0 : 0.0;
   }
   return e;
 }
@@ -592,8 +594,8 @@ __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const Sam
   float sum = 0.0f;
   uint32_t n = 0;
   if (r.by_k || r.by_p) mean_in(v, top, r.T, sum, n);
-  const float e = a.logprob ? exp_sum_in(v, top) : 0.0f;
-  const double ds = wave_sum((double)sum), de = wave_sum((double)e);
+  const double e = a.logprob ? exp_sum_in(v, top) : 0.0;
+  const double ds = wave_sum((double)sum), de = wave_sum(e);
   n = wave_sum(n);
   if (lane == 0) {
     wsum[wave] = ds;
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const Sam
       x += wexp[i];
       c += wn[i];
     }
-    a.stats[(size_t)row * a.slices + slice] = SliceStat{top, (int)~(uint32_t)best, (float)x, (float)d, c};
+    a.stats[(size_t)row * a.slices + slice] = SliceStat{top, (int)~(uint32_t)best, x, (float)d, c};
   }
 }
 
@@ -1152,13 +1154,14 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
   }
   double exp_sum = 1.0;
   if (cut || a.logprob) {
-    float e = 0.0f, sum = 0.0f;
+    double e = 0.0;
+    float sum = 0.0f;
     uint32_t n = 0;
     held.each([&](int, const float (&v)[kVals]) {
       if (cut) mean_in(v, top, r.T, sum, n);
       if (a.logprob) e += exp_sum_in(v, top);
     });
-    const double de = wave_sum((double)e), ds = wave_sum((double)sum);
+    const double de = wave_sum(e), ds = wave_sum((double)sum);
     n = wave_sum(n);
     if (lane == 0) {
       s.wexp[wave] = de;

@@ -355,6 +355,20 @@ def test_draws_follow_the_weights():
     np.testing.assert_allclose(np.bincount(token, minlength=5) / n, [4 / 7, 1 / 7, 2 / 7, 0, 0], atol=1.01 / n)
 
 
+@pytest.mark.parametrize("d", [4, 8, 14, 20])
+@pytest.mark.parametrize("v", [1000, 20001, 40001])
+def test_log_probabilities_near_zero(v, d):
+    """One token d above all others: -log(1 + (V - 1) exp(-d)), relative to itself.  A term's exponent is
+    rounded thrice (difference, product, constant), each d 2^-24 of it, the exponential by at most two
+    steps of 2^-24, the result once more."""
+    x = np.full((3, v), -float(d), np.float32)
+    x[np.arange(3), [0, v // 2, v - 1]] = 0.0
+    token, lp = draw(x, 0.5, temperature=0.0)
+    np.testing.assert_array_equal(token, [0, v // 2, v - 1])
+    want = -math.log1p((v - 1) * math.exp(-d))
+    assert (np.abs(lp - want) <= (3 * d + 4) * 2.0 ** -24 * -want).all(), (lp, want)
+
+
 def test_draw_without_logprob():
     r = np.random.default_rng(37)
     x = r.standard_normal((3, 500)).astype(np.float32)
