@@ -33,9 +33,9 @@
 // They are five launches with the rows' vocabularies in slices, so that few long rows too
 // are worked on by many CUs, or one launch with a workgroup a row, where a row is short
 // enough for its registers (launch_sample has both sides' figures).  Mixed kinds of rows:
-// 1 x 32000 17 us, 40 x 50001 36, 256 x 131072 105.  The first pass of those 256 rows, 24
+// 1 x 32000 17 us, 40 x 50001 36, 256 x 131072 102.  The first pass of those 256 rows, 24
 // us, is bound by their 134 MB; the second, 40, by fp64, by additions in LDS and by the
-// rows' unlike work; the collecting one, 28, by fp64 and the same; the two with a
+// rows' unlike work; the collecting one, 24, by fp64 and the same; the two with a
 // workgroup a row (6 and 13), and all of them with few rows, by latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
