@@ -44,7 +44,7 @@ logit_rules_kernel(const LogitRulesArgs a, int slice) {
   if constexpr (HELD) held = (int)min((int64_t)max(u.lens[r], 0), u.ld_tokens);
   if constexpr (BIASED) {
     bias_lo = max(u.bias_start[r], 0);
-    bias_hi = (int)min((int64_t)u.bias_start[r + 1], u.n_bias);
+    bias_hi = (int)min((int64_t)max(u.bias_start[r + 1], 0), u.n_bias);   // (below 0: none)
   }
   const bool any = (HELD && held > 0) || (BIASED && bias_hi > bias_lo);
   const uint32_t *mask = nullptr;

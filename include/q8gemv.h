@@ -834,8 +834,8 @@ int q8_attn_rows(const uint16_t *q, int64_t m, int64_t q_heads,
  *     (a row of -1, or any outside 0 .. mask_rows - 1: no mask).
  * In fp32 (a value past its range becomes infinite).  A row's tokens are
  * tokens[r * ld_tokens + 0 .. lens[r] - 1]; lengths below 0 count as 0, above ld_tokens
- * as that; tokens outside 0 .. V - 1 (of a history or a bias) are ignored.  Entries past
- * bias_entries are not read.  Columns V .. ld_out - 1 stay as they were.  out may be
+ * as that; tokens outside 0 .. V - 1 (of a history or a bias) are ignored.  Starts of
+ * biases below 0 count as 0; entries past bias_entries are not read.  Columns V .. ld_out - 1 stay as they were.  out may be
  * logits (then ld_out = ld; only what a rule changes is read and written), else it must
  * not overlap it.
  */

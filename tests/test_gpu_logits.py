@@ -149,6 +149,21 @@ def test_rules_bounds():
                                bias_value=g.dev(np.array([b for _, b in flat], np.float32)), bias_entries=entries))
 
 
+@pytest.mark.parametrize("held", [0, 13])
+def test_rules_of_biases_that_end_below_zero(held):
+    """A start below 0 is 0: a row that ends there has no biases, with a history and without one, and
+    the next row's begin at 0."""
+    m, v = 5, 130
+    s = Rules(m, v, 13, held, 6, 2)
+    flat = [(int(t), np.float32(b)) for t, b in zip(s.r.integers(0, v, 9), s.r.standard_normal(9))]
+    start = np.array([-3, -1, 4, -2 ** 31, -7, 9], np.int32)
+    s.bias = [[], flat[0:4], [], [], flat]
+    x = s.r.standard_normal((m, v)).astype(np.float32)
+    check_rules(s, x, s.device(bias_start=g.dev(start),
+                               bias_token=g.dev(np.array([t for t, _ in flat], np.int32)),
+                               bias_value=g.dev(np.array([b for _, b in flat], np.float32)), bias_entries=9))
+
+
 def test_rules_without_optional_arrays():
     """Every token made, no penalties but one; masks by row."""
     s = Rules(3, 200, 11, 20, 0, 3)
