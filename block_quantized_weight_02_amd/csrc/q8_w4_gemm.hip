@@ -173,7 +173,10 @@ w4_gemm_kernel(const W4Args a, int MB, int NBN) {
   const auto load = [&](Weight &st, int b) Q8_INLINE {
 #pragma unroll
     for (int u = 0; u < kCB; ++u) {
-      const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(wr, (unsigned)lane * 16u, (unsigned)(b + u) * kW4Chunk, 0);
+      // (past K the last block again: a resource's extent need not bound an access by its
+      // uniform offset)
+      const unsigned at = (unsigned)(u ? min(b + u, a.NB - 1) : b) * kW4Chunk;
+      const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(wr, (unsigned)lane * 16u, at, 0);
       st.v[u] = make_uint4(v.x, v.y, v.z, v.w);
     }
     if constexpr (NS == 2) {

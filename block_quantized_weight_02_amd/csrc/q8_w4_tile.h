@@ -233,18 +233,20 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
     Weight w[NT];
   };
   auto load = [&](Stage &st, int bv, int slot) Q8_INLINE {
-    const int b = __builtin_amdgcn_readfirstlane(bv);
+    const int b = __builtin_amdgcn_readfirstlane(bv), last = a.NB - 1;
+    // (past K the last block and pair of groups again, and not used: a resource's extent
+    // need not bound an access by its uniform offset)
     __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the slot's last reads have returned
     fetch(b, slot);
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
       Weight &w = st.w[k];
 #pragma unroll
-      for (int u = 0; u < QB; ++u) w.v[u] = buf_ld16(wr[k], lw, (unsigned)(b + u) * kW4Chunk);
+      for (int u = 0; u < QB; ++u) w.v[u] = buf_ld16(wr[k], lw, (unsigned)min(b + u, last) * kW4Chunk);
       if constexpr (NS >= 2) {           // two groups a load
 #pragma unroll
         for (int p = 0; p < NS / 2; ++p) {
-          const unsigned pair = (unsigned)(b / GB / 2 + p);
+          const unsigned pair = (unsigned)min(b / GB / 2 + p, (int)groups / 2 - 1);
           const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(sr[k], (unsigned)i * 16u, pair * 256u, 0);
           w.sc[2 * p] = make_uint2(v.x, v.y);
           w.sc[2 * p + 1] = make_uint2(v.z, v.w);

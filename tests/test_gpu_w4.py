@@ -259,6 +259,22 @@ def test_pair(m, K, N, group, zeros, fmt, many, act):
     assert torch.isnan(untouched).all()
 
 
+@pytest.mark.parametrize("act", [BF16, Q8])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
+def test_weights_that_end_with_their_allocation(group, zeros, act):
+    """Five blocks of 32 rows, no whole stage of any kernel, and values of exactly 10 MiB, which the
+    allocator gives an allocation of their own: a stage's loads stay within the last tile."""
+    K, N = 160, 1 << 17
+    w = Weight(K, N, group, zeros, 0, 113, exact=True)
+    torch.cuda.empty_cache()
+    w.pack()
+    assert w.values.numel() == 10 << 20
+    for m in (1, 7, 16, 32, 64, 130):
+        a = Act(m, K, act, 109, exact=True)
+        got = u.real(u.gemv(a, w) if m <= 32 else u.gemm(a, w), N)
+        np.testing.assert_array_equal(got, a.times(w)[0], err_msg=f"{m} rows")
+
+
 @pytest.mark.parametrize("m", [2, 20, 70, 1025])
 def test_large_activations(m):
     """Rows at the header's bound on a bf16 activation, 2^112 (the exact case's largest value is 127)."""
