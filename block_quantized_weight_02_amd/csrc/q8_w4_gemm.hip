@@ -8,7 +8,7 @@
 //     tile's dwords straight into registers (one 16-byte load a block) and turns them
 //     into bf16 there, once for its 128 rows: u - 8 (with zero points u - z), exact, in
 //     1/16ths by the 4-bit conversion, two values in 3.5 instructions (5.5).  The
-//     1/16 is in the scale;
+//     sums are 16ths too, until they are stored (16 times a scale could pass fp32's range);
 //   * the activation rows of two blocks are staged in LDS, double buffered: bf16 rows
 //     loaded straight into LDS, Q8_0 codes widened to bf16 on the way (exact: their
 //     products' sums are then the same exact integers, in fp32), with their scales;
@@ -213,8 +213,6 @@ w4_gemm_kernel(const W4Args a, int MB, int NBN) {
     for (int n = 0; n < NS; ++n) {
       float sc[4];
       w4_scales4(st.sc[n], a.scale_bf16 ? ~0u : 0u, sc);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) sc[g] *= 16.0f;
       bf16x8_t bw[CH][4];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -326,6 +324,10 @@ w4_gemm_kernel(const W4Args a, int MB, int NBN) {
   compute(std::false_type{}, wa, (NC - 1) & 1, a.NB - (NC - 1) * kCB);
 
   // ---- the outputs
+#pragma unroll
+  for (int rg = 0; rg < kRG; ++rg)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) acc[rg][g] *= 16.0f;
   const Epi &ep = a.ep;
   if constexpr (!PAIR) {
     if (t >= a.T) return;

@@ -302,6 +302,30 @@ def test_smallest_scales(m, act):
     np.testing.assert_array_equal(got, a.times(w)[0])
 
 
+@pytest.mark.parametrize("act", [BF16, Q8])
+@pytest.mark.parametrize("group,zeros", [(32, True), (128, False)])
+@pytest.mark.parametrize("m", [3, 24, 100, 1025])
+def test_largest_scales(m, group, zeros, act):
+    """bf16 scales of 2^123 .. 2^126 over an activation of 2^-110, the product and the pair: nothing on the
+    way to an output is larger than it."""
+    K, N = 96, 5129 if m > 1000 else 70
+    w = Weight(K, N, group, zeros, 1, 127, exact=True)
+    w.s = (w.s + (126 << 7)).astype(np.uint16)
+    w.canonical = (w.u, w.s, w.z, w.fmt, w.group)
+    w.pack()
+    a = Act(m, K, act, 131, exact=True)
+    x = a.x * 2.0 ** -110
+    bits = (x.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    a.dev = g.quantize(bits) if act == Q8 else g.dev(bits.view(np.int16))
+    a.x, a.d = x, getattr(a, "d", np.ones(1)) * 2.0 ** -110
+    want = a.times(w)[0]
+    got = u.real(u.gemv(a, w) if m <= 32 else u.gemm(a, w), N)
+    np.testing.assert_array_equal(got, want)
+    y = u.real(u.pair(a, w, w, many=m > 32), N)
+    with np.errstate(over="ignore"):
+        u.compare(y, pair_tolerance((want, 0, 0), (want, 0, 0), 0.0, 0.0), "pair")
+
+
 def scale_bits_of(bits, factor):
     return (bits.view(np.float16) * np.float16(factor)).view(np.uint16)
 
