@@ -57,6 +57,18 @@ constexpr int kSampleTile = 1024;             // tokens a wave takes at a time
 constexpr int kSampleSlice = 4096;            // tokens of a slice of the statistics
 constexpr int kSampleBins = 2048, kSampleCand = 1024;
 constexpr int kMaxVocab = 1 << 20;
+constexpr int kSampleHeld = 4 * 16 * kSampleTile;   // of a row in a workgroup's registers
+
+// Which rows are drawn by one launch, a workgroup a row, without a workspace: those that
+// fit its registers, from half of them on only with rows for a third of the CUs (us, mean
+// of the kinds of rows, one launch against slices: 1 x 1000 11 against 23, 1 x 32000 20
+// against 25, 256 x 32000 25 against 46, 128 x 65000 38 against 46, 256 x 65000 43 against
+// 61; but 1 x 50001 28 against 27, 8 x 50001 mixed 42 against 33, 64 x 65000 mixed 57
+// against 49).
+constexpr int kSampleHeldRows = 96;
+constexpr bool sample_in_one_launch(int64_t m, int64_t V) {
+  return V <= kSampleHeld / 2 || (V <= kSampleHeld && m >= kSampleHeldRows);
+}
 
 struct SampleArgs {
   const float *logits;

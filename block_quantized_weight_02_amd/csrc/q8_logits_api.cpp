@@ -24,31 +24,54 @@ int check_rows(const float *logits, int64_t ld, int64_t m, int64_t V, const char
   return Q8_OK;
 }
 
-// The draw's workspace: its bytes, and with `ws` the places in it.  The products' and
-// attention's counters at its start are left alone, so that one workspace serves all.
-size_t sample_layout(SampleArgs &a, char *ws) {
+// Workgroups of a row and pass, at most: of 8 waves, a tile a wave, and not too many for
+// one workgroup to sum their histograms.
+int64_t most_parts(int64_t tiles) { return std::min<int64_t>((tiles + 7) / 8, 64); }
+constexpr int64_t kParts = 1024;           // of all rows together, about
+
+// The workspace of rows drawn in slices, with `parts` workgroups a pass in all: its bytes,
+// and with `ws` the places in it.  The products' and attention's counters at its start are
+// left alone, so that one workspace serves all.
+size_t sample_layout(SampleArgs &a, int64_t rows, int64_t parts, char *ws) {
   const int64_t tiles = (a.V + kSampleTile - 1) / kSampleTile;
   a.slices = (a.V + kSampleSlice - 1) / kSampleSlice;
   a.row_tiles = (int)tiles;
-  // workgroups of a row and pass: of 8 waves, a tile a wave, about 1024 in all and not too
-  // many for one workgroup to sum their histograms (40 rows of 131072, mixed: 8 each 47 us,
-  // 12 46, 16 46, 25 52; 256 rows: 2 each 121, 4 105, 8 99 but all of one kind 83, 85, 93)
-  a.parts = (int)std::min<int64_t>(std::min<int64_t>((tiles + 7) / 8, 64), std::max<int64_t>(1, 1024 / a.m));
   size_t at = kCounterBytes;
   const auto take = [&](size_t bytes) {
     char *p = ws + at;
     at += (size_t)round_up((int64_t)bytes, 256);
     return ws ? p : nullptr;
   };
-  const size_t m = (size_t)a.m;
+  const size_t m = (size_t)rows;
   a.stats = reinterpret_cast<SliceStat *>(take(m * a.slices * sizeof(SliceStat)));
   a.cuts = reinterpret_cast<RowCut *>(take(m * sizeof(RowCut)));
   a.tops = reinterpret_cast<float *>(take(m * tiles * 4));
   a.tiles = reinterpret_cast<unsigned long long *>(take(m * tiles * 8));
-  a.counts = reinterpret_cast<uint32_t *>(take(m * a.parts * kSampleBins * 4));
-  a.masses = reinterpret_cast<unsigned long long *>(take(m * a.parts * kSampleBins * 8));
+  a.counts = reinterpret_cast<uint32_t *>(take((size_t)parts * kSampleBins * 4));
+  a.masses = reinterpret_cast<unsigned long long *>(take((size_t)parts * kSampleBins * 8));
   a.cands = reinterpret_cast<Candidate *>(take(m * kSampleCand * sizeof(Candidate)));
   return at;
+}
+
+// Bytes that serve every call of up to m rows of up to V logits: of the sliced ones among
+// them the most rows and workgroups, and 256 bytes where there are none.
+size_t sample_bytes(int64_t m, int64_t V) {
+  const int64_t rows = sample_in_one_launch(1, V) ? 0
+                       : sample_in_one_launch(m, V) ? kSampleHeldRows - 1 : m;
+  if (rows == 0) return kCounterBytes + 256;
+  SampleArgs a{};
+  a.V = (int)V;
+  const int64_t each = most_parts((V + kSampleTile - 1) / kSampleTile);
+  return sample_layout(a, rows, std::min(rows * each, std::max(kParts, rows)), nullptr);
+}
+
+// A sliced call's places, within sample_bytes(m, V) bytes.
+void sample_places(SampleArgs &a, char *ws) {
+  // (40 rows of 131072, mixed: 8 each 47 us, 12 46, 16 46, 25 52; 256 rows: 2 each 121, 4
+  // 105, 8 99 but all of one kind 83, 85, 93)
+  const int64_t tiles = (a.V + kSampleTile - 1) / kSampleTile;
+  a.parts = (int)std::min(most_parts(tiles), std::max<int64_t>(1, kParts / a.m));
+  sample_layout(a, a.m, (int64_t)a.m * a.parts, ws);
 }
 
 }  // namespace
@@ -118,10 +141,7 @@ int q8_logits_rules(const float *logits, int64_t ld, int64_t m, int64_t V,
 
 size_t q8_sample_workspace_bytes(int64_t m, int64_t V) {
   if (check_rows(nullptr, (V + 3) / 4 * 4, m, V, "ld")) return 0;
-  SampleArgs a{};
-  a.m = (int)m;
-  a.V = (int)V;
-  return sample_layout(a, nullptr);
+  return sample_bytes(m, V);
 }
 
 int q8_sample(const float *logits, int64_t ld, int64_t m, int64_t V, const q8_sampling *sampling,
@@ -148,8 +168,8 @@ int q8_sample(const float *logits, int64_t ld, int64_t m, int64_t V, const q8_sa
   a.u = sampling->u;
   a.token = token;
   a.logprob = logprob;
-  if ((st = check_workspace(workspace, ws_bytes, sample_layout(a, nullptr)))) return st;
-  sample_layout(a, static_cast<char *>(workspace));
+  if ((st = check_workspace(workspace, ws_bytes, sample_bytes(m, V)))) return st;
+  if (!sample_in_one_launch(m, V)) sample_places(a, static_cast<char *>(workspace));
   return done(launch_sample(a, stream), "sample launch");
 }
 

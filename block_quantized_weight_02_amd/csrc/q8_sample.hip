@@ -32,7 +32,7 @@
 //
 // They are five launches with the rows' vocabularies in slices, so that few long rows too
 // are worked on by many CUs, or one launch with a workgroup a row, where a row is short
-// enough for its registers (launch_sample has both sides' figures).  Mixed kinds of rows:
+// enough for its registers (sample_in_one_launch has both sides' figures).  Mixed kinds of rows:
 // 1 x 32000 17 us, 40 x 50001 36, 256 x 131072 102.  The first pass of those 256 rows, 24
 // us, is bound by their 134 MB; the second, 40, by fp64, by additions in LDS and by the
 // rows' unlike work; the collecting one, 24, by fp64 and the same; the two with a
@@ -52,7 +52,7 @@ constexpr int kMaxTiles = kMaxVocab / kSampleTile;
 static_assert(kMaxTiles <= kThreads && kCand <= kThreads && kSampleTile == kThreads,
               "a thread takes a tile's sum, a candidate and a token of the drawn tile");
 constexpr int kVals = 16;                  // tokens of a tile a lane holds
-constexpr int kHeldTokens = 4 * kWaves * kSampleTile;   // of a row in a workgroup's registers
+static_assert(kSampleHeld == 4 * kWaves * kSampleTile, "the row kernels hold four tiles a wave at most");
 constexpr int kStatTiles = kSampleSlice / kSampleTile;   // one a wave
 
 typedef unsigned long long u64;
@@ -1251,19 +1251,13 @@ hipError_t launch_slices(const SampleArgs &a, hipStream_t stream) {
 
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {
   (void)hipGetLastError();
-  // One launch, a workgroup a row, where a row's tiles fit a workgroup's registers; from
-  // half of them on only with rows for a third of the CUs (us, mean of the kinds of rows,
-  // one launch against slices: 1 x 1000 11 against 23, 1 x 32000 20 against 25, 256 x 32000
-  // 25 against 46, 128 x 65000 38 against 46, 256 x 65000 43 against 61; but 1 x 50001 28
-  // against 27, 8 x 50001 mixed 42 against 33, 64 x 65000 mixed 57 against 49)
-  if (a.V <= kHeldTokens / 4)
+  if (!sample_in_one_launch(a.m, a.V)) return launch_slices(a, stream);
+  if (a.V <= kSampleHeld / 4)
     sample_row_kernel<1><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
-  else if (a.V <= kHeldTokens / 2)
+  else if (a.V <= kSampleHeld / 2)
     sample_row_kernel<2><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
-  else if (a.V <= kHeldTokens && a.m >= 96)
-    sample_row_kernel<4><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
   else
-    return launch_slices(a, stream);
+    sample_row_kernel<4><<<(unsigned)a.m, kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

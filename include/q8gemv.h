@@ -879,10 +879,11 @@ int q8_logits_rules(const float *logits, int64_t ld, int64_t m, int64_t V,
  * among equal ones.  NaN and -infinity have no weight; a row of nothing else gets token
  * -1 and log-probability -infinity.  Among logits of +infinity only those are drawn.
  *
- * The workspace is the caller's: q8_sample_workspace_bytes(m, V) bytes, 16-byte aligned.
- * It needs no initialisation, and its first 4 MiB, the counters of other calls that share
- * it, are left alone; calls that share it must be ordered, graphs captured over it
- * included.  Q8_ERR_WORKSPACE when too small.
+ * The workspace is the caller's: q8_sample_workspace_bytes(m, V) bytes, 16-byte aligned;
+ * those of the most rows and the largest vocabulary serve every smaller call.  It needs
+ * no initialisation, and its first 4 MiB, the counters of other calls that share it, are
+ * left alone; calls that share it must be ordered, graphs captured over it included.
+ * Q8_ERR_WORKSPACE when too small.
  */
 typedef struct q8_sampling {
   const float *temperature; /* m, or NULL: 1                                     */

@@ -326,6 +326,31 @@ def test_a_row_is_drawn_alike_alone_and_in_a_batch(v):
             assert draw(x[i:i + 1], u[i:i + 1], **limits)[0][0] == token[i]
 
 
+@pytest.mark.parametrize("m,v", [(3, 1000), (2, 32769), (95, 40001), (96, 40001), (40, 65536), (5, 65537),
+                                 (170, 70001)])
+def test_draw_within_its_workspace(m, v):
+    """Draws over a workspace of exactly the bytes asked for, and of those of more rows: nothing behind
+    them is written, nor the counters in front, and the tokens are the same."""
+    r = np.random.default_rng([61, v])
+    x = (r.standard_normal((m, v)) * 3).astype(np.float32)
+    u = r.random(m)
+    limits = dict(top_k=r.choice([0, 50], m).astype(np.int32), top_p=r.choice([1.0, 0.9], m))
+    want, want_lp = draw(x, u, **limits)
+    rows = torch.zeros((m, ld_of(v)), device=g.DEV)
+    rows[:, :v] = g.dev(x)
+    keep = [g.dev(u), g.dev(limits["top_k"]), g.dev(limits["top_p"].astype(np.float32))]
+    for need in (q8.q8_sample_workspace_bytes(m, v), q8.q8_sample_workspace_bytes(m + 1, v + 5)):
+        ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=g.DEV)
+        token = torch.zeros(m, dtype=torch.int32, device=g.DEV)
+        lp = torch.zeros(m, device=g.DEV)
+        q8.q8_sample(rows, ld_of(v), m, v, q8.make_sampling(keep[0], top_k=keep[1], top_p=keep[2]), token, lp,
+                     None, ws, need)
+        torch.cuda.synchronize()
+        assert (ws[:4 << 20] == 0xA5).all() and (ws[need:] == 0xA5).all()
+        np.testing.assert_array_equal(token.cpu().numpy(), want)
+        np.testing.assert_array_equal(lp.cpu().numpy(), want_lp)
+
+
 def test_draw_at_the_ends_of_u():
     x = np.zeros((6, 40), np.float32)
     x[:, :8] = -INF

@@ -76,6 +76,30 @@ def test_sample_workspace():
     refuse(5, lambda: sample(ws_bytes=need - 1), part="needed")
 
 
+VOCABULARIES = (1, 1000, 32000, 32768, 32769, 50001, 65536, 65537, 131072, 1 << 20)
+
+
+def test_a_sample_workspace_serves_smaller_calls():
+    """Bytes never fall with the rows or the vocabulary."""
+    rows = [*range(1, 400), 511, 512, 513, 1023, 1024, 1025, 4000, 8192]
+    last = {m: 0 for m in rows}
+    for v in VOCABULARIES:
+        need = {m: q8.q8_sample_workspace_bytes(m, v) for m in rows}
+        for a, b in zip(rows, rows[1:]):
+            assert need[a] <= need[b], (a, b, v)
+        for m in rows:
+            assert need[m] >= last[m], (m, v)
+        last = need
+
+
+def test_rows_drawn_by_one_launch_ask_for_no_slices():
+    """Rows of up to 32768 logits: no more than the counters' 4 MiB and a little; longer ones for the
+    slices of fewer than 96 rows where more are drawn by one launch."""
+    for m, v in ((1, 100), (8192, 32000), (300, 32768)):
+        assert q8.q8_sample_workspace_bytes(m, v) <= (4 << 20) + 4096
+    assert q8.q8_sample_workspace_bytes(8192, 50001) == q8.q8_sample_workspace_bytes(95, 50001) > 8 << 20
+
+
 def test_oracle_of_the_rules():
     x = np.array([1.0, -1.0, 2.0, 3.0, 4.0], np.float32)
     y, _ = ol.rules(x, [0, 1, 3, 3, 9, -1], 2, 2.0, 0.5, 0.25, [(2, 1.0), (2, 5.0), (7, 1.0)], np.array([0b01111]))
