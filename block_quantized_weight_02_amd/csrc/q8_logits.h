@@ -38,7 +38,7 @@ struct SliceStat {                            // of a slice of a row
   float top;                                  // its largest logit
   int at;                                     // the lowest index of that
   double exp_sum;                             // of exp(l - top)
-  float sum;                                  // of the logits that can weigh anything
+  float sum;                                  // of the logits not far below it
   unsigned n;                                 // how many those are
 };
 struct RowCut {                               // where a row's order is cut

@@ -15,7 +15,7 @@
 //
 // Five passes:
 //   stats    of a slice: its largest logit with the lowest index, sum of exp(l - that),
-//            the mean of what can weigh anything, and each tile's largest;
+//            the mean of what is not far below it, and each tile's largest;
 //   weights  rows with a limit on the order: counts (for top_p weights too) of 2047 even
 //            steps of M - l, in LDS, a slice's histogram written out whole; rows without
 //            one: the weights' sum of each tile of 1024 tokens;
@@ -207,8 +207,10 @@ __device__ __forceinline__ u64 wave_largest(u64 v) {
 }
 
 // What the launches hand on about a row.
+constexpr float kFar = 60.0f;              // in units of T, below the largest: no weight
 struct Params {                            // the row's limits
   float T;
+  float far;                               // logits this far below the largest are no part of the mean
   int k;
   float p;
   double min_p;
@@ -224,10 +226,12 @@ __device__ __forceinline__ Params params_of(const SampleArgs &a, int row) {
   r.min_p = mp > 0.0f ? fmin((double)mp, 1.0) : 0.0;
   r.by_k = !r.greedy && r.k > 0 && r.k < a.V;
   r.by_p = !r.greedy && r.p < 1.0f;
+  // (top_k's order does not depend on T: at a low one the mean of what can weigh anything
+  // lies beside the largest, and the cut behind all the steps that reach to it)
+  r.far = kFar * (r.by_p ? r.T : fmaxf(r.T, 1.0f));
   return r;
 }
 
-constexpr float kFar = 60.0f;              // in units of T, below the largest: no weight
 struct Total {                             // the slices' statistics together
   float M;                                 // 0 where the largest is infinite (among_infinite)
   int at;
@@ -247,7 +251,7 @@ __device__ __forceinline__ Total total_of(const SampleArgs &a, const Params &r, 
   best = wave_largest(best);
   const float top = of_key((uint32_t)(best >> 32));
   // (slices of masks of the type's lowest value are no part of the mean)
-  const float least = top - kFar * (r.greedy ? 1.0f : r.T);
+  const float least = top - r.far;
   double sum = 0.0;
   uint32_t n = 0;
   for (int i = lane; i < a.slices; i += 64) {
@@ -559,9 +563,9 @@ __device__ __forceinline__ double exp_sum_in(const float (&v)[kVals], float top)
   }
   return e;
 }
-// Sum and number of the logits that can weigh anything beside `top`.
-__device__ __forceinline__ void mean_in(const float (&v)[kVals], float top, float T, float &sum, uint32_t &n) {
-  const float least = fmaxf(top - kFar * T, -3.402823466e38f);
+// Sum and number of the logits not `far` below `top`.
+__device__ __forceinline__ void mean_in(const float (&v)[kVals], float top, float far, float &sum, uint32_t &n) {
+  const float least = fmaxf(top - far, -3.402823466e38f);
   if (top == INFINITY) return;
 #pragma unroll
   for (int j = 0; j < kVals; ++j) {
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(64 * kStatTiles) sample_stats_kernel(const Sam
   top = of_key((uint32_t)(best >> 32));
   float sum = 0.0f;
   uint32_t n = 0;
-  if (r.by_k || r.by_p) mean_in(v, top, r.T, sum, n);
+  if (r.by_k || r.by_p) mean_in(v, top, r.far, sum, n);
   const double e = a.logprob ? exp_sum_in(v, top) : 0.0;
   const double ds = wave_sum((double)sum), de = wave_sum(e);
   n = wave_sum(n);
@@ -1158,7 +1162,7 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(const SampleArgs a
     float sum = 0.0f;
     uint32_t n = 0;
     held.each([&](int, const float (&v)[kVals]) {
-      if (cut) mean_in(v, top, r.T, sum, n);
+      if (cut) mean_in(v, top, r.far, sum, n);
       if (a.logprob) e += exp_sum_in(v, top);
     });
     const double de = wave_sum(e), ds = wave_sum((double)sum);

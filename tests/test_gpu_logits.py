@@ -315,6 +315,43 @@ def test_draw_over_masked_long_rows(m, v, limits):
     assert token[5] in (17, v - 2)
 
 
+@pytest.mark.parametrize("temperature", [0.05, 0.2])
+@pytest.mark.parametrize("top_k", [1, 50, 200, 1500])
+@pytest.mark.parametrize("m,v", LONG)
+def test_top_k_at_low_temperatures(m, v, top_k, temperature):
+    r = np.random.default_rng([67, v])
+    x = (r.standard_normal((m, v)) * 2.5).astype(np.float32)
+    x[:, ::500] += (r.random((m, -(-v // 500))) * 12).astype(np.float32)
+    check_draw(x, r.random(m), temperature=temperature, top_k=top_k)
+
+
+def test_top_k_takes_no_longer_at_a_low_temperature():
+    """The order that top_k cuts does not depend on the temperature, nor does the time by much (a row whose
+    cut lies behind all the steps is read again by one workgroup, three times as long in all)."""
+    v, n = 131072, 20
+    r = np.random.default_rng(71)
+    x = r.standard_normal((1, v)) * 2.5
+    x += (r.random((1, v)) < 0.001) * r.random((1, v)) * 12
+    x = g.dev(x.astype(np.float32))
+    u, k = torch.full((1,), 0.5, dtype=torch.float64, device=g.DEV), torch.full((1,), 50, dtype=torch.int32, device=g.DEV)
+    need = q8.q8_sample_workspace_bytes(1, v)
+    ws = torch.zeros(need, dtype=torch.uint8, device=g.DEV)
+    token = torch.zeros(1, dtype=torch.int32, device=g.DEV)
+    heat = [torch.full((1,), t, device=g.DEV) for t in (0.05, 1.0)]
+    times = [[], []]
+    for _ in range(10):
+        for i, t in enumerate(heat):
+            begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            sampling = q8.make_sampling(u, temperature=t, top_k=k)
+            begin.record()
+            for _ in range(n):
+                q8.q8_sample(x, v, 1, v, sampling, token, None, None, ws, need)
+            end.record()
+            torch.cuda.synchronize()
+            times[i].append(begin.elapsed_time(end))
+    assert min(times[0]) < 1.7 * min(times[1]), times
+
+
 @pytest.mark.parametrize("v", [20001, 40001])
 def test_a_row_is_drawn_alike_alone_and_in_a_batch(v):
     r = np.random.default_rng([53, v])
