@@ -446,6 +446,38 @@ def test_log_probabilities_near_zero(v, d):
     assert (np.abs(lp - want) <= (3 * d + 4) * 2.0 ** -24 * -want).all(), (lp, want)
 
 
+def logprob_bound(x, p):
+    """The most that a log-probability may be off.  A term exp(-d) below its slice's largest has an exponent
+    rounded thrice in fp32 (difference, product, constant), each d 2^-24 of it at most, and an exponential
+    within two steps of 2^-24; the largest terms are 1, and sums and logarithm are fp64 (a hundredth of a
+    step over all).  The result is rounded once."""
+    x = x.astype(np.float64)
+    d = x.max() - x
+    w = np.exp(-d)
+    return 2.0 ** -24 * (1.01 * float((w * np.where(d > 0, 3 * np.minimum(d, 800) + 2, 0)).sum() / w.sum()) + 1.01 * abs(p))
+
+
+@pytest.mark.parametrize("limits", [{}, dict(temperature=0.0), dict(temperature=1.3, top_k=300, top_p=0.9)])
+@pytest.mark.parametrize("kind", ["spread", "two", "steps", "narrow", "far", "outlier"])
+@pytest.mark.parametrize("m,v", [(4, 1000), *LONG])
+def test_log_probabilities(m, v, kind, limits):
+    """Rows of one launch and of slices, whose maxima differ ("far": all of them 15 and more below one
+    token); drawn tokens and the largest."""
+    r = np.random.default_rng([73, v])
+    n = r.standard_normal((4, v))
+    far = -20 + 0.5 * n - 5 * np.sin(np.arange(v) // 4096)
+    far[np.arange(4), r.integers(0, v, 4)] = 0.0
+    x = {"spread": n * np.array([[0.3], [1], [3], [10]]), "two": np.where(n > 1.0, 2.0, 1.0), "steps": np.round(n * 2),
+         "narrow": 7 + n * 1e-6, "far": far, "outlier": np.where(np.arange(v) == 77, 1e30, n)}[kind].astype(np.float32)
+    rows = x[np.arange(m) % 4]
+    token, lp = draw(rows, r.random(m), **limits)
+    for i in {0, 1, 2, 3, m - 1} & set(range(m)):
+        p = ol.logprob(rows[i], token[i])
+        assert abs(lp[i] - p) <= logprob_bound(rows[i], p), (i, lp[i], p)
+        if kind == "far":
+            assert token[i] == rows[i].argmax() and -1e-2 < lp[i] < 0
+
+
 def test_draw_without_logprob():
     r = np.random.default_rng(37)
     x = r.standard_normal((3, 500)).astype(np.float32)
