@@ -68,23 +68,33 @@ int check_pair(const q8_w4_weight *g, const q8_w4_weight *u) {
 
 // ---- what runs ------------------------------------------------------------------
 
-// The tile kernel's shape.  Sixteen waves, all of a workgroup's loads in flight sooner,
-// while every tile has a CU of its own (16 rows, K = 4096, N = 14336 9.2 us against 9.6 with
-// eight; N = 20000, K = 8192, a second step 26.6 against 24.6); with Q8_0 rows above four
-// and groups of 128 they lack registers (11.6 against 9.6).
+// The tile kernel's shape changes where the tiles are more than the CUs (us, K = 4096).
+//   * Sixteen waves, all of a workgroup's loads in flight sooner, while every tile has a CU
+//     of its own; then eight, two workgroups a CU (1 row, 224 tiles 7.0 against 7.7 with
+//     eight, 256 6.6 against 8.1, 261 11.1 against 10.5, 383 11.9 against 11.2, 500 13.2
+//     against 12.1; 16 rows, 224 tiles 9.2 against 9.6).  With Q8_0 rows above four and
+//     groups of 128 they lack registers (11.6 against 9.6).
+//   * Above 16 rows one tile a wave, then two that share its activation (32 rows, 256 tiles
+//     12.2 against 17.9 with two, 258 21.7 against 18.5, 438 22.3 against 19.2; Q8_0, 258
+//     29.2 against 24.7, 501 with K = 5120 35.6 against 29.7).  17 to 24 rows of Q8_0 scale
+//     less and keep one tile (24 rows, 258 tiles 19.7 against 21.9, 500 21.8 against 22.7),
+//     but for weights with zero points in groups of 64 and 128, whose results take more
+//     steps (282 tiles 27.2 against 24.2, 500 28.3 against 25.0).
 W4Plan tile_plan(const W4Args &a, bool pair, int act_fmt) {
-  const bool q8 = act_fmt == Q8_ACT_Q8_0;
-  const int tiles = pair || a.T >= 384 ? 2 : 1;
-  if (a.m <= 4) return {4, pair || a.T < 384 ? 16 : 8, pair ? 2 : 1};
+  const bool q8 = act_fmt == Q8_ACT_Q8_0, more = a.T > 256;
+  if (a.m <= 4) return {4, pair || !more ? 16 : 8, pair ? 2 : 1};
   if (a.m <= 8 && q8) return {8, 8, pair ? 2 : 1};
-  if (a.m <= 16) return {16, pair || a.T > 256 || (q8 && a.group == 128) ? 8 : 16, pair ? 2 : 1};
-  if (a.m <= 24 && q8) return {24, 8, tiles};
-  if (a.m <= 32 || pair) return {32, 8, tiles};
+  if (a.m <= 16) return {16, pair || more || (q8 && a.group == 128) ? 8 : 16, pair ? 2 : 1};
+  if (a.m <= 24 && q8) return {24, 8, pair || (more && a.w.zeros && a.group > 32) ? 2 : 1};
+  if (a.m <= 32 || pair) return {32, 8, pair || more ? 2 : 1};
   return {64, 8, 1};
 }
 
-// K splits across workgroups: only where the column tiles leave CUs idle, as in
-// the 8-bit tile plans.
+// K splits across workgroups: only where the column tiles leave half of the CUs idle, as in
+// the 8-bit tile plans.  The join of more costs more than it spares (us, one split against
+// two: 1 row, K = 4096, 172 tiles 6.8 against 9.5, 16 rows 8.5 against 12.1; 1 row, K =
+// 14336, 141 tiles 16.0 against 20.1; pairs of 172 tiles, 1 row 11.9 against 16.0, 24 rows of
+// Q8_0 25.5 against 36.0).
 int tile_splits(int64_t K, int64_t N) {
   const int64_t T = round_up(N, Q8_TILE_COLS) / Q8_TILE_COLS;
   const int64_t quads = (K / Q8_BLOCK + 3) / 4;

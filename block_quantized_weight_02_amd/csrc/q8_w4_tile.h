@@ -522,29 +522,43 @@ __global__ void __launch_bounds__(64 * W, w4_waves_per_simd(ACT, RG, EL, NT, GB)
   }
 }
 
+// Instances that the host side's plans reach.  Not sixteen waves with Q8_0 rows above four
+// and groups of 128 (they leave it 128 registers, fewer than it has in use), nor two tiles of
+// one weight for 24 Q8_0 rows without zero points or with groups of 32.
+template <int ACT, int W, int RG, int EL, int LE, int NT, int GB, bool ZEROS, bool PAIR>
+constexpr bool w4_reached() {
+  if (ACT != kActQ8 || EL < 4) return true;
+  if (W == 16) return GB != 4;
+  return !(RG == 2 && LE == 2 && NT == 2 && !PAIR) || (ZEROS && GB > 1);
+}
+
 template <int ACT, int W, int RG, int EL, int LE, int NT, int GB, bool ZEROS, bool PAIR>
 hipError_t launch_w4_k(const W4Args &a, hipStream_t stream) {
-  constexpr int MR = w4_rows(RG, EL), lds = w4_lds(ACT, W, RG, EL, NT);
-  const auto kern = w4_tile_kernel<ACT, W, RG, EL, LE, NT, GB, ZEROS, PAIR>;
-  if constexpr (lds > 64 * 1024) {
-    // once a device: dynamic LDS above the default 64 KiB
-    static std::atomic<uint64_t> granted{0};
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev > 63 || !(granted.load(std::memory_order_relaxed) & bit)) {
-      e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if constexpr (!w4_reached<ACT, W, RG, EL, LE, NT, GB, ZEROS, PAIR>()) {
+    return hipErrorInvalidValue;
+  } else {
+    constexpr int MR = w4_rows(RG, EL), lds = w4_lds(ACT, W, RG, EL, NT);
+    const auto kern = w4_tile_kernel<ACT, W, RG, EL, LE, NT, GB, ZEROS, PAIR>;
+    if constexpr (lds > 64 * 1024) {
+      // once a device: dynamic LDS above the default 64 KiB
+      static std::atomic<uint64_t> granted{0};
+      int dev = 0;
+      hipError_t e = hipGetDevice(&dev);
       if (e != hipSuccess) return e;
-      granted.fetch_or(bit, std::memory_order_relaxed);
+      const uint64_t bit = 1ull << (dev & 63);
+      if (dev > 63 || !(granted.load(std::memory_order_relaxed) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        granted.fetch_or(bit, std::memory_order_relaxed);
+      }
     }
+    const unsigned chunks = (unsigned)((a.m + MR - 1) / MR);
+    (void)hipGetLastError();
+    const unsigned units = PAIR ? (unsigned)a.T : (unsigned)((a.T + NT - 1) / NT);
+    kern<<<dim3(units, (unsigned)a.split_k, chunks), dim3(64 * W), lds, stream>>>(a);
+    return hipGetLastError();
   }
-  const unsigned chunks = (unsigned)((a.m + MR - 1) / MR);
-  (void)hipGetLastError();
-  const unsigned units = PAIR ? (unsigned)a.T : (unsigned)((a.T + NT - 1) / NT);
-  kern<<<dim3(units, (unsigned)a.split_k, chunks), dim3(64 * W), lds, stream>>>(a);
-  return hipGetLastError();
 }
 
 template <int ACT, int W, int RG, int EL, int LE, int NT, bool PAIR>
@@ -555,11 +569,8 @@ hipError_t launch_w4_g(const W4Args &a, hipStream_t stream) {
                       : launch_w4_k<ACT, W, RG, EL, LE, NT, 1, false, PAIR>(a, stream);
     case 64: return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 2, true, PAIR>(a, stream)
                       : launch_w4_k<ACT, W, RG, EL, LE, NT, 2, false, PAIR>(a, stream);
-    case 128:
-      // (16 waves leave it 128 registers, fewer than it has in use)
-      if constexpr (ACT == kActQ8 && W == 16 && EL == 4) return hipErrorInvalidValue;
-      else return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 4, true, PAIR>(a, stream)
-                    : launch_w4_k<ACT, W, RG, EL, LE, NT, 4, false, PAIR>(a, stream);
+    case 128: return z ? launch_w4_k<ACT, W, RG, EL, LE, NT, 4, true, PAIR>(a, stream)
+                       : launch_w4_k<ACT, W, RG, EL, LE, NT, 4, false, PAIR>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -88,6 +88,17 @@ def test_exact_part_filled_row_groups(m, group, zeros, fmt, act):
 
 
 @pytest.mark.parametrize("act", [BF16, Q8])
+@pytest.mark.parametrize("group,zeros,fmt", FORMS)
+def test_exact_with_as_many_tiles_as_cus_and_more(group, zeros, fmt, act):
+    """256 tiles of columns and 258, where the launch takes another shape."""
+    for K, N in ((160, 16384), (576, 16449)):
+        w = Weight(K, N, group, zeros, fmt, 5, exact=True).pack()
+        for m in (1, 4, 7, 13, 17, 24, 32):
+            a = Act(m, K, act, 7, exact=True)
+            np.testing.assert_array_equal(u.real(u.gemv(a, w), N), a.times(w)[0], err_msg=f"{m}x{K}x{N}")
+
+
+@pytest.mark.parametrize("act", [BF16, Q8])
 @pytest.mark.parametrize("m,K,N,group,zeros,fmt", [
     (1, 4096, 1024, 128, False, 0), (1, 4096, 40, 32, True, 0), (2, 1024, 9000, 64, False, 1),
     (8, 14336, 512, 64, True, 1), (16, 4096, 320, 128, True, 0), (27, 2080, 1000, 32, False, 0),
