@@ -18,7 +18,7 @@
 //     2e-7..1e-6 at K = 1024..16384, that of the plain fp32 product).
 //   * Q8_0 activations: u is an int8 operand as it is, the accumulator starts at
 //     -z sum x, all exact; the activation's bytes take the nibbles' order.
-//   * a group's blocks chain in one accumulator and are scaled once.
+//   * a stage's blocks of a group chain in one accumulator and are scaled once.
 //   * activation row 4 e + q sits in operand row 4 q + e, so that with up to 4 rows
 //     only the first of a lane's four results counts, and is scaled; with Q8_0
 //     activations, whose results are each converted and scaled twice a block, of 8 or 24
@@ -32,9 +32,10 @@
 // Measured, calls back to back: m = 1, K = 4096, N = 14336 8.1 us, N = 32000 13.5 (68 MB,
 // 5.0 TB/s); m = 16, N = 14336, zero points 9.1 (31 MB; a plain read 4.9): the launch, the
 // first loads' latency and the join stand beside the stream.  Q8_0, groups of 32, m = 32, K
-// = 5120, N = 32001 31 (92 MB; a plain read 14): the vector unit, busy 60 % (three
-// instructions a result and block, conversion and two scales; with zero points four), the
-// matrix unit 15 %, beside the activation's loads through L2.
+// = 5120, N = 32001 31..34 (92 MB; a plain read 14): the vector unit is busy half of the
+// cycles (three instructions a result and block, conversion and two scales; with zero
+// points four), the matrix unit an eighth, and the two waves that the registers leave a
+// SIMD wait for each other's chains of them.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -511,7 +511,7 @@ int q8_w4_unpack(const q8_w4_weight *W /* host pointer */, uint8_t *u_kn, uint16
  * q8_w4_gemv: y = x . W for 1 <= m <= 32 rows, with q8_gemv_fused's epilogue (NULL:
  * y only), layouts and activation formats bf16 and Q8_0 (two words: Q8_ERR_ACT_FMT).
  * The sums are fp32: bf16 activations are multiplied exactly and added in fp32, a
- * group's sum is scaled once; Q8_0 activations' dots are exact int32 per 32 rows.
+ * group's sum is scaled in one or two parts; Q8_0 activations' dots are exact per 32 rows.
  * An infinity or NaN in a row of a bf16 activation makes that row's outputs NaN or
  * infinite, no other row's; so may a value above 2^112 in size, since a group's sum may
  * be taken of (16 + u) x and (16 + z) x.
@@ -870,9 +870,10 @@ int q8_logits_rules(const float *logits, int64_t ld, int64_t m, int64_t V,
  *   top_p  the tokens whose predecessors weigh less than top_p[r] of the whole row's
  *          weight (>= 1: all; the first always);
  *   min_p  the tokens of w >= min_p[r] (<= 0: all; above 1 counts as 1).
- * Each limit is taken over the whole row, and the shortest prefix is kept.  The token is
- * the lowest t whose kept tokens 0 .. t weigh more than u[r] times the kept weight,
- * u[r] in [0, 1) (numbers outside count as the nearer end, NaN as 0).  Weights are
+ * Each limit is taken over the whole row (top_p not of what top_k leaves), and the
+ * shortest prefix is kept.  The token is the lowest t whose kept tokens 0 .. t weigh more
+ * than u[r] times the kept weight, u[r] in [0, 1) (numbers outside count as the nearer
+ * end, NaN as 0).  Weights are
  * whole multiples of 2^-min(51, 62 - ceil(log2(V + 1))) of the largest, computed to
  * 1e-13 and summed exactly, so a token does not depend on the order of additions; ones
  * that round to 0 are not drawn.  T <= 0 (or NaN): the largest logit, the lowest index
